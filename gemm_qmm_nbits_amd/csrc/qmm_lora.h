@@ -1,0 +1,87 @@
+// Low-rank adapters (qmm_lora_add, qmm_lora_grad): kernel interfaces.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "qmm.h"
+
+namespace qmm {
+
+// Rows per tile: the rows of one adapter are dealt in tiles of this many.
+constexpr int kLoraTile = 64;
+// Up to this many rows the kernels group the rows themselves: slot m is the tile of row
+// m's adapter when m is its first row, and empty otherwise.
+constexpr int kLoraInlineRows = 64;
+constexpr int kLoraRankChunk = 64;  // ranks per work-group of the kernels that produce ranks
+
+inline int lora_rank_pad(int r) { return (r + 15) / 16 * 16; }
+
+// Rows sorted by adapter (rows without one last, as group L), and the tiles of that order.
+// Group a owns positions off[a] .. off[a+1]-1 and the tile slots off[a] / 64 + a + j for
+// j < ceil(rows / 64); the slots between are empty (count 0).
+struct LoraPlan {
+  int32_t* off;    // [L + 2]
+  int32_t* perm;   // [M] row at each position
+  int32_t* tiles;  // [M / 64 + L + 2][4] group, first position, rows, 0
+};
+
+struct LoraArgs {
+  int64_t M, K, N;
+  int r, rp;  // rank, and rounded up to a multiple of 16
+  int64_t L;
+  int type;  // QMM_F16 or QMM_BF16: X, dY, A, B
+  const int32_t* ids;
+  const void* X;
+  const void* dY;
+  const void* A;       // [L][r][K]
+  const void* B;       // [L][N][r]
+  const float* scale;  // [L] or NULL
+  LoraPlan plan;
+  int use_plan;        // 0: the kernels group the rows (M <= kLoraInlineRows)
+  int slots;           // tile slots (grid)
+  float* part;         // fp32 partial products [splits][M][rp], by position
+  int splits;
+  int64_t split_len;   // contraction elements per split (a multiple of 256)
+  const void* base;
+  int base_type;
+  void* out;
+  int out_type;
+  float* T;            // [M][r] by row, or NULL
+  int vec;             // X, A, dY, B rows allow 16-byte loads
+  int vec_out;         // base and out rows allow 4-element accesses
+};
+
+hipError_t launch_lora_plan(const LoraArgs& p, hipStream_t st);
+// part = X A_a^T (contraction over K), or dY B_a (contraction over N)
+hipError_t launch_lora_shrink_x(const LoraArgs& p, hipStream_t st);
+hipError_t launch_lora_shrink_dy(const LoraArgs& p, hipStream_t st);
+// T[row] = sum over the splits of part (x scale_a when `scaled`)
+hipError_t launch_lora_finalize(const LoraArgs& p, bool scaled, float* T, hipStream_t st);
+// out = base + scale_a * (sum of part) B_a^T; writes T when it is given
+hipError_t launch_lora_expand(const LoraArgs& p, hipStream_t st);
+// out = base + dT A_a (dT [M][r] by row)
+hipError_t launch_lora_expand_dx(const LoraArgs& p, const float* dT, hipStream_t st);
+
+// out[a] = sum over the rows m of adapter a of Z[m][c] * t[m][rank]: [P][r] (rank_major 0)
+// or [r][P] (rank_major 1), times scale[a] when given.
+struct LoraOuterArgs {
+  const void* Z;  // [M][P] of `type`
+  int type;
+  int64_t P;
+  const float* t;  // [M][r] by row
+  int r;
+  int64_t M, L;
+  LoraPlan plan;
+  const float* scale;
+  void* out;
+  int out_type;
+  int rank_major;
+  float* part;  // fp32 [2 M / chunk + 1][P][r] in out's element order
+  int chunk;    // rows per chunk (a multiple of 16)
+  int vec;
+};
+int lora_outer_chunk(int64_t M, int64_t P);
+hipError_t launch_lora_outer(const LoraOuterArgs& p, hipStream_t st);
+
+}  // namespace qmm

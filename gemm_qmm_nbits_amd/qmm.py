@@ -43,6 +43,10 @@ class qmm_nested_absmax(Structure):
                 ("group", c_int)]
 
 
+class qmm_lora_weights(Structure):
+    _fields_ = [("A", c_void_p), ("B", c_void_p), ("scale", c_void_p)]
+
+
 _lib = None
 
 _SIGS = {
@@ -94,6 +98,20 @@ _SIGS = {
                          c_void_p, c_void_p]),
     "qmm_qswiglu": (c_int, [c_void_p, c_void_p, c_int, c_int64, c_int, POINTER(qmm_qparams), c_void_p,
                             c_void_p]),
+    "qmm_lora_add": (c_int, [c_void_p, c_int, c_int64, c_int64, c_int64, c_int, c_int64, c_void_p,
+                             qmm_lora_weights, c_void_p, c_int, c_void_p, c_int, c_void_p, c_void_p, c_size_t,
+                             c_void_p]),
+    "qmm_lora_add_workspace_bytes": (c_size_t, [c_int64, c_int64, c_int64, c_int, c_int64]),
+    "qmm_lora_grad": (c_int, [c_void_p, c_void_p, c_int, c_int64, c_int64, c_int64, c_int, c_int64, c_void_p,
+                              qmm_lora_weights, c_void_p, c_void_p, c_int, c_void_p, c_int, c_void_p, c_void_p,
+                              c_int, c_void_p, c_size_t, c_void_p]),
+    "qmm_lora_grad_workspace_bytes": (c_size_t, [c_int64, c_int64, c_int64, c_int, c_int64]),
+    "qmm_validate_lora_add": (c_int, [c_void_p, c_int, c_int64, c_int64, c_int64, c_int, c_int64, c_void_p,
+                                      qmm_lora_weights, c_void_p, c_int, c_void_p, c_int, c_void_p, c_void_p,
+                                      c_size_t]),
+    "qmm_validate_lora_grad": (c_int, [c_void_p, c_void_p, c_int, c_int64, c_int64, c_int64, c_int, c_int64,
+                                       c_void_p, qmm_lora_weights, c_void_p, c_void_p, c_int, c_void_p, c_int,
+                                       c_void_p, c_void_p, c_int, c_void_p, c_size_t]),
     "qmm_hbm_read_probe": (c_int, [c_void_p, c_int64, c_void_p, c_int, c_void_p]),
     "qmm_launch_timing_begin": (c_int, [c_int]),
     "qmm_launch_timing_end": (c_int, [c_void_p, c_int, c_void_p]),
@@ -445,6 +463,113 @@ def qswiglu(gate, up, qparams, bits, out=None, stream=None):
     _check("qmm_qswiglu", lib().qmm_qswiglu(_ptr(gate), _ptr(up), dtype_code(gate), gate.numel(), bits, arr,
                                             _ptr(out), _stream(stream)))
     return out
+
+
+# ---------------------------------------------------------------------------
+# low-rank adapters
+# ---------------------------------------------------------------------------
+
+def _expect(t, name, shape, dtypes, like=None):
+    """A dense device tensor of the given shape and one of the dtypes, on like's device."""
+    if t is None:
+        return None
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be one of {dtypes}, got {t.dtype}")
+    if not t.is_cuda or (like is not None and t.device != like.device):
+        raise ValueError(f"{name} must be on the device of the call")
+    return _contig(t, name)
+
+
+def _on_current_device(t):
+    """Kernels are launched on the current device: the tensors have to be there."""
+    torch = _torch()
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError("the tensors must be on the current device (torch.cuda.set_device)")
+
+
+def _workspace(workspace, need, like):
+    torch = _torch()
+    if workspace is None:
+        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=like.device)
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def _lora_shapes(X, A, B, ids, scale):
+    torch = _torch()
+    if X.dim() != 2 or A.dim() != 3:
+        raise ValueError("rows must be [M, K] and A [L, r, K]")
+    if X.dtype not in (torch.float16, torch.bfloat16):
+        raise TypeError(f"unsupported dtype {X.dtype}")
+    M, (L, r, K) = X.shape[0], A.shape
+    N = B.shape[1] if B.dim() == 3 else -1
+    _on_current_device(X)
+    _expect(A, "A", (L, r, K), (X.dtype,), X)
+    _expect(B, "B", (L, N, r), (X.dtype,), X)
+    _expect(ids, "ids", (M,), (torch.int32,), X)
+    _expect(scale, "scale", (L,), (torch.float32,), X)
+    return M, K, N, r, L
+
+
+def qmm_lora_add(X, A, B, ids, scale=None, base=None, out=None, out_dtype=None, T=None, workspace=None,
+                 stream=None):
+    """Y[m] = base[m] + scale[a] * B[a] (A[a] X[m]), a = ids[m] (outside [0, L): Y[m] = base[m]).
+
+    X [M, K], A [L, r, K], B [L, N, r] fp16 or bf16; ids int32 [M]; scale fp32 [L]; base [M, N],
+    for instance the fp32 output of qmm_nbits.  T (fp32 [M, r]) receives A[a] X[m] for qmm_lora_grad."""
+    torch = _torch()
+    M, K, N, r, L = _lora_shapes(X, A, B, ids, scale)
+    any_type = (torch.float32, torch.float16, torch.bfloat16)
+    _expect(X, "X", (M, K), (A.dtype,))
+    _expect(base, "base", (M, N), any_type, X)
+    _expect(T, "T", (M, r), (torch.float32,), X)
+    if out is None:
+        out = torch.empty((M, N), dtype=out_dtype or X.dtype, device=X.device)
+    _expect(out, "out", (M, N), any_type, X)
+    workspace, wsb = _workspace(workspace, lib().qmm_lora_add_workspace_bytes(M, K, N, r, L), X)
+    w = qmm_lora_weights(A.data_ptr(), B.data_ptr(), None if scale is None else scale.data_ptr())
+    st = lib().qmm_lora_add(_ptr(X), dtype_code(X), M, K, N, r, L, _ptr(ids), w, _ptr(base),
+                            QMM_F32 if base is None else dtype_code(base), _ptr(out), dtype_code(out), _ptr(T),
+                            _ptr(workspace), wsb, _stream(stream))
+    _check("qmm_lora_add", st)
+    return out
+
+
+def qmm_lora_grad(dY, X, A, B, ids, scale=None, T=None, base=None, dX=None, dA=None, dB=None, dx_dtype=None,
+                  grad_dtype=None, need=(True, True, True), workspace=None, stream=None):
+    """Gradients (dX, dA, dB) of qmm_lora_add; need: which of the three to compute (others None).
+
+    dX[m] = base[m] + A[a]^T dT[m] with dT[m] = scale[a] B[a]^T dY[m]; dA[a] = sum dT[m] X[m]^T;
+    dB[a] = scale[a] sum dY[m] T[m]^T.  T: kept from qmm_lora_add, or None (computed again).
+    dX is of dx_dtype (default X's), dA and dB of grad_dtype (default fp32)."""
+    torch = _torch()
+    M, K, N, r, L = _lora_shapes(X, A, B, ids, scale)
+    any_type = (torch.float32, torch.float16, torch.bfloat16)
+    _expect(X, "X", (M, K), (A.dtype,))
+    _expect(dY, "dY", (M, N), (X.dtype,), X)
+    _expect(T, "T", (M, r), (torch.float32,), X)
+    _expect(base, "base", (M, K), any_type, X)
+
+    def output(t, wanted, name, shape, dtype):
+        if t is None and wanted:
+            t = torch.empty(shape, dtype=dtype, device=X.device)
+        return _expect(t, name, shape, any_type, X)
+
+    dX = output(dX, need[0], "dX", (M, K), dx_dtype or X.dtype)
+    dA = output(dA, need[1], "dA", (L, r, K), grad_dtype or torch.float32)
+    dB = output(dB, need[2], "dB", (L, N, r), grad_dtype or torch.float32)
+    if dA is not None and dB is not None and dA.dtype != dB.dtype:
+        raise TypeError("dA and dB differ in dtype")
+    g = dA if dA is not None else dB
+    workspace, wsb = _workspace(workspace, lib().qmm_lora_grad_workspace_bytes(M, K, N, r, L), X)
+    w = qmm_lora_weights(A.data_ptr(), B.data_ptr(), None if scale is None else scale.data_ptr())
+    st = lib().qmm_lora_grad(_ptr(dY), _ptr(X), dtype_code(X), M, K, N, r, L, _ptr(ids), w, _ptr(T), _ptr(base),
+                             QMM_F32 if base is None else dtype_code(base), _ptr(dX),
+                             QMM_F32 if dX is None else dtype_code(dX), _ptr(dA), _ptr(dB),
+                             QMM_F32 if g is None else dtype_code(g), _ptr(workspace), wsb, _stream(stream))
+    _check("qmm_lora_grad", st)
+    return dX, dA, dB
 
 
 def hbm_read_probe(buf, sink, groups, stream=None):

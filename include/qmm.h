@@ -380,6 +380,63 @@ qmm_status qmm_qswiglu(const void* gate, const void* up, int x_type, int64_t n, 
                        const qmm_qparams* q, void* y, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * Low-rank adapters of many requests beside a shared projection, and their gradients.
+ *
+ * Row m of a batch belongs to a request with adapter a = ids[m] (an id outside [0, L):
+ * none).  Next to any projection of this library, whose output is `base`:
+ *   T[m] = A_a x_m                       fp32, products exact, fp32 sums
+ *   Y[m] = base[m] + s_a * (B_a T[m])    rounded once to Y's type; Y[m] = base[m] for rows
+ *                                        without an adapter
+ * and the gradients, for dY:
+ *   dT[m] = s_a * (B_a^T dy_m)           fp32
+ *   dX[m] = base[m] + A_a^T dT[m]        base: the projection's own input gradient
+ *   dA_a  = sum over its rows m of dT[m] x_m^T;  dB_a = s_a * sum over m of dy_m T[m]^T
+ * (zeros for an adapter without rows).  T and dT are not rounded below fp32.
+ *
+ *   X [M][K], dY [M][N], A [L][r][K], B [L][N][r], all of `type` (QMM_F16 or QMM_BF16).
+ *   ids   int32 [M] (device), in any order.   scale fp32 [L] (device) or NULL (1).
+ *   base  [M][N] (qmm_lora_add) or [M][K] (qmm_lora_grad) of base_type, or NULL (0); may be
+ *         the output itself when the types agree.
+ *   T     fp32 [M][r].  qmm_lora_add writes it when given (rows without an adapter: zeros);
+ *         qmm_lora_grad reads it, or computes it again from X when NULL.
+ *   dX / dA / dB of qmm_lora_grad: each may be NULL (not computed).  dA [L][r][K] and dB
+ *         [L][N][r] of g_type.
+ *   M <= 2^24, 1 <= K, N <= 2^22, 1 <= r <= 512, 1 <= L <= 32768.  Any sizes and element
+ *   alignment are served; rows of 16-byte multiples (K, N, r multiples of 8, 16-byte
+ *   aligned tensors) take the vector loads.
+ *   workspace: at least the bytes of the query, 256-byte aligned.  Calls that share a
+ *   workspace must not overlap.  The sums' order depends only on the shape and the ids.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  const void* A;       /* [L][r][K] */
+  const void* B;       /* [L][N][r] */
+  const float* scale;  /* [L] or NULL */
+} qmm_lora_weights;
+
+qmm_status qmm_lora_add(const void* X, int type, int64_t M, int64_t K, int64_t N, int r, int64_t L,
+                        const int32_t* ids, qmm_lora_weights w, const void* base, int base_type,
+                        void* Y, int y_type, float* T, void* workspace, size_t workspace_bytes,
+                        void* stream);
+size_t qmm_lora_add_workspace_bytes(int64_t M, int64_t K, int64_t N, int r, int64_t L);
+
+qmm_status qmm_lora_grad(const void* dY, const void* X, int type, int64_t M, int64_t K, int64_t N,
+                         int r, int64_t L, const int32_t* ids, qmm_lora_weights w, const float* T,
+                         const void* base, int base_type, void* dX, int dx_type, void* dA, void* dB,
+                         int g_type, void* workspace, size_t workspace_bytes, void* stream);
+size_t qmm_lora_grad_workspace_bytes(int64_t M, int64_t K, int64_t N, int r, int64_t L);
+
+/* Host-only checks of the arguments, as qmm_validate_nbits. */
+qmm_status qmm_validate_lora_add(const void* X, int type, int64_t M, int64_t K, int64_t N, int r,
+                                 int64_t L, const int32_t* ids, qmm_lora_weights w, const void* base,
+                                 int base_type, const void* Y, int y_type, const float* T,
+                                 const void* workspace, size_t workspace_bytes);
+qmm_status qmm_validate_lora_grad(const void* dY, const void* X, int type, int64_t M, int64_t K,
+                                  int64_t N, int r, int64_t L, const int32_t* ids,
+                                  qmm_lora_weights w, const float* T, const void* base, int base_type,
+                                  const void* dX, int dx_type, const void* dA, const void* dB,
+                                  int g_type, const void* workspace, size_t workspace_bytes);
+
+/* ---------------------------------------------------------------------------
  * Tuning control and introspection.
  * qmm_tuning_mode: 0 = time candidates on the first call of a shape (default),
  *   1 = never time, always use the default tiling, 2 = force candidate

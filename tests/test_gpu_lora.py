@@ -1,0 +1,321 @@
+"""GPU parity of the low-rank adapters (qmm_lora_add, qmm_lora_grad) against the fp64 oracle."""
+import numpy as np
+import pytest
+
+from gemm_qmm_nbits_amd import inputs as gen
+from gemm_qmm_nbits_amd import qmm as Q
+from oracle import adapters_oracle as AO
+from oracle import qmm_oracle as O
+
+from gpu_util import assert_elementwise, dev, gamma, host_bits, host_f64, say, torch
+
+pytestmark = pytest.mark.gpu
+
+DT = {"f32": "float32", "f16": "float16", "bf16": "bfloat16"}
+
+
+def tt(name):
+    return getattr(torch(), DT[name])
+
+
+class Problem:
+    """One batch over L adapters, on the device and as fp64 on the host."""
+
+    def __init__(self, M, K, N, r, L, ty, seed, ids="mixed", scaled=True, base=None, base_width=None, offset=0):
+        t = torch()
+        rng = np.random.default_rng(seed)
+        self.dims = (M, K, N, r, L)
+        self.ty = ty
+
+        def put(x, dtype):
+            """On the device; `offset` elements past an aligned address."""
+            flat = t.zeros(x.size + offset, dtype=dtype, device="cuda")
+            v = flat[offset:].view(x.shape)
+            v.copy_(t.from_numpy(np.ascontiguousarray(x)))
+            return v
+
+        self.X = put(rng.standard_normal((M, K)), tt(ty))
+        self.dY = put(rng.standard_normal((M, N)) * 0.1, tt(ty))
+        self.A = put(rng.standard_normal((L, r, K)) / np.sqrt(K), tt(ty))
+        self.B = put(rng.standard_normal((L, N, r)) * 0.3, tt(ty))
+        if isinstance(ids, str):
+            if ids == "mixed":
+                v = rng.integers(-1, L + 1, M)           # -1 and L: no adapter
+            elif ids == "none":
+                v = np.full(M, -1)
+            elif ids == "one":
+                v = np.full(M, L - 1)
+            else:                                        # runs of a request's rows
+                v = np.sort(rng.integers(0, L, M))[::-1]
+        else:
+            v = np.asarray(ids)
+        self.ids_h = v.astype(np.int32)
+        self.ids = dev(self.ids_h)
+        self.scale = dev(rng.uniform(0.25, 2.0, L).astype(np.float32)) if scaled else None
+        self.base = None
+        if base is not None:
+            self.base = put(rng.standard_normal((M, base_width or N)), tt(base))
+
+    def host(self, name):
+        v = getattr(self, name)
+        return None if v is None else host_f64(v)
+
+    def oracle_args(self):
+        return self.host("X"), self.host("A"), self.host("B"), self.ids_h, self.host("scale")
+
+
+def abs_add(p):
+    """sum of the absolute values of the terms of each output element of lora_add."""
+    X, A, B, ids, s = p.oracle_args()
+    base = p.host("base")
+    return AO.lora_add(np.abs(X), np.abs(A), np.abs(B), ids, s, None if base is None else np.abs(base))
+
+
+def abs_grad(p, T):
+    X, A, B, ids, s = p.oracle_args()
+    base = p.host("base")
+    return AO.lora_grad(np.abs(p.host("dY")), np.abs(X), np.abs(A), np.abs(B), ids, s, np.abs(T),
+                        None if base is None else np.abs(base))
+
+
+def check_add(p, out, with_t=False, label=""):
+    t = torch()
+    M, K, N, r, L = p.dims
+    T = t.full((M, r), float("nan"), device="cuda") if with_t else None
+    say(f"  lora_add {label} M={M} K={K} N={N} r={r} L={L} {p.ty} out={out}")
+    y = Q.qmm_lora_add(p.X, p.A, p.B, p.ids, scale=p.scale, base=p.base, out_dtype=tt(out), T=T)
+    args = p.oracle_args()
+    ref = AO.lora_add(*args, base=p.host("base"))
+    # T: K products summed in fp32 in some order; then r products, the scale and base
+    assert_elementwise(host_f64(y), ref, gamma(K + r + 40) * abs_add(p), out, label)
+    if with_t:
+        want = AO.lora_t(args[0], args[1], p.ids_h)
+        lim = AO.lora_t(np.abs(args[0]), np.abs(args[1]), p.ids_h)
+        assert_elementwise(host_f64(T), want, gamma(K + 40) * lim, "f32", label + " T")
+    return y
+
+
+SIZES = [
+    # M, K, N, r, L: one row; a few; the border of the ballot form; odd and tiny sizes; several
+    # tiles; ranks below, at and past the fragments; one column; one adapter
+    (1, 256, 64, 16, 1), (1, 5120, 640, 16, 8), (2, 257, 33, 1, 3), (3, 1, 1, 1, 1), (5, 8, 4, 4, 2),
+    (17, 320, 100, 8, 4), (63, 96, 130, 24, 70), (64, 512, 256, 32, 5), (65, 512, 256, 64, 5), (66, 77, 51, 5, 2),
+    (130, 1000, 300, 100, 6), (333, 264, 72, 48, 3), (500, 640, 200, 130, 2), (1100, 128, 64, 16, 40),
+]
+
+
+@pytest.mark.parametrize("M,K,N,r,L", SIZES)
+@pytest.mark.parametrize("ty", ["f16", "bf16"])
+def test_add_sizes(M, K, N, r, L, ty):
+    p = Problem(M, K, N, r, L, ty, seed=M + K + r, base="f32")
+    check_add(p, ty, with_t=True)
+    check_add(p, "f32")
+
+
+@pytest.mark.parametrize("ids", ["none", "one", "runs"])
+@pytest.mark.parametrize("M", [9, 200])
+def test_add_orders(ids, M):
+    check_add(Problem(M, 200, 96, 16, 4, "bf16", seed=7, ids=ids, base="bf16"), "bf16", with_t=True, label=ids)
+
+
+@pytest.mark.parametrize("base", [None, "f32", "f16", "bf16"])
+@pytest.mark.parametrize("out", ["f32", "f16", "bf16"])
+def test_add_types(base, out):
+    for ty in ("f16", "bf16"):
+        check_add(Problem(70, 128, 48, 8, 3, ty, seed=11, base=base, scaled=False), out)
+
+
+@pytest.mark.parametrize("M", [4, 100])
+def test_add_misaligned(M):
+    """Every tensor starts one element past an aligned address (the element loads)."""
+    p = Problem(M, 128, 64, 16, 3, "f16", seed=13, base="f16", offset=1)
+    assert p.X.data_ptr() % 16 != 0
+    check_add(p, "f16", with_t=True)
+
+
+@pytest.mark.parametrize("M", [20, 300])
+def test_add_in_place_and_nothing_else_written(M):
+    """The output may be the base; elements around it stay."""
+    t = torch()
+    p = Problem(M, 128, 72, 8, 3, "bf16", seed=17, base="bf16")
+    fresh = Q.qmm_lora_add(p.X, p.A, p.B, p.ids, scale=p.scale, base=p.base)
+    room = t.full((M * 72 + 64,), 3.0, dtype=t.bfloat16, device="cuda")
+    own = room[32:32 + M * 72].view(M, 72)
+    own.copy_(p.base)
+    Q.qmm_lora_add(p.X, p.A, p.B, p.ids, scale=p.scale, base=own, out=own)
+    assert np.array_equal(host_bits(own), host_bits(fresh))
+    assert bool((room[:32] == 3.0).all()) and bool((room[32 + M * 72:] == 3.0).all())
+
+
+@pytest.mark.parametrize("M", [30, 150])
+def test_bad_values_stay_in_their_rows(M):
+    """Inf and NaN in a row (or in a row without an adapter) reach no other row, and no adapter's
+    gradient but their own."""
+    t = torch()
+    ids = np.arange(M) % 3
+    ids[4] = -1
+    p = Problem(M, 136, 40, 12, 3, "f16", seed=19, ids=ids, base="f32")
+    clean = Q.qmm_lora_add(p.X, p.A, p.B, p.ids, scale=p.scale, base=p.base)
+    _, dA, dB = Q.qmm_lora_grad(p.dY, p.X, p.A, p.B, p.ids, scale=p.scale)
+    p.X[4] = float("nan")
+    p.dY[4] = float("inf")
+    p.X[0] = float("inf")          # row 0: adapter 0
+    p.dY[0] = float("nan")
+    y = Q.qmm_lora_add(p.X, p.A, p.B, p.ids, scale=p.scale, base=p.base)
+    dX, dA2, dB2 = Q.qmm_lora_grad(p.dY, p.X, p.A, p.B, p.ids, scale=p.scale)
+    keep = np.arange(M) != 0
+    assert np.array_equal(host_bits(y)[keep], host_bits(clean)[keep])     # row 4 has no adapter: base
+    assert not bool(t.isfinite(y[0]).any())
+    assert bool(t.isfinite(dX[1:]).all()) and not bool(t.isfinite(dX[0]).any())
+    for g, g2 in ((dA, dA2), (dB, dB2)):
+        assert np.array_equal(host_bits(g)[1:], host_bits(g2)[1:])
+        assert not bool(t.isfinite(g2[0]).any())
+
+
+def check_grad(p, dx, g, keep_t, label=""):
+    t = torch()
+    M, K, N, r, L = p.dims
+    say(f"  lora_grad {label} M={M} K={K} N={N} r={r} L={L} {p.ty} dx={dx} g={g} T={keep_t}")
+    T = None
+    if keep_t:
+        T = t.empty((M, r), device="cuda")
+        Q.qmm_lora_add(p.X, p.A, p.B, p.ids, scale=p.scale, T=T)
+    got = Q.qmm_lora_grad(p.dY, p.X, p.A, p.B, p.ids, scale=p.scale, T=T, base=p.base, dx_dtype=tt(dx),
+                          grad_dtype=tt(g))
+    args = p.oracle_args()
+    tw = AO.lora_t(args[0], args[1], p.ids_h) if T is None else host_f64(T)
+    ref = AO.lora_grad(p.host("dY"), *args, T=tw, base=p.host("base"))
+    lim = abs_grad(p, AO.lora_t(np.abs(args[0]), np.abs(args[1]), p.ids_h))
+    # dT: N products; dX: r more; dA: M more; dB: M products with T (K when computed again)
+    for y, want, a, n, ty, name in zip(got, ref, lim, (N + r, N + M, K + M), (dx, g, g), ("dX", "dA", "dB")):
+        assert_elementwise(host_f64(y), want, gamma(n + 60) * a, ty, f"{label} {name}")
+    return got
+
+
+@pytest.mark.parametrize("M,K,N,r,L", SIZES)
+@pytest.mark.parametrize("ty", ["f16", "bf16"])
+def test_grad_sizes(M, K, N, r, L, ty):
+    check_grad(Problem(M, K, N, r, L, ty, seed=M + N + r, base="f32", base_width=K), ty, "f32", keep_t=True)
+
+
+@pytest.mark.parametrize("ids", ["none", "one", "runs"])
+def test_grad_orders_and_types(ids):
+    """No rows at all, one adapter's long run (several chunks), runs; 16-bit gradients; T computed
+    again."""
+    for ty, g in (("f16", "f16"), ("bf16", "bf16"), ("bf16", "f32")):
+        p = Problem(700, 264, 136, 16, 3, ty, seed=23, ids=ids, base=ty, base_width=264)
+        dX, dA, dB = check_grad(p, "f32", g, keep_t=False, label=ids)
+        if ids == "none":
+            assert not bool(dA.any()) and not bool(dB.any())
+
+
+def test_grad_misaligned():
+    check_grad(Problem(130, 128, 64, 16, 3, "bf16", seed=29, offset=1), "bf16", "f32", keep_t=True)
+
+
+def test_grad_many_rows_one_adapter():
+    """8192 rows: many chunks of one adapter, and an adapter without rows."""
+    p = Problem(8192, 256, 384, 16, 2, "bf16", seed=31, ids=np.zeros(8192), base="f32", base_width=256)
+    _, dA, dB = check_grad(p, "bf16", "f32", keep_t=True)
+    assert not bool(dA[1].any()) and not bool(dB[1].any())
+
+
+def test_grad_parts_and_empty_batch():
+    """Each gradient alone equals the joint call; no rows give zero dA and dB."""
+    t = torch()
+    p = Problem(90, 128, 64, 8, 3, "f16", seed=37)
+    full = Q.qmm_lora_grad(p.dY, p.X, p.A, p.B, p.ids, scale=p.scale)
+    for i in range(3):
+        need = tuple(j == i for j in range(3))
+        one = Q.qmm_lora_grad(p.dY, p.X, p.A, p.B, p.ids, scale=p.scale, need=need)
+        assert [v is not None for v in one] == list(need)
+        assert np.array_equal(host_bits(one[i]), host_bits(full[i]))
+    e = Problem(0, 128, 64, 8, 3, "f16", seed=41)
+    dA = t.full((3, 8, 128), 5.0, device="cuda")
+    dB = t.full((3, 64, 8), 5.0, device="cuda")
+    dX, dA, dB = Q.qmm_lora_grad(e.dY, e.X, e.A, e.B, e.ids, scale=e.scale, dA=dA, dB=dB)
+    assert dX.shape == (0, 128) and not bool(dA.any()) and not bool(dB.any())
+    assert Q.qmm_lora_add(e.X, e.A, e.B, e.ids).shape == (0, 64)
+
+
+@pytest.mark.parametrize("M", [8, 400])
+def test_repeats_streams_and_graph(M):
+    """Repeated calls, a call on another stream and replays of a captured graph (with the inputs
+    changed between replays) give the bits of the plain call."""
+    t = torch()
+    p = Problem(M, 640, 192, 16, 4, "bf16", seed=43, base="f32")
+    p.base_dx = t.randn(M, 640, device="cuda")
+    add_ws = t.empty(Q.lib().qmm_lora_add_workspace_bytes(M, 640, 192, 16, 4), dtype=t.uint8, device="cuda")
+    grad_ws = t.empty(Q.lib().qmm_lora_grad_workspace_bytes(M, 640, 192, 16, 4), dtype=t.uint8, device="cuda")
+
+    def step(outs=None):
+        o = outs or [t.empty(M, 192, dtype=t.bfloat16, device="cuda"), t.empty(M, 16, device="cuda"),
+                     t.empty(M, 640, dtype=t.bfloat16, device="cuda"), t.empty(4, 16, 640, device="cuda"),
+                     t.empty(4, 192, 16, device="cuda")]
+        Q.qmm_lora_add(p.X, p.A, p.B, p.ids, scale=p.scale, base=p.base, out=o[0], T=o[1], workspace=add_ws)
+        Q.qmm_lora_grad(p.dY, p.X, p.A, p.B, p.ids, scale=p.scale, T=o[1], base=p.base_dx, dX=o[2], dA=o[3], dB=o[4],
+                        workspace=grad_ws)
+        return o
+
+    ref = [host_bits(v).copy() for v in step()]
+    for _ in range(5):
+        for v, want in zip(step(), ref):
+            assert np.array_equal(host_bits(v), want)
+    side = t.cuda.Stream()
+    side.wait_stream(t.cuda.current_stream())
+    with t.cuda.stream(side):
+        outs = step()
+    side.synchronize()
+    for v, want in zip(outs, ref):
+        assert np.array_equal(host_bits(v), want)
+    g = t.cuda.CUDAGraph()
+    with t.cuda.graph(g):
+        step(outs)
+    x0, ids0 = p.X.clone(), p.ids.clone()
+    for k in range(4):
+        p.X.copy_(x0 * (k + 1))
+        p.ids.copy_(t.roll(ids0, k))
+        g.replay()
+        t.cuda.synchronize()
+        got = [host_bits(v).copy() for v in outs]
+        for v, want in zip(got, step()):
+            assert np.array_equal(v, host_bits(want)), k
+
+
+@pytest.mark.parametrize("M", [1, 24, 200])
+def test_adapters_beside_a_low_bit_projection(M):
+    """The operator as it is used: qmm_nbits with an fp32 output, then the adapters on it."""
+    K, N, L, r = 512, 384, 5, 16
+    p = gen.nbits_problem(M, K, N, 4, 64, seed=51, a_dtype="bf16", zp="packed")
+    q = Problem(M, K, N, r, L, "bf16", seed=53)
+    x = dev(p["A"]).view(torch().bfloat16)
+    base = Q.qmm_nbits(x, dev(p["W"]), dev(p["scales"]), K, 4, 64, dev(p["zp"]), Q.QMM_ZP_PACKED,
+                       out_dtype=torch().float32)
+    y = Q.qmm_lora_add(x, q.A, q.B, q.ids, scale=q.scale, base=base)
+    q.X, q.base = x, base
+    exact = O.qmm_nbits(p["A"], "bf16", p["W"], 4, K, 64, p["scales"], p["zp"], O.ZP_PACKED)
+    ref = AO.lora_add(*q.oracle_args(), base=exact)
+    # the projection's fp16 operands (M > 8): 2^-11 each, relative to the sum's absolute values
+    w = np.abs(O.dequant_nbits(p["W"], 4, K, 64, p["scales"], p["zp"], O.ZP_PACKED).astype(np.float64))
+    lim = gamma(K + r + 40) * abs_add(q) + 2.0 ** -10 * (np.abs(q.host("X")) @ w.T)
+    assert_elementwise(host_f64(y), ref, lim, "bf16", f"M={M}")
+
+
+def test_refusals_on_the_device():
+    t = torch()
+    p = Problem(4, 64, 32, 8, 2, "f16", seed=61)
+    with pytest.raises(ValueError):
+        Q.qmm_lora_add(p.X, p.A, p.B, p.ids[:3])
+    with pytest.raises(TypeError):
+        Q.qmm_lora_add(p.X, p.A, p.B, p.ids.long())
+    with pytest.raises(ValueError):
+        Q.qmm_lora_add(p.X.t().contiguous().t(), p.A, p.B, p.ids)
+    with pytest.raises(TypeError):
+        Q.qmm_lora_add(p.X, p.A.bfloat16(), p.B, p.ids)
+    with pytest.raises(ValueError):
+        Q.qmm_lora_add(p.X, p.A, p.B[:, :, :4].contiguous(), p.ids)
+    with pytest.raises(Q.QmmError) as e:
+        Q.qmm_lora_add(p.X, p.A, p.B, p.ids, workspace=t.empty(16, dtype=t.uint8, device="cuda"))
+    assert e.value.status == -7
+    with pytest.raises(ValueError):
+        Q.qmm_lora_grad(p.dY.t().contiguous(), p.X, p.A, p.B, p.ids)
