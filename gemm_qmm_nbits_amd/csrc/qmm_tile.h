@@ -1,0 +1,169 @@
+// Tiles of 16-bit operands in LDS for the matrix cores: how a stage of 32 contraction
+// values is copied in and read back as operands of v_mfma_f32_32x32x16.
+//
+// An operand tile holds T rows (output rows or columns) by 32 contraction values, in one of
+// two forms, by how the operand lies in memory:
+//   along   the contraction runs along memory rows: [T][32], 64 bytes per tile row.  A lane's
+//           operand (8 consecutive contraction values of one row) is one 16-byte read.
+//   across  the contraction runs down memory columns: [32][T], 2 T bytes per contraction
+//           value.  A lane's operand is two ds_read_b64_tr_b16, each of which hands a group
+//           of 16 lanes a 4 x 16 block transposed.
+// Either way tiles are filled by direct global->LDS copies of 16 bytes per lane, which write
+// LDS in lane order, so the bank swizzle is applied by choosing which 16 bytes a lane fetches:
+//   along   piece p (of 4) of row r sits at p ^ ((r / 4) % 4): 16 rows read at one piece cover
+//           the 16 bank groups of a 256-byte line.
+//   across  the 64-byte segment s of contraction row c sits at s ^ (c % 4) (T = 64, two segments:
+//           s ^ ((c / 2) % 2)): the four rows of a transposed read lie in four bank quarters.
+// Bytes outside the operand (rows past the end, contraction values past the end) read as zero:
+// their lanes address past the buffer descriptor's range, which fetches nothing and writes 0.
+#pragma once
+
+#include "qmm_device.h"
+
+namespace qmm {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kStage = 32;                       // contraction values per stage
+constexpr uint32_t kPastRange = 0x80000000u;     // an offset past every descriptor's range
+constexpr uint32_t kTileRange = 0x7fffffffu;
+
+typedef __attribute__((address_space(3))) uint8_t lds_u8;
+
+template <int TY>
+__device__ __forceinline__ f32x16 mfma32(const uint4& a, const uint4& b, f32x16 c) {
+  if constexpr (TY == QMM_F16)
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0,
+                                                   0);
+}
+
+// Copies one operand's tiles.  T: tile rows; NW: waves; ACROSS: the form; VEC: 16-byte
+// copies (else element loads through registers).
+template <int T, int NW, bool ACROSS, bool VEC>
+struct TileLoad {
+  static constexpr int kPer = T * 64 / 1024 / NW;  // copies per wave and stage
+  static_assert(kPer >= 1, "every wave copies, so that all wait for the same count");
+  const uint8_t* base;  // first row (along) or first contraction row (across)
+  int64_t ld;           // bytes between memory rows
+  uint32_t off[kPer];   // this lane's offset (bytes), or kPastRange
+  int left;             // along: contraction values in all; across: contraction rows in all
+  int crow[kPer];       // first contraction value of this lane's piece within the stage
+  int width;            // across: elements of the tile's row range that exist (VEC off)
+  int rows;             // along: rows of the tile that exist
+
+  // p: the operand's first row / first contraction row; `exist`: rows (along) or columns
+  // (across) of the tile inside the operand; `total`: contraction length.
+  __device__ __forceinline__ void init(const uint16_t* p, int64_t ld_elems, int64_t exist, int64_t total, int wave,
+                                       int lane) {
+    base = (const uint8_t*)p;
+    ld = ld_elems * 2;
+    left = (int)total;
+    rows = width = exist < T ? (int)exist : T;
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) {
+      const int at = (wave * kPer + q) * 1024 + lane * 16;  // LDS byte of this lane's piece
+      if constexpr (ACROSS) {
+        const int c = at / (2 * T), pos = (at % (2 * T)) / 16;
+        const int piece = pos ^ (T == 64 ? ((c >> 1) & 1) << 2 : (c & 3) << 2);
+        crow[q] = c;
+        off[q] = piece * 8 < width ? (uint32_t)(c * ld) + (uint32_t)piece * 16u : kPastRange;
+      } else {
+        const int r = at / 64, piece = ((at % 64) / 16) ^ ((r >> 2) & 3);
+        crow[q] = piece * 8;
+        off[q] = r < rows ? (uint32_t)(r * ld) + (uint32_t)piece * 16u : kPastRange;
+      }
+    }
+  }
+
+  // Stage s of the contraction into dst.
+  __device__ __forceinline__ void stage(int s, uint8_t* dst, int wave, int lane) const {
+    const int c0 = s * kStage;
+    if constexpr (VEC) {
+      const uint8_t* p = ACROSS ? base + (int64_t)c0 * ld : base + (int64_t)c0 * 2;
+      const __amdgpu_buffer_rsrc_t r = make_rsrc(p, kTileRange);
+#pragma unroll
+      for (int q = 0; q < kPer; ++q) {
+        const uint32_t o = c0 + crow[q] < left ? off[q] : kPastRange;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)(dst + (wave * kPer + q) * 1024),
+                                                 16, (int)o, 0, 0, 0);
+      }
+    } else {
+#pragma unroll
+      for (int q = 0; q < kPer; ++q) {
+        const int at = (wave * kPer + q) * 1024 + lane * 16;
+        uint32_t w[4] = {0u, 0u, 0u, 0u};
+        if (off[q] != kPastRange) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            bool ok;
+            const uint16_t* src;
+            if constexpr (ACROSS) {
+              const int pos = (at % (2 * T)) / 16;
+              const int piece = pos ^ (T == 64 ? ((crow[q] >> 1) & 1) << 2 : (crow[q] & 3) << 2);
+              ok = piece * 8 + e < width && c0 + crow[q] < left;
+              src = (const uint16_t*)(base + (int64_t)(c0 + crow[q]) * ld) + piece * 8 + e;
+            } else {
+              ok = c0 + crow[q] + e < left;
+              src = (const uint16_t*)(base + (int64_t)(at / 64) * ld) + c0 + crow[q] + e;
+            }
+            if (ok) w[e / 2] |= (uint32_t)*src << (16 * (e & 1));
+          }
+        }
+        *(uint4*)(dst + at) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+  }
+};
+
+// Reads operands of one 32-row fragment.  The lane part of the address is fixed; `row` (a
+// multiple of 32) and the half (contraction values 16 half ..) are constants of the code.
+template <int T, bool ACROSS>
+struct TileRead {
+  uint32_t at;     // along: byte of row lane % 32;  across: byte of this lane's block row
+  uint32_t sw;     // along: (row / 4) % 4;  across: the segment exclusive-or
+
+  __device__ __forceinline__ void init(int row0, int lane) {
+    if constexpr (ACROSS) {
+      const int i = lane & 15, g = lane >> 4;
+      const int c = 8 * (g >> 1) + (i >> 2);
+      sw = T == 64 ? (uint32_t)((c >> 1) & 1) : (uint32_t)(c & 3);
+      at = (uint32_t)(c * 2 * T + ((g & 1) * 16 + 4 * (i & 3)) * 2);
+    } else {
+      const int r = lane & 31;
+      sw = (uint32_t)((r >> 2) & 3);
+      at = (uint32_t)((row0 + r) * 64);
+    }
+    seg0 = row0 / 32;
+  }
+  int seg0;
+
+  // fragment f (rows row0 + 32 f ..), half h (0 or 1)
+  __device__ __forceinline__ uint4 get(const uint8_t* tile, int f, int h, int lane) const {
+    if constexpr (ACROSS) {
+      const uint32_t o = at + (uint32_t)(h * 16 * 2 * T) + ((uint32_t)(seg0 + f) ^ sw) * 64u;
+      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(tile + o));
+      // four contraction rows on; the segment swizzle is the same there for T > 64, and
+      // repeats with period four rows for T = 64
+      const s16x4 hi =
+          __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(tile + o + 4 * 2 * T));
+      const uint2 l2 = __builtin_bit_cast(uint2, lo), h2 = __builtin_bit_cast(uint2, hi);
+      return make_uint4(l2.x, l2.y, h2.x, h2.y);
+    } else {
+      const uint32_t piece = (uint32_t)(2 * h + (lane >> 5)) ^ sw;
+      return *(const uint4*)(tile + at + (uint32_t)f * 32u * 64u + piece * 16u);
+    }
+  }
+};
+
+// Waits until this wave's copies into LDS but the newest N, and all its LDS accesses, are
+// done, then for the other waves of the work-group: after it, every wave's copies older than
+// those are in LDS, and no wave still reads what they had read before.
+template <int N>
+__device__ __forceinline__ void stage_barrier() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+}  // namespace qmm

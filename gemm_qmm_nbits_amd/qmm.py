@@ -98,6 +98,14 @@ _SIGS = {
                          c_void_p, c_void_p]),
     "qmm_qswiglu": (c_int, [c_void_p, c_void_p, c_int, c_int64, c_int, POINTER(qmm_qparams), c_void_p,
                             c_void_p]),
+    "qmoe_grouped_mm": (c_int, [c_void_p, c_int, c_int64, c_int64, c_int64, c_int64, c_void_p, c_void_p, c_void_p,
+                                c_void_p, c_int, c_void_p]),
+    "qmoe_grouped_mm_grad": (c_int, [c_void_p, c_void_p, c_int, c_int64, c_int64, c_int64, c_int64, c_void_p,
+                                     c_void_p, c_void_p, c_int, c_void_p, c_void_p, c_int, c_void_p]),
+    "qmm_validate_grouped_mm": (c_int, [c_void_p, c_int, c_int64, c_int64, c_int64, c_int64, c_void_p, c_void_p,
+                                        c_void_p, c_void_p, c_int]),
+    "qmm_validate_grouped_mm_grad": (c_int, [c_void_p, c_void_p, c_int, c_int64, c_int64, c_int64, c_int64, c_void_p,
+                                             c_void_p, c_void_p, c_int, c_void_p, c_void_p, c_int]),
     "qmm_lora_add": (c_int, [c_void_p, c_int, c_int64, c_int64, c_int64, c_int, c_int64, c_void_p,
                              qmm_lora_weights, c_void_p, c_int, c_void_p, c_int, c_void_p, c_void_p, c_size_t,
                              c_void_p]),
@@ -570,6 +578,69 @@ def qmm_lora_grad(dY, X, A, B, ids, scale=None, T=None, base=None, dX=None, dA=N
                              QMM_F32 if g is None else dtype_code(g), _ptr(workspace), wsb, _stream(stream))
     _check("qmm_lora_grad", st)
     return dX, dA, dB
+
+
+# ---------------------------------------------------------------------------
+# ragged products of 16-bit weights
+# ---------------------------------------------------------------------------
+
+def _grouped_shapes(X, W, row_offsets):
+    torch = _torch()
+    if X.dim() != 2 or W.dim() != 3:
+        raise ValueError("rows must be [R, K] and W [E, N, K]")
+    if X.dtype not in (torch.float16, torch.bfloat16):
+        raise TypeError(f"unsupported dtype {X.dtype}")
+    R, (E, N, K) = X.shape[0], W.shape
+    _on_current_device(X)
+    _expect(X, "X", (R, K), (X.dtype,))
+    _expect(W, "W", (E, N, K), (X.dtype,), X)
+    _expect(row_offsets, "row_offsets", (E + 1,), (torch.int32,), X)
+    return R, K, N, E
+
+
+def qmoe_grouped_mm(X, row_offsets, W, bias=None, out=None, out_dtype=None, stream=None):
+    """Y[r] = X[r] W[e]^T (+ bias[e]) for the rows row_offsets[e] .. row_offsets[e+1] of expert e.
+
+    X [R, K], W [E, N, K] fp16 or bf16; bias [E, N] of the output's dtype (default X's)."""
+    torch = _torch()
+    R, K, N, E = _grouped_shapes(X, W, row_offsets)
+    if out is None:
+        out = torch.empty((R, N), dtype=out_dtype or X.dtype, device=X.device)
+    _expect(out, "out", (R, N), (torch.float32, torch.float16, torch.bfloat16), X)
+    _expect(bias, "bias", (E, N), (out.dtype,), X)
+    st = lib().qmoe_grouped_mm(_ptr(X), dtype_code(X), R, K, N, E, _ptr(row_offsets), _ptr(W), _ptr(bias), _ptr(out),
+                               dtype_code(out), _stream(stream))
+    _check("qmoe_grouped_mm", st)
+    return out
+
+
+def qmoe_grouped_mm_grad(dY, X, row_offsets, W, dX=None, dW=None, dbias=None, dx_dtype=None, dw_dtype=None,
+                         need=(True, True), need_dbias=False, stream=None):
+    """Gradients (dX, dW, dbias) of qmoe_grouped_mm; need: whether dX and dW are computed.
+
+    dX[r] = dY[r] W[e] of dx_dtype (default X's); dW[e] = sum dY[r]^T X[r] and dbias[e] = sum dY[r]
+    over the rows of expert e, of dw_dtype (default X's)."""
+    torch = _torch()
+    R, K, N, E = _grouped_shapes(X, W, row_offsets)
+    any_type = (torch.float32, torch.float16, torch.bfloat16)
+    _expect(dY, "dY", (R, N), (X.dtype,), X)
+
+    def output(t, wanted, name, shape, dtype):
+        if t is None and wanted:
+            t = torch.empty(shape, dtype=dtype, device=X.device)
+        return _expect(t, name, shape, any_type, X)
+
+    dX = output(dX, need[0], "dX", (R, K), dx_dtype or X.dtype)
+    dW = output(dW, need[1], "dW", (E, N, K), dw_dtype or X.dtype)
+    dbias = output(dbias, need_dbias, "dbias", (E, N), dw_dtype or (X.dtype if dW is None else dW.dtype))
+    if dW is not None and dbias is not None and dW.dtype != dbias.dtype:
+        raise TypeError("dW and dbias differ in dtype")
+    g = dW if dW is not None else dbias
+    st = lib().qmoe_grouped_mm_grad(_ptr(dY), _ptr(X), dtype_code(X), R, K, N, E, _ptr(row_offsets), _ptr(W),
+                                    _ptr(dX), QMM_F32 if dX is None else dtype_code(dX), _ptr(dW), _ptr(dbias),
+                                    QMM_F32 if g is None else dtype_code(g), _stream(stream))
+    _check("qmoe_grouped_mm_grad", st)
+    return dX, dW, dbias
 
 
 def hbm_read_probe(buf, sink, groups, stream=None):

@@ -380,6 +380,40 @@ qmm_status qmm_qswiglu(const void* gate, const void* up, int x_type, int64_t n, 
                        const qmm_qparams* q, void* y, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * qmoe_grouped_mm -- the ragged expert product of 16-bit weights, and its gradients (layers
+ * kept in 16 bits next to the low-bit ones of qmoe_ragged_mm, and their training).
+ *   Rows are grouped by expert as for qmoe_ragged_mm (row_offsets [E+1] int32 on the device;
+ *   values are clamped into [0, R]).  For each row r of expert e
+ *     Y[r]    = X[r] . W_e^T (+ bias_e)
+ *     dX[r]   = dY[r] . W_e
+ *     dW_e    = sum over the rows r of expert e of dY[r]^T X[r];  dbias_e = sum of dY[r]
+ *   (zeros for an expert without rows; rows no expert owns are not written and their values
+ *   reach no result), products exact, fp32 sums in an order that depends only on the sizes and
+ *   offsets, each output rounded once.
+ *   X [R][K], dY [R][N], W [E][N][K] of `type` (QMM_F16 or QMM_BF16).  bias [E][N] of y_type or
+ *   NULL.  Y [R][N] of y_type, dX [R][K] of dx_type, dW [E][N][K] and dbias [E][N] of dw_type;
+ *   of qmoe_grouped_mm_grad's outputs each may be NULL (not computed).
+ *   R <= 2^24, 1 <= K, N <= 2^20, 1 <= E <= 65535.  Any sizes and element alignment are served;
+ *   rows of 16-byte multiples from 16-byte aligned tensors take the direct copies into LDS.
+ * ------------------------------------------------------------------------- */
+qmm_status qmoe_grouped_mm(const void* X, int type, int64_t R, int64_t K, int64_t N, int64_t E,
+                           const int32_t* row_offsets, const void* W, const void* bias, void* Y,
+                           int y_type, void* stream);
+qmm_status qmoe_grouped_mm_grad(const void* dY, const void* X, int type, int64_t R, int64_t K,
+                                int64_t N, int64_t E, const int32_t* row_offsets, const void* W,
+                                void* dX, int dx_type, void* dW, void* dbias, int dw_type,
+                                void* stream);
+
+/* Host-only checks of the arguments, as qmm_validate_nbits. */
+qmm_status qmm_validate_grouped_mm(const void* X, int type, int64_t R, int64_t K, int64_t N,
+                                   int64_t E, const int32_t* row_offsets, const void* W,
+                                   const void* bias, const void* Y, int y_type);
+qmm_status qmm_validate_grouped_mm_grad(const void* dY, const void* X, int type, int64_t R,
+                                        int64_t K, int64_t N, int64_t E, const int32_t* row_offsets,
+                                        const void* W, const void* dX, int dx_type, const void* dW,
+                                        const void* dbias, int dw_type);
+
+/* ---------------------------------------------------------------------------
  * Low-rank adapters of many requests beside a shared projection, and their gradients.
  *
  * Row m of a batch belongs to a request with adapter a = ids[m] (an id outside [0, L):
