@@ -98,6 +98,15 @@ _SIGS = {
                          c_void_p, c_void_p]),
     "qmm_qswiglu": (c_int, [c_void_p, c_void_p, c_int, c_int64, c_int, POINTER(qmm_qparams), c_void_p,
                             c_void_p]),
+    "qmm_nbits_dgrad": (c_int, [c_void_p, c_int, c_int64, c_int64, c_int64, c_void_p, c_int, c_int, c_void_p, c_void_p,
+                                c_int, c_float, c_void_p, c_int, c_void_p, c_size_t, c_void_p]),
+    "qmm_codebook4_dgrad": (c_int, [c_void_p, c_int, c_int64, c_int64, c_int64, c_void_p, c_int, c_void_p, c_void_p,
+                                    c_void_p, c_int, c_void_p, c_size_t, c_void_p]),
+    "qmm_dgrad_workspace_bytes": (c_size_t, [c_int64, c_int64, c_int64]),
+    "qmm_validate_nbits_dgrad": (c_int, [c_void_p, c_int, c_int64, c_int64, c_int64, c_void_p, c_int, c_int, c_void_p,
+                                         c_void_p, c_int, c_void_p, c_int, c_void_p, c_size_t]),
+    "qmm_validate_codebook4_dgrad": (c_int, [c_void_p, c_int, c_int64, c_int64, c_int64, c_void_p, c_int, c_void_p,
+                                             c_void_p, c_void_p, c_int, c_void_p, c_size_t]),
     "qmoe_grouped_mm": (c_int, [c_void_p, c_int, c_int64, c_int64, c_int64, c_int64, c_void_p, c_void_p, c_void_p,
                                 c_void_p, c_int, c_void_p]),
     "qmoe_grouped_mm_grad": (c_int, [c_void_p, c_void_p, c_int, c_int64, c_int64, c_int64, c_int64, c_void_p,
@@ -578,6 +587,64 @@ def qmm_lora_grad(dY, X, A, B, ids, scale=None, T=None, base=None, dX=None, dA=N
                              QMM_F32 if g is None else dtype_code(g), _ptr(workspace), wsb, _stream(stream))
     _check("qmm_lora_grad", st)
     return dX, dA, dB
+
+
+# ---------------------------------------------------------------------------
+# input gradients of low-bit projections
+# ---------------------------------------------------------------------------
+
+def _dgrad_shapes(dY, W, K, block, bits, out, out_dtype):
+    """Checks dY [M, N] and the packed weights W [N, nblk, block * bits / 8]; returns M, N, out."""
+    torch = _torch()
+    any_type = (torch.float32, torch.float16, torch.bfloat16)
+    if dY.dim() != 2:
+        raise ValueError("dY must be [M, N]")
+    M, N = dY.shape
+    _on_current_device(dY)
+    _expect(dY, "dY", (M, N), any_type)
+    if W.shape[0] != N or W.numel() != N * nblocks(K, block) * (block * bits // 8):
+        raise ValueError(f"W does not hold {N} rows of {K} codes of {bits} bits in blocks of {block}")
+    _expect(W, "W", W.shape, (torch.uint8,), dY)
+    if out is None:
+        out = torch.empty((M, K), dtype=out_dtype or dY.dtype, device=dY.device)
+    return M, N, _expect(out, "out", (M, K), any_type, dY)
+
+
+def _sized(t, name, count, like):
+    """A dense tensor of at least `count` elements on like's device."""
+    if t.numel() < count:
+        raise ValueError(f"{name} must hold {count} elements, got {t.numel()}")
+    if t.device != like.device:
+        raise ValueError(f"{name} must be on the device of the call")
+    return _contig(t, name)
+
+
+def qmm_nbits_dgrad(dY, W, scales, K, bits, block, zp=None, zp_kind=QMM_ZP_NONE, uniform_zp=0.0, out=None,
+                    out_dtype=None, workspace=None, stream=None):
+    """dX[M, K] = dY[M, N] . dequant(W): the input gradient of qmm_nbits, from the same weight buffers."""
+    M, N, out = _dgrad_shapes(dY, W, K, block, bits, out, out_dtype)
+    nblk = nblocks(K, block)
+    _sized(scales, "scales", N * nblk, dY)
+    if zp is not None and zp_kind in (QMM_ZP_PACKED, QMM_ZP_F16):
+        _sized(zp, "zp", N * ((nblk * bits + 7) // 8 if zp_kind == QMM_ZP_PACKED else nblk), dY)
+    workspace, wsb = _workspace(workspace, lib().qmm_dgrad_workspace_bytes(M, K, N), dY)
+    st = lib().qmm_nbits_dgrad(_ptr(dY), dtype_code(dY), M, K, N, _ptr(W), bits, block, _ptr(scales), _ptr(zp),
+                               zp_kind, float(uniform_zp), _ptr(out), dtype_code(out), _ptr(workspace), wsb,
+                               _stream(stream))
+    _check("qmm_nbits_dgrad", st)
+    return out
+
+
+def qmm_codebook4_dgrad(dY, W, absmax, codebook, K, block=64, out=None, out_dtype=None, workspace=None, stream=None):
+    """dX[M, K] = dY[M, N] . (codebook[q] * absmax): the input gradient of qmm_codebook4."""
+    M, N, out = _dgrad_shapes(dY, W, K, block, 4, out, out_dtype)
+    _sized(absmax, "absmax", N * nblocks(K, block), dY)
+    _sized(codebook, "codebook", 16, dY)
+    workspace, wsb = _workspace(workspace, lib().qmm_dgrad_workspace_bytes(M, K, N), dY)
+    st = lib().qmm_codebook4_dgrad(_ptr(dY), dtype_code(dY), M, K, N, _ptr(W), block, _ptr(absmax), _ptr(codebook),
+                                   _ptr(out), dtype_code(out), _ptr(workspace), wsb, _stream(stream))
+    _check("qmm_codebook4_dgrad", st)
+    return out
 
 
 # ---------------------------------------------------------------------------

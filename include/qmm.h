@@ -380,6 +380,39 @@ qmm_status qmm_qswiglu(const void* gate, const void* up, int x_type, int64_t n, 
                        const qmm_qparams* q, void* y, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * qmm_nbits_dgrad, qmm_codebook4_dgrad -- the input gradient of a frozen low-bit projection:
+ *   dX[M][K] = dY[M][N] . dequant(W)
+ *   with W, scales, zp / absmax, codebook as for qmm_nbits / qmm_codebook4 (the same buffers;
+ *   nested absmax: decode it once with qmm_dequantize_absmax_nested).
+ *   dY [M][N] of dy_type, dX [M][K] of dx_type (any of the three types).  W 4-byte aligned.
+ *   M <= 2^24, 1 <= K, N <= 2^20.
+ * Operands as on the forward matrix-core paths, for every M: dY is rounded to fp16 after one
+ * exact power-of-two scale per row (fp16 dY that is 16-byte aligned with N a multiple of 8 is
+ * read in place), each weight is dequantized exactly in fp32 and rounded to fp16, products are
+ * accumulated in fp32, and the result is rounded once.
+ *   workspace: at least qmm_dgrad_workspace_bytes(M, K, N) bytes, 256-byte aligned.
+ * ------------------------------------------------------------------------- */
+qmm_status qmm_nbits_dgrad(const void* dY, int dy_type, int64_t M, int64_t K, int64_t N,
+                           const uint8_t* W, int bits, int block, const uint16_t* scales,
+                           const void* zp, int zp_kind, float uniform_zp, void* dX, int dx_type,
+                           void* workspace, size_t workspace_bytes, void* stream);
+qmm_status qmm_codebook4_dgrad(const void* dY, int dy_type, int64_t M, int64_t K, int64_t N,
+                               const uint8_t* W, int block, const float* absmax,
+                               const float* codebook, void* dX, int dx_type, void* workspace,
+                               size_t workspace_bytes, void* stream);
+size_t qmm_dgrad_workspace_bytes(int64_t M, int64_t K, int64_t N);
+
+/* Host-only checks of the arguments, as qmm_validate_nbits. */
+qmm_status qmm_validate_nbits_dgrad(const void* dY, int dy_type, int64_t M, int64_t K, int64_t N,
+                                    const uint8_t* W, int bits, int block, const uint16_t* scales,
+                                    const void* zp, int zp_kind, const void* dX, int dx_type,
+                                    const void* workspace, size_t workspace_bytes);
+qmm_status qmm_validate_codebook4_dgrad(const void* dY, int dy_type, int64_t M, int64_t K, int64_t N,
+                                        const uint8_t* W, int block, const float* absmax,
+                                        const float* codebook, const void* dX, int dx_type,
+                                        const void* workspace, size_t workspace_bytes);
+
+/* ---------------------------------------------------------------------------
  * qmoe_grouped_mm -- the ragged expert product of 16-bit weights, and its gradients (layers
  * kept in 16 bits next to the low-bit ones of qmoe_ragged_mm, and their training).
  *   Rows are grouped by expert as for qmoe_ragged_mm (row_offsets [E+1] int32 on the device;
