@@ -48,8 +48,6 @@ struct LoraArgs {
   void* out;
   int out_type;
   float* T;            // [M][r] by row, or NULL
-  int vec;             // X, A, dY, B rows allow 16-byte loads
-  int vec_out;         // base and out rows allow 4-element accesses
 };
 
 hipError_t launch_lora_plan(const LoraArgs& p, hipStream_t st);
@@ -64,24 +62,29 @@ hipError_t launch_lora_expand(const LoraArgs& p, hipStream_t st);
 hipError_t launch_lora_expand_dx(const LoraArgs& p, const float* dT, hipStream_t st);
 
 // out[a] = sum over the rows m of adapter a of Z[m][c] * t[m][rank]: [P][r] (rank_major 0)
-// or [r][P] (rank_major 1), times scale[a] when given.
-struct LoraOuterArgs {
-  const void* Z;  // [M][P] of `type`
-  int type;
+// or [r][P] (rank_major 1), times scale[a] when given.  The two sides are dB (Z = dY) and
+// dA (Z = X); one that is not wanted has no blocks.
+struct LoraSide {
+  const void* Z;  // [M][P]
   int64_t P;
   const float* t;  // [M][r] by row
+  const float* scale;
+  void* out;
+  int rank_major;
+  int blocks;   // ceil(P / 128), or 0
+  float* part;  // fp32 [2 M / chunk + 1][P][r] in out's element order
+};
+struct LoraOuterArgs {
+  LoraSide side[2];
+  int type;
   int r;
   int64_t M, L;
   LoraPlan plan;
-  const float* scale;
-  void* out;
   int out_type;
-  int rank_major;
-  float* part;  // fp32 [2 M / chunk + 1][P][r] in out's element order
-  int chunk;    // rows per chunk (a multiple of 16)
-  int vec;
+  int chunk;  // rows per chunk (a multiple of 64)
 };
-int lora_outer_chunk(int64_t M, int64_t P);
+// Rows per chunk for the column blocks of both sides together.
+int lora_outer_chunk(int64_t M, int64_t blocks);
 hipError_t launch_lora_outer(const LoraOuterArgs& p, hipStream_t st);
 
 }  // namespace qmm

@@ -22,6 +22,8 @@
 #include "qmm_internal.h"
 #include "qmm_lora.h"
 
+#include <type_traits>
+
 namespace qmm {
 
 namespace {
@@ -56,69 +58,105 @@ __device__ __forceinline__ f32x4 mfma16(const uint4& a, const uint4& b, f32x4 c)
                                                    0);
 }
 
-// Elements i .. i + 7 of a row of n 16-bit elements (zeros past n); VEC: n % 8 == 0 and a
-// 16-byte aligned row.
-template <bool VEC>
+// Vectors at any element's address (the hardware takes unaligned vector accesses; aligned
+// ones lose nothing).
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+struct __attribute__((packed, aligned(2))) H8 { u32x4 v; };
+struct __attribute__((packed, aligned(2))) H4 { u32x2 v; };
+struct __attribute__((packed, aligned(4))) F4 { u32x4 v; };
+struct __attribute__((packed, aligned(4))) I4 { u32x4 v; };
+
+__device__ __forceinline__ uint4 load_h8(const uint16_t* p) {
+  const u32x4 v = ((const H8*)p)->v;
+  return make_uint4(v[0], v[1], v[2], v[3]);
+}
+
+// Elements i .. i + 7 of a row of n 16-bit elements, zeros past n.  WHOLE: all are inside.
+template <bool WHOLE>
 __device__ __forceinline__ uint4 load8(const uint16_t* row, int64_t i, int64_t n) {
-  if constexpr (VEC) {
-    if (i < n) return *(const uint4*)(row + i);
-    return make_uint4(0u, 0u, 0u, 0u);
-  } else {
-    uint32_t w[4];
+  if (WHOLE || i + 8 <= n) return load_h8(row + i);
+  uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const uint32_t lo = i + 2 * e < n ? row[i + 2 * e] : 0u;
-      const uint32_t hi = i + 2 * e + 1 < n ? row[i + 2 * e + 1] : 0u;
-      w[e] = lo | (hi << 16);
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
-  }
+  for (int e = 0; e < 8; ++e)
+    if (i + e < n) w[e / 2] |= (uint32_t)row[i + e] << (16 * (e & 1));
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // ---- rows sorted by adapter ---------------------------------------------------------
 //
-// Work-group a collects group a: each thread counts the rows of its contiguous share that
-// belong to the group and to earlier groups, one scan over the threads gives every share
-// its first position, and the thread writes its rows in order.  Every group's position
-// depends only on the ids, so one launch does it.  An id outside [0, L) is group L.
+// Work-group a collects group a.  Each thread takes 8 consecutive ids per sweep of 8192: the
+// first sweeps count the rows of earlier groups (the group's first position), the second
+// ones scan the group's own rows over the threads and write them in order.  Every group's
+// place depends only on the ids, so one launch does it.  An id outside [0, L) is group L.
+// (8192 rows: 4 us, two reads of the ids and two scans; a loop over single ids took 12.)
 constexpr int kPlanThreads = 1024;
+constexpr int kPlanSweep = kPlanThreads * 8;
 
 __global__ __launch_bounds__(kPlanThreads) void lora_plan_kernel(const int32_t* ids, int64_t M, int64_t L, LoraPlan plan) {
-  __shared__ int wave_eq[kPlanThreads / 64], wave_lt[kPlanThreads / 64];
-  const int64_t a = blockIdx.x;
+  constexpr int NW = kPlanThreads / 64;
+  __shared__ int red[2][NW];
+  const int a = (int)blockIdx.x;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int64_t share = (M + kPlanThreads - 1) / kPlanThreads;
-  const int64_t m0 = tid * share < M ? tid * share : M;
-  const int64_t m1 = m0 + share < M ? m0 + share : M;
-  auto group = [&](int64_t m) {
-    const int64_t id = ids[m];
-    return id < 0 || id >= L ? L : id;
-  };
-  int eq = 0, lt = 0;
-  for (int64_t m = m0; m < m1; ++m) {
-    const int64_t g = group(m);
-    eq += g == a;
-    lt += g < a;
-  }
-  int incl = eq, sum_lt = lt;
+  // groups of this thread's 8 ids at m (-1 past the end)
+  auto groups = [&](int64_t m, int (&g)[8]) {
+    if (m + 8 <= M) {
+      const u32x4 u = ((const I4*)(ids + m))->v, v = ((const I4*)(ids + m + 4))->v;
 #pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int v = __shfl_up(incl, d, 64);
-    incl += lane >= d ? v : 0;
-    sum_lt += __shfl_xor(sum_lt, d, 64);
+      for (int e = 0; e < 4; ++e) {
+        g[e] = (int)u[e];
+        g[4 + e] = (int)v[e];
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) g[e] = m + e < M ? ids[m + e] : 0;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) g[e] = m + e >= M ? -1 : g[e] < 0 || g[e] >= (int)L ? (int)L : g[e];
+  };
+  int lt = 0;
+  for (int64_t m = tid * 8; m < M; m += kPlanSweep) {
+    int g[8];
+    groups(m, g);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) lt += g[e] >= 0 && g[e] < a;
   }
-  if (lane == 63) wave_eq[wave] = incl;
-  if (lane == 0) wave_lt[wave] = sum_lt;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) lt += __shfl_xor(lt, d, 64);
+  if (lane == 0) red[0][wave] = lt;
   __syncthreads();
-  int before = 0, first = 0, count = 0;
-  for (int w = 0; w < kPlanThreads / 64; ++w) {
-    before += w < wave ? wave_eq[w] : 0;
-    count += wave_eq[w];
-    first += wave_lt[w];
+  int first = 0;
+#pragma unroll
+  for (int w = 0; w < NW; ++w) first += red[0][w];
+  int count = 0;
+  for (int64_t sweep = 0; sweep < M; sweep += kPlanSweep) {
+    const int64_t m = sweep + tid * 8;
+    int g[8], eq = 0;
+    groups(m, g);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) eq += g[e] == a;
+    int incl = eq;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int v = __shfl_up(incl, d, 64);
+      incl += lane >= d ? v : 0;
+    }
+    __syncthreads();  // the sums of the sweep before have been read
+    if (lane == 63) red[1][wave] = incl;
+    __syncthreads();
+    int before = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      const int v = red[1][w];
+      before += w < wave ? v : 0;
+      all += v;
+    }
+    int pos = first + count + before + incl - eq;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (g[e] == a) plan.perm[pos++] = (int32_t)(m + e);
+    count += all;
   }
-  int pos = first + before + incl - eq;
-  for (int64_t m = m0; m < m1; ++m)
-    if (group(m) == a) plan.perm[pos++] = (int32_t)m;
   if (tid == 0) {
     plan.off[a] = first;
     if (a == L) plan.off[L + 1] = (int32_t)M;
@@ -130,7 +168,7 @@ __global__ __launch_bounds__(kPlanThreads) void lora_plan_kernel(const int32_t* 
     const int64_t at = (s - slot0) * kLoraTile;
     const int64_t left = count - at;
     int32_t* t = plan.tiles + s * 4;
-    t[0] = (int32_t)a;
+    t[0] = a;
     t[1] = (int32_t)(first + at);
     t[2] = left <= 0 ? 0 : (int32_t)(left < kLoraTile ? left : kLoraTile);
     t[3] = 0;
@@ -185,7 +223,7 @@ __device__ __forceinline__ int64_t position(const LoraArgs& p, const Tile& t, co
 // sums are added in wave order through LDS.  TR: B_a is [N][r], its ranks run along the
 // row, so a wave copies 64 rows into LDS and reads them back transposed
 // (ds_read_b64_tr_b16).  NF: 16-rank fragments (1, 2 or 4).
-template <int TY, int NF, bool VEC, bool TR>
+template <int TY, int NF, bool TR>
 __global__ __launch_bounds__(LT) void lora_shrink_kernel(LoraArgs p) {
   constexpr int RS = NF * 16 + 8;  // LDS row of the transposed operand (16-bit elements)
   constexpr int kTrBytes = TR ? 4 * 64 * RS * 2 : 0;
@@ -223,23 +261,29 @@ __global__ __launch_bounds__(LT) void lora_shrink_kernel(LoraArgs p) {
     for (int f = 0; f < NF; ++f) acc[s][f] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
   uint16_t* tr = (uint16_t*)lds + wave * 64 * RS;
-  for (int64_t c0 = c_begin + wave * 64; c0 < c_end; c0 += 256) {
+  auto step = [&](auto whole_c, int64_t c0) {
+    constexpr bool WHOLE = decltype(whole_c)::value;  // all 64 contraction values exist
     uint4 xv[2][4];
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int s = 0; s < 4; ++s)
-        if (s * 16 < t.count) xv[h][s] = load8<VEC>(xrow[s], c0 + 32 * h + 8 * lg, c_end);
+        if (s * 16 < t.count) xv[h][s] = load8<WHOLE>(xrow[s], c0 + 32 * h + 8 * lg, c_end);
     uint4 wv[2][NF];
     if constexpr (TR) {
       // rows c0 .. c0 + 63 of B_a, ranks r0 .. (zeros past r and past the range)
       constexpr int P = NF * 2;  // 8-rank pieces of a row
+      uint4 u[P];
 #pragma unroll
       for (int j = 0; j < P; ++j) {
         const int q = j * 64 + lane, row = q / P, piece = q % P;
-        uint4 u = make_uint4(0u, 0u, 0u, 0u);
-        if (c0 + row < c_end) u = load8<VEC>(W + (c0 + row) * r, r0 + piece * 8, r);
-        *(uint4*)(tr + row * RS + piece * 8) = u;
+        u[j] = make_uint4(0u, 0u, 0u, 0u);
+        if (WHOLE || c0 + row < c_end) u[j] = load8<false>(W + (c0 + row) * r, r0 + piece * 8, r);
+      }
+#pragma unroll
+      for (int j = 0; j < P; ++j) {
+        const int q = j * 64 + lane, row = q / P, piece = q % P;
+        *(uint4*)(tr + row * RS + piece * 8) = u[j];
       }
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       // lane 4i + j of a 16-lane group addresses row i, ranks 4j ..; it receives rows
@@ -259,7 +303,7 @@ __global__ __launch_bounds__(LT) void lora_shrink_kernel(LoraArgs p) {
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int f = 0; f < NF; ++f) wv[h][f] = load8<VEC>(wrow[f], c0 + 32 * h + 8 * lg, c_end);
+        for (int f = 0; f < NF; ++f) wv[h][f] = load8<WHOLE>(wrow[f], c0 + 32 * h + 8 * lg, c_end);
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h)
@@ -269,17 +313,22 @@ __global__ __launch_bounds__(LT) void lora_shrink_kernel(LoraArgs p) {
 #pragma unroll
           for (int f = 0; f < NF; ++f) acc[s][f] = mfma16<TY>(xv[h][s], wv[h][f], acc[s][f]);
         }
-  }
+  };
+  int64_t c0 = c_begin + wave * 64;
+  for (; c0 + 64 <= c_end; c0 += 256) step(std::true_type{}, c0);
+  if (c0 < c_end) step(std::false_type{}, c0);
   // accumulator v of lane: tile row 16 s + 4 (lane / 16) + v, rank 16 f + lane % 16
   __syncthreads();
   float* red = (float*)lds;
 #pragma unroll
   for (int s = 0; s < 4; ++s)
+    if (s * 16 < t.count) {
 #pragma unroll
-    for (int f = 0; f < NF; ++f)
+      for (int f = 0; f < NF; ++f)
 #pragma unroll
-      for (int v = 0; v < 4; ++v)
-        red[(wave * 64 + s * 16 + 4 * lg + v) * (NF * 16) + f * 16 + ln] = acc[s][f][v];
+        for (int v = 0; v < 4; ++v)
+          red[(wave * 64 + s * 16 + 4 * lg + v) * (NF * 16) + f * 16 + ln] = acc[s][f][v];
+    }
   __syncthreads();
   for (int i = threadIdx.x; i < t.count * NF * 16; i += LT) {
     const int row = i / (NF * 16), c = i % (NF * 16);
@@ -292,6 +341,20 @@ __global__ __launch_bounds__(LT) void lora_shrink_kernel(LoraArgs p) {
   }
 }
 
+// Sum of the splits' parts at q (in split order), eight loads at a time.
+__device__ __forceinline__ float sum_parts(const LoraArgs& p, const float* q) {
+  const int64_t stride = p.M * p.rp;
+  float v = 0.0f;
+  for (int s = 0; s < p.splits; s += 8) {
+    float u[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) u[e] = q[(s + e < p.splits ? s + e : p.splits - 1) * stride];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v += s + e < p.splits ? u[e] : 0.0f;
+  }
+  return v;
+}
+
 // T[row][rank] = sum over the splits of part, in split order, times scale_a; rows without
 // an adapter get zeros.
 __global__ __launch_bounds__(LT) void lora_finalize_kernel(LoraArgs p, int scaled, float* T) {
@@ -302,241 +365,252 @@ __global__ __launch_bounds__(LT) void lora_finalize_kernel(LoraArgs p, int scale
     const int row = i / p.r, c = i - row * p.r;
     float v = 0.0f;
     if (t.a < p.L) {
-      const float* q = p.part + position(p, t, rows, row) * p.rp + c;
-      v = q[0];
-      for (int s = 1; s < p.splits; ++s) v += q[(int64_t)s * p.M * p.rp];
-      v *= sc;
+      v = sc * sum_parts(p, p.part + position(p, t, rows, row) * p.rp + c);
     }
     T[(int64_t)rows[row] * p.r + c] = v;
   }
 }
 
-// ---- expand: out = base + t W, W = B_a^T (rank along B's rows) ------------------------
+// ---- expand: out = base + t B_a^T, and of the gradient: out = base + dt A_a (DX) ---------
 //
-// One work-group: a tile and every (4 gridDim.y)-th group of 64 output columns per wave.
-// t (summed over the splits, times scale_a) is staged in LDS.  v_mfma_f32_16x16x4_f32 with
-// the columns as its rows: lane l gives B element (column l % 16, ranks 16 s + 4 (l / 16)
-// + 0..3, one 8-byte load) and t element (row l % 16, the same ranks) for four steps, and
-// holds 4 consecutive columns of one row of the result.
+// One work-group: a tile and, per wave, every (4 gridDim.y)-th group of 64 output columns.
+// t is staged in LDS.  v_mfma_f32_16x16x4_f32 with the columns as its rows: a lane gives
+// B_a (or A_a) at one of 16 columns and 4 ranks for four steps and 16-column parts, and t of
+// row lane % 16 at the same ranks.
+//   forward  column 16 f + i is row i of part f: lane l loads B[16 f + l % 16][16 c + 4 (l / 16) ..]
+//            (ranks along the row), and ends with columns 16 f + 4 (l / 16) ..
+//   DX       column 4 i + f is row i of part f: lane l loads A[16 c + 4 (l / 16) + j][4 (l % 16) ..]
+//            (columns along the row), and ends with columns 16 (l / 16) + 4 v ..
+// NR: the 16-rank steps whose operands a wave keeps in registers over the tile's rows (up to
+// 64 ranks), or 0: any number, loaded again (from L1) for every 16 rows.
+//
+// Bound by base and out, so those are accessed by whole rows: 16 lanes x 4 columns, 4 rows at
+// a time, the next 16 rows' base on its way during the current ones'; the sums change places
+// through a wave's own piece of LDS.  BB: bytes of a base element (0: no base).
+//
+// Rows need no alignment (a vector access may start at any element).  The last group of a
+// width that is no multiple of 64 starts at width - 64 and stores its new columns only.
 template <int TY>
-__device__ __forceinline__ void load_b4(const uint16_t* row, int c, int r, bool vec, float (&v)[4]) {
-  if (vec && c + 4 <= r) {
-    const uint2 u = *(const uint2*)(row + c);
-    v[0] = widen<TY>(u.x & 0xffffu);
-    v[1] = widen<TY>(u.x >> 16);
-    v[2] = widen<TY>(u.y & 0xffffu);
-    v[3] = widen<TY>(u.y >> 16);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = c + e < r ? widen<TY>(row[c + e]) : 0.0f;
-  }
+__device__ __forceinline__ void widen4(u32x2 u, float (&v)[4]) {
+  v[0] = widen<TY>(u[0] & 0xffffu);
+  v[1] = widen<TY>(u[0] >> 16);
+  v[2] = widen<TY>(u[1] & 0xffffu);
+  v[3] = widen<TY>(u[1] >> 16);
 }
 
-__device__ __forceinline__ f32x4 load_base4(const void* base, int type, int64_t i, int left, bool vec) {
-  f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-  if (!base || left <= 0) return v;
-  if (vec && left >= 4) {
-    if (type == QMM_F32) return *(const f32x4*)((const float*)base + i);
-    const uint2 u = *(const uint2*)((const uint16_t*)base + i);
-    const uint32_t h[4] = {u.x & 0xffffu, u.x >> 16, u.y & 0xffffu, u.y >> 16};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = type == QMM_F16 ? f16_to_f32((uint16_t)h[e]) : bf16_to_f32((uint16_t)h[e]);
-    return v;
+// Four elements of base as loaded.
+template <int BB>
+__device__ __forceinline__ u32x4 load_base4(const void* base, int64_t i) {
+  u32x4 v = {0u, 0u, 0u, 0u};
+  if constexpr (BB == 4) v = ((const F4*)((const float*)base + i))->v;
+  if constexpr (BB == 2) {
+    const u32x2 u = ((const H4*)((const uint16_t*)base + i))->v;
+    v[0] = u[0];
+    v[1] = u[1];
   }
-#pragma unroll
-  for (int e = 0; e < 4; ++e)
-    if (e < left) v[e] = load_elem_rt(base, type, i + e);
   return v;
 }
 
-__device__ __forceinline__ void store_out4(void* out, int type, int64_t i, int left, bool vec, f32x4 v) {
-  if (left <= 0) return;
-  if (vec && left >= 4) {
-    if (type == QMM_F32) {
-      *(f32x4*)((float*)out + i) = v;
-      return;
-    }
-    uint32_t h[4];
+template <int BB>
+__device__ __forceinline__ f32x4 base_values(u32x4 v, int type) {
+  if constexpr (BB == 4) return __builtin_bit_cast(f32x4, v);
+  if constexpr (BB == 0) return f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  float f[4];
+  const u32x2 u = {v[0], v[1]};
+  if (type == QMM_F16) widen4<QMM_F16>(u, f);
+  else widen4<QMM_BF16>(u, f);
+  return f32x4{f[0], f[1], f[2], f[3]};
+}
+
+// Elements i .. i + 3 of out, those from `from` on.
+__device__ __forceinline__ void store_out4(void* out, int type, int64_t i, int from, f32x4 v) {
+  if (type == QMM_F32) {
+    float* p = (float*)out + i;
+    if (from <= 0) ((F4*)p)->v = __builtin_bit_cast(u32x4, v);
+    else
 #pragma unroll
-    for (int e = 0; e < 4; ++e) h[e] = type == QMM_F16 ? f32_to_f16(v[e]) : f32_to_bf16(v[e]);
-    *(uint2*)((uint16_t*)out + i) = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+      for (int e = 1; e < 4; ++e)
+        if (e >= from) p[e] = v[e];
     return;
   }
+  uint32_t h[4];
 #pragma unroll
-  for (int e = 0; e < 4; ++e)
-    if (e < left) store_elem_rt(out, type, i + e, v[e]);
+  for (int e = 0; e < 4; ++e) h[e] = type == QMM_F16 ? f32_to_f16(v[e]) : f32_to_bf16(v[e]);
+  uint16_t* p = (uint16_t*)out + i;
+  if (from <= 0) ((H4*)p)->v = u32x2{h[0] | (h[1] << 16), h[2] | (h[3] << 16)};
+  else
+#pragma unroll
+    for (int e = 1; e < 4; ++e)
+      if (e >= from) p[e] = (uint16_t)h[e];
 }
 
-// Rows without an adapter: out = base.
-__device__ __forceinline__ void copy_rows(const LoraArgs& p, const Tile& t, const int* rows, int64_t width, int64_t c0,
-                                          int64_t step) {
-  // each wave takes groups of 64 columns from c0 on: 16 lanes a row, 4 rows at a time
-  const int lane = threadIdx.x & 63;
-  const int ln = lane & 15, lg = lane >> 4;
-  for (int64_t c = c0; c < width; c += step)
-    for (int i = lg; i < t.count; i += 4) {
-      const int64_t col = c + 4 * ln;
-      const int64_t at = (int64_t)rows[i] * width + col;
-      const int left = width - col < 4 ? (int)(width - col) : 4;
-      store_out4(p.out, p.out_type, at, left, p.vec_out, load_base4(p.base, p.base_type, at, left, p.vec_out));
+constexpr int kXp = 68;  // floats of a row of 64 columns in the wave's piece of LDS
+
+// The operands of one 16-rank step c of the 64 columns from n0: [part] (forward) or [rank step]
+// (DX), four elements each; zeros past r.
+template <bool DX>
+__device__ __forceinline__ void load_ranks(const uint16_t* Bm, int64_t W, int r, int64_t n0, int c, int ln, int lg,
+                                           u32x2 (&u)[4]) {
+  const int rank = 16 * c + 4 * lg;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    u[k] = u32x2{0u, 0u};
+    if constexpr (DX) {
+      if (rank + k < r) u[k] = ((const H4*)(Bm + (int64_t)(rank + k) * W + n0 + 4 * ln))->v;
+    } else {
+      const uint16_t* q = Bm + (n0 + 16 * k + ln) * r + rank;
+      if (rank + 4 <= r) u[k] = ((const H4*)q)->v;
+      else
+#pragma unroll
+        for (int e = 0; e < 3; ++e)
+          if (rank + e < r) u[k][e / 2] |= (uint32_t)q[e] << (16 * (e & 1));
     }
+  }
 }
 
-template <int TY>
-__global__ __launch_bounds__(LT) void lora_expand_kernel(LoraArgs p) {
+template <int TY, bool DX>
+__device__ __forceinline__ void rank_step(const u32x2 (&u)[4], f32x4 tv, f32x4 (&acc)[4]) {
+  float w[4][4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) widen4<TY>(u[k], w[k]);
+#pragma unroll
+  for (int f = 0; f < 4; ++f)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      acc[f] = __builtin_amdgcn_mfma_f32_16x16x4f32(DX ? w[j][f] : w[f][j], tv[j], acc[f], 0, 0, 0);
+}
+
+// t of the tile (times scale_a) into ts [64][rp + 4]; the forward form keeps it in p.T.
+template <bool DX>
+__device__ __forceinline__ void stage_t(const LoraArgs& p, const float* dT, const Tile& t, const int* rows, float* ts) {
+  const int r = p.r, rp = p.rp, ld = rp + 4;
+  const bool none = t.a == p.L;
+  const bool keep_t = !DX && p.T && blockIdx.y == 0;
+  const float sc = !DX && p.scale && !none ? p.scale[t.a] : 1.0f;
+  if (!none || keep_t)
+    for (int i = threadIdx.x; i < kLoraTile * rp; i += LT) {
+      const int row = i / rp, c = i - row * rp;
+      float v = 0.0f;
+      if (row < t.count && c < r) {
+        if (DX) v = dT[(int64_t)rows[row] * r + c];
+        else if (!none) v = sum_parts(p, p.part + position(p, t, rows, row) * rp + c);
+        if (keep_t) p.T[(int64_t)rows[row] * r + c] = v;
+      }
+      ts[row * ld + c] = v * sc;
+    }
+  __syncthreads();
+}
+
+template <int TY, bool DX, int BB, int NR>
+__global__ __launch_bounds__(LT) void lora_expand_kernel(LoraArgs p, const float* dT) {
   extern __shared__ __attribute__((aligned(16))) float ts[];  // [64][rp + 4]
+  __shared__ __attribute__((aligned(16))) float xp[4][16 * kXp];
   __shared__ int rows[kLoraTile];
   const Tile t = find_tile(p, rows);
   if (t.count == 0) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int ln = lane & 15, lg = lane >> 4;
-  const int64_t N = p.N;
-  const int64_t first = ((int64_t)blockIdx.y * 4 + wave) * 64, step = (int64_t)gridDim.y * 256;
-  if (t.a == p.L) {
-    if (p.T && blockIdx.y == 0)
-      for (int i = threadIdx.x; i < t.count * p.r; i += LT) p.T[(int64_t)rows[i / p.r] * p.r + i % p.r] = 0.0f;
-    copy_rows(p, t, rows, N, first, step);
-    return;
-  }
-  const int rp = p.rp, ld = rp + 4;
-  const float sc = p.scale ? p.scale[t.a] : 1.0f;
-  for (int i = threadIdx.x; i < kLoraTile * rp; i += LT) {
-    const int row = i / rp, c = i - row * rp;
-    float v = 0.0f;
-    if (row < t.count) {
-      const float* q = p.part + position(p, t, rows, row) * rp + c;
-      v = q[0];
-      for (int s = 1; s < p.splits; ++s) v += q[(int64_t)s * p.M * rp];
-      if (p.T && blockIdx.y == 0 && c < p.r) p.T[(int64_t)rows[row] * p.r + c] = v;
-      v *= sc;
+  const int64_t W = DX ? p.K : p.N;  // output columns, at least 64
+  const int r = p.r, ld = p.rp + 4, steps = p.rp / 16;
+  const bool none = t.a == p.L;
+  stage_t<DX>(p, dT, t, rows, ts);
+  const uint16_t* Bm = (const uint16_t*)(DX ? p.A : p.B) + (none ? 0 : t.a * W * r);
+  float* x = xp[wave];
+  for (int64_t g0 = ((int64_t)blockIdx.y * 4 + wave) * 64; g0 < W; g0 += (int64_t)gridDim.y * 256) {
+    const int64_t n0 = g0 + 64 <= W ? g0 : W - 64;
+    const int from = (int)(g0 - n0) - 4 * ln;  // first of this lane's four columns to store
+    auto load_base = [&](int s, u32x4 (&raw)[4]) {  // rows 16 s + 4 i + lane / 16
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = 16 * s + 4 * i + lg;
+        raw[i] = load_base4<BB>(p.base, (int64_t)rows[row < t.count ? row : t.count - 1] * W + n0 + 4 * ln);
+      }
+    };
+    auto finish = [&](int s, const u32x4 (&raw)[4], const f32x4 (&acc)[4]) {
+      if (!none) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const f32x4 d = DX ? f32x4{acc[0][q], acc[1][q], acc[2][q], acc[3][q]} : acc[q];
+          *(f32x4*)(x + ln * kXp + (DX ? 16 * lg + 4 * q : 16 * q + 4 * lg)) = d;
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = 16 * s + 4 * i + lg;
+        f32x4 v = base_values<BB>(raw[i], p.base_type);
+        if (!none) v += *(const f32x4*)(x + (4 * i + lg) * kXp + 4 * ln);
+        if (row < t.count && from < 4) store_out4(p.out, p.out_type, (int64_t)rows[row] * W + n0 + 4 * ln, from, v);
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    };
+    u32x2 keep[NR ? NR : 1][4];
+    if constexpr (NR > 0) {
+      if (!none)
+#pragma unroll
+        for (int c = 0; c < NR; ++c) load_ranks<DX>(Bm, W, r, n0, c, ln, lg, keep[c]);
     }
-    ts[row * ld + c] = v;
-  }
-  __syncthreads();
-  const uint16_t* B = (const uint16_t*)p.B + t.a * N * p.r;
-  const bool vb = p.vec != 0;
-  for (int64_t n0 = first; n0 < N; n0 += step) {
-    f32x4 acc[4][4];  // [16-row part][16-column part]
+    u32x4 raw[2][4];
+    load_base(0, raw[0]);
 #pragma unroll
-    for (int s = 0; s < 4; ++s)
-      if (s * 16 < t.count) {
-        const int64_t row = rows[s * 16 + ln < t.count ? s * 16 + ln : 0];
+    for (int s = 0; s < 4; ++s) {
+      if (s * 16 >= t.count) break;
+      if (s < 3 && (s + 1) * 16 < t.count) load_base(s + 1, raw[(s + 1) & 1]);
+      f32x4 acc[4];
 #pragma unroll
-        for (int f = 0; f < 4; ++f) {
-          const int64_t col = n0 + f * 16 + 4 * lg;
-          const int left = N - col < 4 ? (int)(N - col) : 4;
-          acc[s][f] = load_base4(p.base, p.base_type, row * N + col, left, p.vec_out);
+      for (int f = 0; f < 4; ++f) acc[f] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      if (!none) {
+        const float* trow = ts + (s * 16 + ln) * ld + 4 * lg;
+        if constexpr (NR > 0) {
+#pragma unroll
+          for (int c = 0; c < NR; ++c)
+            if (c < steps) rank_step<TY, DX>(keep[c], *(const f32x4*)(trow + 16 * c), acc);
+        } else {
+          for (int c = 0; c < steps; ++c) {
+            u32x2 u[4];
+            load_ranks<DX>(Bm, W, r, n0, c, ln, lg, u);
+            rank_step<TY, DX>(u, *(const f32x4*)(trow + 16 * c), acc);
+          }
         }
       }
-    for (int c = 0; c < rp; c += 16) {
-      float bv[4][4];
-#pragma unroll
-      for (int f = 0; f < 4; ++f) {
-        const int64_t col = n0 + f * 16 + ln;
-        load_b4<TY>(B + (col < N ? col : N - 1) * p.r, c + 4 * lg, p.r, vb, bv[f]);
-      }
-#pragma unroll
-      for (int s = 0; s < 4; ++s)
-        if (s * 16 < t.count) {
-          const f32x4 tv = *(const f32x4*)(ts + (s * 16 + ln) * ld + c + 4 * lg);
-#pragma unroll
-          for (int f = 0; f < 4; ++f)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              acc[s][f] = __builtin_amdgcn_mfma_f32_16x16x4f32(bv[f][e], tv[e], acc[s][f], 0, 0, 0);
-        }
+      finish(s, raw[s & 1], acc);
     }
-#pragma unroll
-    for (int s = 0; s < 4; ++s)
-      if (s * 16 + ln < t.count) {
-        const int64_t row = rows[s * 16 + ln];
-#pragma unroll
-        for (int f = 0; f < 4; ++f) {
-          const int64_t col = n0 + f * 16 + 4 * lg;
-          const int left = N - col < 4 ? (int)(N - col) : 4;
-          store_out4(p.out, p.out_type, row * N + col, left, p.vec_out, acc[s][f]);
-        }
-      }
   }
 }
 
-// ---- expand of the gradient: out = base + dt A_a (A_a [r][K], ranks down its columns) --
-//
-// As lora_expand_kernel, with 128 columns per wave: lane l loads 8 consecutive columns
-// (8 (l % 16) ..) of rank row 4 s + l / 16 of A, one 16-byte load for eight matrix steps,
-// and column 8 i + f is row i of step f, so a lane ends with 32 consecutive columns of
-// one row (8 per accumulator index).
-template <int TY, bool VEC>
-__global__ __launch_bounds__(LT) void lora_expand_dx_kernel(LoraArgs p, const float* dT) {
-  extern __shared__ __attribute__((aligned(16))) float ts[];  // [64][rp + 1]
+// Outputs narrower than 64 columns: one thread per element, ranks in order.
+template <int TY, bool DX>
+__global__ __launch_bounds__(LT) void lora_expand_narrow_kernel(LoraArgs p, const float* dT) {
+  extern __shared__ __attribute__((aligned(16))) float ts[];
   __shared__ int rows[kLoraTile];
   const Tile t = find_tile(p, rows);
   if (t.count == 0) return;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int ln = lane & 15, lg = lane >> 4;
-  const int64_t K = p.K;
-  if (t.a == p.L) {
-    copy_rows(p, t, rows, K, ((int64_t)blockIdx.y * 4 + wave) * 64, (int64_t)gridDim.y * 256);
-    return;
-  }
-  const int r = p.r, rp = p.rp, ld = rp + 1;
-  for (int i = threadIdx.x; i < kLoraTile * rp; i += LT) {
-    const int row = i / rp, c = i - row * rp;
-    ts[row * ld + c] = row < t.count && c < r ? dT[(int64_t)rows[row] * r + c] : 0.0f;
-  }
-  __syncthreads();
-  const uint16_t* A = (const uint16_t*)p.A + t.a * (int64_t)r * K;
-  for (int64_t k0 = ((int64_t)blockIdx.y * 4 + wave) * 128; k0 < K; k0 += (int64_t)gridDim.y * 512) {
-    // two halves of the tile, so that the sums of 32 rows x 128 columns stay in registers
-    for (int half = 0; half < 2 && half * 32 < t.count; ++half) {
-      f32x4 acc[2][8];
-#pragma unroll
-      for (int s = 0; s < 2; ++s)
-#pragma unroll
-        for (int f = 0; f < 8; ++f) acc[s][f] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-      for (int c = 0; c < r; c += 4) {
-        const int rank = c + lg;
-        uint4 u = make_uint4(0u, 0u, 0u, 0u);
-        if (rank < r) u = load8<VEC>(A + (int64_t)rank * K, k0 + 8 * ln, K);
-        float av[8];
-        widen8<TY>(u, av);
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          const float tv = ts[(half * 32 + s * 16 + ln) * ld + rank];
-#pragma unroll
-          for (int f = 0; f < 8; ++f) acc[s][f] = __builtin_amdgcn_mfma_f32_16x16x4f32(av[f], tv, acc[s][f], 0, 0, 0);
-        }
-      }
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const int i = half * 32 + s * 16 + ln;
-        if (i >= t.count) continue;
-        const int64_t row = rows[i];
-#pragma unroll
-        for (int v = 0; v < 4; ++v)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int64_t col = k0 + 32 * lg + 8 * v + 4 * h;
-            const int left = K - col < 4 ? (int)(K - col) : 4;
-            const f32x4 b = load_base4(p.base, p.base_type, row * K + col, left, p.vec_out);
-            const f32x4 d = {acc[s][4 * h][v], acc[s][4 * h + 1][v], acc[s][4 * h + 2][v], acc[s][4 * h + 3][v]};
-            store_out4(p.out, p.out_type, row * K + col, left, p.vec_out, b + d);
-          }
-      }
-    }
+  const int W = (int)(DX ? p.K : p.N), r = p.r, ld = p.rp + 4;
+  stage_t<DX>(p, dT, t, rows, ts);
+  const bool none = t.a == p.L;
+  const uint16_t* Bm = (const uint16_t*)(DX ? p.A : p.B) + (none ? 0 : t.a * W * r);
+  for (int i = threadIdx.x; i < t.count * W; i += LT) {
+    const int row = i / W, n = i - row * W;
+    const int64_t at = (int64_t)rows[row] * W + n;
+    float v = 0.0f;
+    if (!none)
+      for (int c = 0; c < r; ++c) v = fmaf(ts[row * ld + c], widen<TY>(DX ? Bm[c * W + n] : Bm[n * r + c]), v);
+    if (p.base) v += load_elem_rt(p.base, p.base_type, at);
+    store_elem_rt(p.out, p.out_type, at, v);
   }
 }
 
 // ---- outer sums: dA and dB -----------------------------------------------------------
 //
-// One work-group: 128 columns of Z (blockIdx.y), up to 64 ranks (blockIdx.z) and a chunk of one
-// adapter's rows (slot blockIdx.x of the same numbering as the tiles, with `chunk` rows).
-// The waves take steps of 4 rows in turn: lane l loads 8 consecutive columns of row l / 16
-// (one 16-byte load) and t of rank l % 16, and feeds v_mfma_f32_16x16x4_f32 once per column
-// and 16 ranks.  The waves' sums are added in a fixed order through LDS.  An adapter with
-// one chunk is written at once; the chunks of larger ones go to `part` (slot
-// 2 off / chunk + j) and are added in order by lora_outer_reduce_kernel, which also writes
-// the zeros of adapters without rows.
+// One work-group: 128 columns of X or dY (blockIdx.y runs over both sides), up to 64 ranks
+// (blockIdx.z) and a chunk of one adapter's rows (slot blockIdx.x of the same numbering as
+// the tiles, with `chunk` rows).  The waves take 16 rows in turn, 4 per matrix step: lane l
+// loads 8 consecutive columns of row l / 16 (one 16-byte load, four rows' loads under way at
+// once) and t of rank l % 16, and feeds v_mfma_f32_16x16x4_f32 once per column and 16 ranks.
+// The waves' sums are added in a fixed order through LDS.  An adapter with one chunk is
+// written at once; the chunks of larger ones go to `part` (slot 2 off / chunk + j) and are
+// added in order by lora_outer_reduce_kernel, which also writes the zeros of adapters without
+// rows.
 struct Chunk {
   int64_t a;
   int begin, end;  // positions
@@ -561,42 +635,62 @@ __device__ __forceinline__ Chunk find_chunk(const LoraOuterArgs& p, int64_t slot
   return c;
 }
 
-template <int TY, int NF, bool VEC>
+template <int TY, int NF>
 __global__ __launch_bounds__(LT) void lora_outer_kernel(LoraOuterArgs p) {
   __shared__ __attribute__((aligned(16))) float red[2][8 * NF * 4 * 64];
   const Chunk ch = find_chunk(p, blockIdx.x);
   if (ch.index >= ch.chunks) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int ln = lane & 15, lg = lane >> 4;
-  const int64_t P = p.P, c0 = (int64_t)blockIdx.y * 128;
+  const bool second = (int)blockIdx.y >= p.side[0].blocks;
+  const LoraSide& sd = p.side[second ? 1 : 0];
+  // the last block of a width that is no multiple of 128 starts at width - 128 and stores its
+  // new columns only
+  const int64_t P = sd.P, g0 = (int64_t)(blockIdx.y - (second ? p.side[0].blocks : 0)) * 128;
+  const int64_t c0 = P < 128 || g0 + 128 <= P ? g0 : P - 128;
   const int r = p.r, r0 = (int)blockIdx.z * kLoraRankChunk;
   f32x4 acc[8][NF];
 #pragma unroll
   for (int f = 0; f < 8; ++f)
 #pragma unroll
     for (int q = 0; q < NF; ++q) acc[f][q] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  const uint16_t* Z = (const uint16_t*)p.Z;
-  for (int at = ch.begin + wave * 4; at < ch.end; at += 16) {
-    const int pos = at + lg;
-    uint4 u = make_uint4(0u, 0u, 0u, 0u);
-    float tv[NF];
+  const uint16_t* Z = (const uint16_t*)sd.Z;
+  const float* tt = sd.t;
+  auto step = [&](auto whole_c, int at) {
+    constexpr bool WHOLE = decltype(whole_c)::value;  // 16 rows of 128 columns exist
+    uint4 u[4];
+    float tv[4][NF];
+    int64_t row[4];
 #pragma unroll
-    for (int q = 0; q < NF; ++q) tv[q] = 0.0f;
-    if (pos < ch.end) {
-      const int64_t row = p.plan.perm[pos];
-      u = load8<VEC>(Z + row * P, c0 + 8 * ln, P);
+    for (int k = 0; k < 4; ++k) {
+      const int pos = at + 4 * k + lg;
+      row[k] = p.plan.perm[WHOLE || pos < ch.end ? pos : ch.end - 1];
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const bool in = WHOLE || at + 4 * k + lg < ch.end;
+      u[k] = make_uint4(0u, 0u, 0u, 0u);
+      if (in) u[k] = load8<WHOLE>(Z + row[k] * P, c0 + 8 * ln, P);
 #pragma unroll
       for (int q = 0; q < NF; ++q) {
         const int rank = r0 + q * 16 + ln;
-        if (rank < r) tv[q] = p.t[row * r + rank];
+        tv[k][q] = in && rank < r ? tt[row[k] * r + rank] : 0.0f;
       }
     }
-    float zv[8];
-    widen8<TY>(u, zv);
 #pragma unroll
-    for (int q = 0; q < NF; ++q)
+    for (int k = 0; k < 4; ++k) {
+      float zv[8];
+      widen8<TY>(u[k], zv);
 #pragma unroll
-      for (int f = 0; f < 8; ++f) acc[f][q] = __builtin_amdgcn_mfma_f32_16x16x4f32(zv[f], tv[q], acc[f][q], 0, 0, 0);
+      for (int q = 0; q < NF; ++q)
+#pragma unroll
+        for (int f = 0; f < 8; ++f) acc[f][q] = __builtin_amdgcn_mfma_f32_16x16x4f32(zv[f], tv[k][q], acc[f][q], 0, 0, 0);
+    }
+  };
+  const bool full = c0 + 128 <= P;
+  for (int at = ch.begin + wave * 16; at < ch.end; at += 64) {
+    if (full && at + 16 <= ch.end) step(std::true_type{}, at);
+    else step(std::false_type{}, at);
   }
   // (wave 0 + wave 2) + (wave 1 + wave 3)
   auto put = [&](float* b) {
@@ -625,9 +719,9 @@ __global__ __launch_bounds__(LT) void lora_outer_kernel(LoraOuterArgs p) {
   add(red[0]);
   // accumulator v: column c0 + 8 (4 (lane / 16) + v) + f, rank r0 + 16 q + lane % 16
   const bool direct = ch.chunks == 1;
-  const float sc = direct && p.scale ? p.scale[ch.a] : 1.0f;
+  const float sc = direct && sd.scale ? sd.scale[ch.a] : 1.0f;
   const int64_t slot = 2 * (int64_t)p.plan.off[ch.a] / p.chunk + ch.index;
-  float* part = direct ? nullptr : p.part + slot * P * r;
+  float* part = direct ? nullptr : sd.part + slot * P * r;
 #pragma unroll
   for (int q = 0; q < NF; ++q) {
     const int rank = r0 + q * 16 + ln;
@@ -637,59 +731,88 @@ __global__ __launch_bounds__(LT) void lora_outer_kernel(LoraOuterArgs p) {
 #pragma unroll
       for (int f = 0; f < 8; ++f) {
         const int64_t col = c0 + 8 * (4 * lg + v) + f;
-        if (col >= P) continue;
-        const int64_t i = p.rank_major ? (int64_t)rank * P + col : col * r + rank;
-        if (direct) store_elem_rt(p.out, p.out_type, ch.a * P * r + i, acc[f][q][v] * sc);
+        if (col >= P || col < g0) continue;
+        const int64_t i = sd.rank_major ? (int64_t)rank * P + col : col * r + rank;
+        if (direct) store_elem_rt(sd.out, p.out_type, ch.a * P * r + i, acc[f][q][v] * sc);
         else part[i] = acc[f][q][v];
       }
   }
 }
 
+// Adds the chunks of the adapters with several, eight loads at a time.
 __global__ __launch_bounds__(256) void lora_outer_reduce_kernel(LoraOuterArgs p) {
   const int64_t a = blockIdx.y;
   const int o0 = p.plan.off[a], o1 = p.plan.off[a + 1];
   const int chunks = (o1 - o0 + p.chunk - 1) / p.chunk;
   if (chunks == 1) return;
-  const int64_t total = p.P * p.r;
-  const float sc = p.scale ? p.scale[a] : 1.0f;
-  const float* part = p.part + (2 * (int64_t)o0 / p.chunk) * total;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-    float v = 0.0f;
-    for (int c = 0; c < chunks; ++c) v += part[c * total + i];
-    store_elem_rt(p.out, p.out_type, a * total + i, v * sc);
+  for (int s = 0; s < 2; ++s) {
+    const LoraSide& sd = p.side[s];
+    const int64_t total = sd.blocks ? sd.P * p.r : 0;
+    const float sc = sd.scale ? sd.scale[a] : 1.0f;
+    const float* part = sd.part + (2 * (int64_t)o0 / p.chunk) * total;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+      float v = 0.0f;
+      for (int c = 0; c < chunks; c += 8) {
+        float u[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) u[e] = part[(c + e < chunks ? c + e : chunks - 1) * total + i];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v += c + e < chunks ? u[e] : 0.0f;
+      }
+      store_elem_rt(sd.out, p.out_type, a * total + i, v * sc);
+    }
   }
 }
 
-template <int TY, bool VEC, bool TR>
+template <int TY, bool TR>
 void shrink_nf(const LoraArgs& p, hipStream_t st) {
   const dim3 grid((unsigned)p.slots, (unsigned)p.splits, (unsigned)((p.r + kLoraRankChunk - 1) / kLoraRankChunk));
-  if (p.r <= 16) launch((lora_shrink_kernel<TY, 1, VEC, TR>), grid, dim3(LT), 0, st, p);
-  else if (p.r <= 32) launch((lora_shrink_kernel<TY, 2, VEC, TR>), grid, dim3(LT), 0, st, p);
-  else launch((lora_shrink_kernel<TY, 4, VEC, TR>), grid, dim3(LT), 0, st, p);
+  if (p.r <= 16) launch((lora_shrink_kernel<TY, 1, TR>), grid, dim3(LT), 0, st, p);
+  else if (p.r <= 32) launch((lora_shrink_kernel<TY, 2, TR>), grid, dim3(LT), 0, st, p);
+  else launch((lora_shrink_kernel<TY, 4, TR>), grid, dim3(LT), 0, st, p);
 }
 
-template <bool TR>
-hipError_t shrink(const LoraArgs& p, hipStream_t st) {
-  if (p.type == QMM_F16) p.vec ? shrink_nf<QMM_F16, true, TR>(p, st) : shrink_nf<QMM_F16, false, TR>(p, st);
-  else p.vec ? shrink_nf<QMM_BF16, true, TR>(p, st) : shrink_nf<QMM_BF16, false, TR>(p, st);
-  return hipSuccess;
-}
-
-template <int TY, bool VEC>
+template <int TY>
 void outer_nf(const LoraOuterArgs& p, dim3 grid, hipStream_t st) {
-  if (p.r <= 16) launch((lora_outer_kernel<TY, 1, VEC>), grid, dim3(LT), 0, st, p);
-  else if (p.r <= 32) launch((lora_outer_kernel<TY, 2, VEC>), grid, dim3(LT), 0, st, p);
-  else launch((lora_outer_kernel<TY, 4, VEC>), grid, dim3(LT), 0, st, p);
+  if (p.r <= 16) launch((lora_outer_kernel<TY, 1>), grid, dim3(LT), 0, st, p);
+  else if (p.r <= 32) launch((lora_outer_kernel<TY, 2>), grid, dim3(LT), 0, st, p);
+  else launch((lora_outer_kernel<TY, 4>), grid, dim3(LT), 0, st, p);
 }
 
 // Column slices (gridDim.y) of the expand kernels: about four work-groups per compute
 // unit over all tiles, at most one per 4 waves' columns.
-unsigned column_slices(const LoraArgs& p, int64_t width, int64_t per_wg) {
-  const int64_t most = (width + per_wg - 1) / per_wg;
+unsigned column_slices(const LoraArgs& p, int64_t width) {
+  const int64_t most = (width + 255) / 256;
   const int64_t tiles = p.use_plan ? (p.M + kLoraTile - 1) / kLoraTile : 1;
   int64_t want = (1024 + tiles - 1) / tiles;
   if (want < 1) want = 1;
   return (unsigned)(want < most ? want : most);
+}
+
+template <int TY, bool DX>
+hipError_t expand(const LoraArgs& p, const float* dT, hipStream_t st) {
+  const int64_t W = DX ? p.K : p.N;
+  const uint32_t lds = (uint32_t)(kLoraTile * (p.rp + 4) * 4);
+  const dim3 grid((unsigned)p.slots, W < 64 ? 1u : column_slices(p, W));
+  auto go = [&](auto kern) {
+    if (lds > 32 * 1024) {
+      const hipError_t e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+      if (e != hipSuccess) return e;
+    }
+    launch(kern, grid, dim3(LT), lds, st, p, dT);
+    return hipSuccess;
+  };
+  if (W < 64) return go(lora_expand_narrow_kernel<TY, DX>);
+  auto go_base = [&](auto bb) {
+    constexpr int BB = decltype(bb)::value;
+    if (p.r <= 16) return go(lora_expand_kernel<TY, DX, BB, 1>);
+    if (p.r <= 32) return go(lora_expand_kernel<TY, DX, BB, 2>);
+    if (p.r <= 64) return go(lora_expand_kernel<TY, DX, BB, 4>);
+    return go(lora_expand_kernel<TY, DX, BB, 0>);
+  };
+  if (!p.base) return go_base(std::integral_constant<int, 0>{});
+  if (p.base_type == QMM_F32) return go_base(std::integral_constant<int, 4>{});
+  return go_base(std::integral_constant<int, 2>{});
 }
 
 }  // namespace
@@ -699,8 +822,15 @@ hipError_t launch_lora_plan(const LoraArgs& p, hipStream_t st) {
   return hipSuccess;
 }
 
-hipError_t launch_lora_shrink_x(const LoraArgs& p, hipStream_t st) { return shrink<false>(p, st); }
-hipError_t launch_lora_shrink_dy(const LoraArgs& p, hipStream_t st) { return shrink<true>(p, st); }
+hipError_t launch_lora_shrink_x(const LoraArgs& p, hipStream_t st) {
+  p.type == QMM_F16 ? shrink_nf<QMM_F16, false>(p, st) : shrink_nf<QMM_BF16, false>(p, st);
+  return hipSuccess;
+}
+
+hipError_t launch_lora_shrink_dy(const LoraArgs& p, hipStream_t st) {
+  p.type == QMM_F16 ? shrink_nf<QMM_F16, true>(p, st) : shrink_nf<QMM_BF16, true>(p, st);
+  return hipSuccess;
+}
 
 hipError_t launch_lora_finalize(const LoraArgs& p, bool scaled, float* T, hipStream_t st) {
   launch(lora_finalize_kernel, dim3((unsigned)p.slots), dim3(LT), 0, st, p, scaled ? 1 : 0, T);
@@ -708,39 +838,18 @@ hipError_t launch_lora_finalize(const LoraArgs& p, bool scaled, float* T, hipStr
 }
 
 hipError_t launch_lora_expand(const LoraArgs& p, hipStream_t st) {
-  const dim3 grid((unsigned)p.slots, column_slices(p, p.N, 256));
-  const uint32_t lds = (uint32_t)(kLoraTile * (p.rp + 4) * 4);
-  const void* kern = p.type == QMM_F16 ? (const void*)lora_expand_kernel<QMM_F16> : (const void*)lora_expand_kernel<QMM_BF16>;
-  if (lds > 64 * 1024) {
-    const hipError_t e = hipFuncSetAttribute(kern, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-    if (e != hipSuccess) return e;
-  }
-  if (p.type == QMM_F16) launch(lora_expand_kernel<QMM_F16>, grid, dim3(LT), lds, st, p);
-  else launch(lora_expand_kernel<QMM_BF16>, grid, dim3(LT), lds, st, p);
-  return hipSuccess;
+  return p.type == QMM_F16 ? expand<QMM_F16, false>(p, nullptr, st) : expand<QMM_BF16, false>(p, nullptr, st);
 }
 
 hipError_t launch_lora_expand_dx(const LoraArgs& p, const float* dT, hipStream_t st) {
-  const dim3 grid((unsigned)p.slots, column_slices(p, p.K, 512));
-  const uint32_t lds = (uint32_t)(kLoraTile * (p.rp + 1) * 4);
-  auto go = [&](auto kern) {
-    if (lds > 64 * 1024) {
-      const hipError_t e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-      if (e != hipSuccess) return e;
-    }
-    launch(kern, grid, dim3(LT), lds, st, p, dT);
-    return hipSuccess;
-  };
-  if (p.type == QMM_F16) return p.vec ? go(lora_expand_dx_kernel<QMM_F16, true>) : go(lora_expand_dx_kernel<QMM_F16, false>);
-  return p.vec ? go(lora_expand_dx_kernel<QMM_BF16, true>) : go(lora_expand_dx_kernel<QMM_BF16, false>);
+  return p.type == QMM_F16 ? expand<QMM_F16, true>(p, dT, st) : expand<QMM_BF16, true>(p, dT, st);
 }
 
-int lora_outer_chunk(int64_t M, int64_t P) {
-  // about 1024 work-groups of 128 columns: rows per chunk from the column count, at least
+int lora_outer_chunk(int64_t M, int64_t blocks) {
+  // about 1024 work-groups of 128 columns: rows per chunk from the column blocks, at least
   // 64 (a chunk's sums are written and read once, 8 bytes per element against 2 bytes per
   // row element read)
-  const int64_t blocks = (P + 127) / 128;
-  int64_t c = (M * blocks / 1024 + 15) / 16 * 16;
+  int64_t c = (M * blocks / 1024 + 63) / 64 * 64;
   if (c < 64) c = 64;
   if (c > 4096) c = 4096;
   return (int)c;
@@ -748,13 +857,13 @@ int lora_outer_chunk(int64_t M, int64_t P) {
 
 hipError_t launch_lora_outer(const LoraOuterArgs& p, hipStream_t st) {
   if (p.M > 0) {
-    const dim3 grid((unsigned)(p.M / p.chunk + p.L + 1), (unsigned)((p.P + 127) / 128),
+    const dim3 grid((unsigned)(p.M / p.chunk + p.L + 1), (unsigned)(p.side[0].blocks + p.side[1].blocks),
                     (unsigned)((p.r + kLoraRankChunk - 1) / kLoraRankChunk));
-    if (p.type == QMM_F16) p.vec ? outer_nf<QMM_F16, true>(p, grid, st) : outer_nf<QMM_F16, false>(p, grid, st);
-    else p.vec ? outer_nf<QMM_BF16, true>(p, grid, st) : outer_nf<QMM_BF16, false>(p, grid, st);
+    p.type == QMM_F16 ? outer_nf<QMM_F16>(p, grid, st) : outer_nf<QMM_BF16>(p, grid, st);
   }
-  int64_t bx = (p.P * p.r + 1023) / 1024;
-  if (bx > 256) bx = 256;
+  const int64_t most = (p.side[0].P > p.side[1].P ? p.side[0].P : p.side[1].P) * p.r;
+  int64_t bx = (most + 255) / 256;
+  if (bx > 1024) bx = 1024;
   launch(lora_outer_reduce_kernel, dim3((unsigned)bx, (unsigned)p.L), dim3(256), 0, st, p);
   return hipSuccess;
 }

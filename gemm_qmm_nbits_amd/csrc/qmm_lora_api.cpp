@@ -33,8 +33,11 @@ int splits(int64_t M, int64_t C) {
 }
 
 struct Layout {
-  size_t off = 0, perm = 0, tiles = 0, part = 0, t = 0, dt = 0, outer = 0, total = 0;
+  size_t off = 0, perm = 0, tiles = 0, part = 0, t = 0, dt = 0, db = 0, da = 0, total = 0;
+  int chunk = 0;  // rows per chunk of the outer sums
 };
+
+int col_blocks(int64_t P) { return (int)((P + 127) / 128); }
 
 int64_t tile_slots(int64_t M, int64_t L) { return M / kLoraTile + L + 2; }
 
@@ -58,13 +61,13 @@ Layout layout(int64_t M, int64_t K, int64_t N, int r, int64_t L, bool grad) {
     at += up256((size_t)M * (size_t)r * 4);
     w.dt = at;
     at += up256((size_t)M * (size_t)r * 4);
-    w.outer = at;
-    size_t most = 0;
-    for (const int64_t P : {K, N}) {
-      const int64_t slots = 2 * M / lora_outer_chunk(M, P) + 1;
-      most = std::max(most, (size_t)slots * (size_t)P * (size_t)r * 4);
-    }
-    at += up256(most);
+    // partial outer sums of both sides (a function of the shape, whatever is asked for)
+    w.chunk = lora_outer_chunk(M, col_blocks(K) + col_blocks(N));
+    const size_t slots = (size_t)(2 * M / w.chunk + 1);
+    w.db = at;
+    at += up256(slots * (size_t)N * (size_t)r * 4);
+    w.da = at;
+    at += up256(slots * (size_t)K * (size_t)r * 4);
   }
   w.total = at;
   return w;
@@ -145,11 +148,6 @@ void set_split(LoraArgs& p, int64_t C) {
   p.splits = splits(p.M, C);
 }
 
-// 4-element accesses of rows of `width` elements at base and out
-int vector_rows(int64_t width, const void* base, int base_type, const void* out, int out_type) {
-  return width % 4 == 0 && aligned(out, 4 * type_size(out_type)) && (!base || aligned(base, 4 * type_size(base_type)));
-}
-
 }  // namespace
 
 extern "C" {
@@ -197,11 +195,8 @@ qmm_status qmm_lora_add(const void* X, int type, int64_t M, int64_t K, int64_t N
   p.out_type = y_type;
   p.T = T;
   set_split(p, K);
-  p.vec = K % 8 == 0 && aligned(X, 16) && aligned(w.A, 16);
   hipError_t e = p.use_plan ? launch_lora_plan(p, st) : hipSuccess;
   if (e == hipSuccess) e = launch_lora_shrink_x(p, st);
-  p.vec = r % 4 == 0 && aligned(w.B, 8);
-  p.vec_out = vector_rows(N, base, base_type, Y, y_type);
   if (e == hipSuccess) e = launch_lora_expand(p, st);
   if (e != hipSuccess) return (qmm_status)e;
   return (qmm_status)hipGetLastError();
@@ -226,45 +221,26 @@ qmm_status qmm_lora_grad(const void* dY, const void* X, int type, int64_t M, int
   if (M > 0 && dB && !T) {  // T was not kept: X A^T again
     p.X = X;
     set_split(p, K);
-    p.vec = K % 8 == 0 && aligned(X, 16) && aligned(w.A, 16);
     if (e == hipSuccess) e = launch_lora_shrink_x(p, st);
     if (e == hipSuccess) e = launch_lora_finalize(p, false, t, st);
   }
   if (M > 0 && (dX || dA)) {
     p.dY = dY;
     set_split(p, N);
-    p.vec = N % 8 == 0 && r % 8 == 0 && aligned(dY, 16) && aligned(w.B, 16);
     if (e == hipSuccess) e = launch_lora_shrink_dy(p, st);
     if (e == hipSuccess) e = launch_lora_finalize(p, true, dt, st);
   }
-  LoraOuterArgs o{};
-  o.type = type;
-  o.r = r;
-  o.M = M;
-  o.L = L;
-  o.plan = p.plan;
-  o.out_type = g_type;
-  o.part = (float*)(ws + l.outer);
-  if (dB) {
-    o.Z = dY;
-    o.P = N;
-    o.t = T ? T : t;
-    o.scale = w.scale;
-    o.out = dB;
-    o.rank_major = 0;
-    o.chunk = lora_outer_chunk(M, N);
-    o.vec = N % 8 == 0 && aligned(dY, 16);
-    if (e == hipSuccess) e = launch_lora_outer(o, st);
-  }
-  if (dA) {
-    o.Z = X;
-    o.P = K;
-    o.t = dt;
-    o.scale = nullptr;  // dt holds it
-    o.out = dA;
-    o.rank_major = 1;
-    o.chunk = lora_outer_chunk(M, K);
-    o.vec = K % 8 == 0 && aligned(X, 16);
+  if (dA || dB) {
+    LoraOuterArgs o{};
+    o.type = type;
+    o.r = r;
+    o.M = M;
+    o.L = L;
+    o.plan = p.plan;
+    o.out_type = g_type;
+    o.chunk = l.chunk;
+    if (dB) o.side[0] = {dY, N, T ? T : t, w.scale, dB, 0, col_blocks(N), (float*)(ws + l.db)};
+    if (dA) o.side[1] = {X, K, dt, nullptr, dA, 1, col_blocks(K), (float*)(ws + l.da)};  // dt holds the scale
     if (e == hipSuccess) e = launch_lora_outer(o, st);
   }
   if (dX && M > 0) {
@@ -272,8 +248,6 @@ qmm_status qmm_lora_grad(const void* dY, const void* X, int type, int64_t M, int
     p.base_type = base_type;
     p.out = dX;
     p.out_type = dx_type;
-    p.vec = K % 8 == 0 && aligned(w.A, 16);
-    p.vec_out = vector_rows(K, base, base_type, dX, dx_type);
     if (e == hipSuccess) e = launch_lora_expand_dx(p, dt, st);
   }
   if (e != hipSuccess) return (qmm_status)e;
