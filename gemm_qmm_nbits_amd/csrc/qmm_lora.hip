@@ -550,12 +550,7 @@ __global__ __launch_bounds__(LT) void lora_expand_kernel(LoraArgs p, const float
 #pragma unroll
         for (int c = 0; c < NR; ++c) load_ranks<DX>(Bm, W, r, n0, c, ln, lg, keep[c]);
     }
-    u32x4 raw[2][4];
-    load_base(0, raw[0]);
-#pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      if (s * 16 >= t.count) break;
-      if (s < 3 && (s + 1) * 16 < t.count) load_base(s + 1, raw[(s + 1) & 1]);
+    auto part = [&](int s, const u32x4 (&raw)[4]) {  // rows 16 s ..
       f32x4 acc[4];
 #pragma unroll
       for (int f = 0; f < 4; ++f) acc[f] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -573,7 +568,19 @@ __global__ __launch_bounds__(LT) void lora_expand_kernel(LoraArgs p, const float
           }
         }
       }
-      finish(s, raw[s & 1], acc);
+      finish(s, raw, acc);
+    };
+    u32x4 even[4], odd[4];
+    load_base(0, even);
+    // not unrolled: the rows' addresses of four parts would take the registers of two waves
+#pragma unroll 1
+    for (int s = 0; s * 16 < t.count; s += 2) {
+      const bool more = (s + 1) * 16 < t.count;
+      if (more) load_base(s + 1, odd);
+      part(s, even);
+      if (!more) break;
+      if ((s + 2) * 16 < t.count) load_base(s + 2, even);
+      part(s + 1, odd);
     }
   }
 }
@@ -636,7 +643,7 @@ __device__ __forceinline__ Chunk find_chunk(const LoraOuterArgs& p, int64_t slot
 }
 
 template <int TY, int NF>
-__global__ __launch_bounds__(LT) void lora_outer_kernel(LoraOuterArgs p) {
+__global__ __launch_bounds__(LT, NF == 1 ? 4 : NF == 2 ? 3 : 2) void lora_outer_kernel(LoraOuterArgs p) {
   __shared__ __attribute__((aligned(16))) float red[2][8 * NF * 4 * 64];
   const Chunk ch = find_chunk(p, blockIdx.x);
   if (ch.index >= ch.chunks) return;

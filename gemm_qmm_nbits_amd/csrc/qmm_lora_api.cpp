@@ -18,12 +18,12 @@ size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 bool valid_type(int t) { return t == QMM_F32 || t == QMM_F16 || t == QMM_BF16; }
 size_t type_size(int t) { return t == QMM_F32 ? 4 : 2; }
 
-// Splits of a contraction of C elements: enough work-groups (about 512 over the tiles) to
+// Splits of a contraction of C elements: enough work-groups (about 1024 over the tiles) to
 // cover the chip, at least 256 elements each (one step per wave), at most 32.  A function
 // of the shape only, so the summation order never depends on the device.
 int64_t split_len(int64_t M, int64_t C) {
   const int64_t tiles = M <= kLoraInlineRows ? 1 : (M + kLoraTile - 1) / kLoraTile;
-  int64_t s = std::min<int64_t>((512 + tiles - 1) / tiles, 32);
+  int64_t s = std::min<int64_t>((1024 + tiles - 1) / tiles, 32);
   s = std::max<int64_t>(1, std::min(s, (C + 255) / 256));
   return ((C + s - 1) / s + 255) / 256 * 256;
 }

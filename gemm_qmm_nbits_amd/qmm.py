@@ -8,6 +8,7 @@ missing the binding raises: there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from ctypes import POINTER, Structure, c_double, c_float, c_int, c_int64, c_size_t, c_void_p
 
@@ -483,50 +484,108 @@ def qswiglu(gate, up, qparams, bits, out=None, stream=None):
 
 
 # ---------------------------------------------------------------------------
+# checks of the training and adapter operators' tensors (a decode step makes hundreds of these
+# calls, so each check is one attribute read)
+# ---------------------------------------------------------------------------
+
+class _Types:
+    """torch, its dtypes by element-type code, and the current stream's handle."""
+
+    def __init__(self):
+        torch = _torch()
+        self.torch = torch
+        self.any = {torch.float32: QMM_F32, torch.float16: QMM_F16, torch.bfloat16: QMM_BF16}
+        self.half = {torch.float16: QMM_F16, torch.bfloat16: QMM_BF16}
+        self.only = {d: {d: c} for d, c in self.any.items()}
+        self.f32 = self.only[torch.float32]
+        self.i32 = {torch.int32: 0}
+        self.u8 = {torch.uint8: 0}
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        self.current = raw or (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
+_types_cache = None
+
+
+def _types() -> _Types:
+    global _types_cache
+    if _types_cache is None:
+        _types_cache = _Types()
+    return _types_cache
+
+
+def _expect(t, name, shape, codes, dev):
+    """Checks a dense tensor of the given shape on device index `dev`; its element-type code."""
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    code = codes.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be one of {list(codes)}, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on the device of the call")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return code
+
+
+def _optional(t, name, shape, codes, dev):
+    """_expect of a tensor that may be None: its address (or None) and element-type code."""
+    if t is None:
+        return None, QMM_F32
+    code = _expect(t, name, shape, codes, dev)
+    return t.data_ptr(), code
+
+
+def _device_of(t):
+    """Index of the tensor's device, which has to be the current one (kernels launch there)."""
+    dev = t.get_device()
+    if dev < 0 or dev != _types().torch.cuda.current_device():
+        raise ValueError("the tensors must be on the current device (torch.cuda.set_device)")
+    return dev
+
+
+def _handle(stream, dev):
+    return _types().current(dev) if stream is None else stream.cuda_stream
+
+
+def _scratch(workspace, need, like):
+    """Address and size of the workspace, allocated here when not given."""
+    if workspace is None:
+        workspace = _types().torch.empty(need, dtype=_types().torch.uint8, device=like.device)
+        return workspace, workspace.data_ptr(), need
+    if not workspace.is_contiguous() or workspace.get_device() != like.get_device():
+        raise ValueError("workspace must be contiguous and on the device of the call")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+@functools.lru_cache(maxsize=4096)
+def _bytes_of(query, *sizes):
+    """Workspace bytes of a shape (a pure function of the sizes)."""
+    return max(1, getattr(lib(), query)(*sizes))
+
+
+# ---------------------------------------------------------------------------
 # low-rank adapters
 # ---------------------------------------------------------------------------
 
-def _expect(t, name, shape, dtypes, like=None):
-    """A dense device tensor of the given shape and one of the dtypes, on like's device."""
-    if t is None:
-        return None
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name} must be one of {dtypes}, got {t.dtype}")
-    if not t.is_cuda or (like is not None and t.device != like.device):
-        raise ValueError(f"{name} must be on the device of the call")
-    return _contig(t, name)
-
-
-def _on_current_device(t):
-    """Kernels are launched on the current device: the tensors have to be there."""
-    torch = _torch()
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
-        raise ValueError("the tensors must be on the current device (torch.cuda.set_device)")
-
-
-def _workspace(workspace, need, like):
-    torch = _torch()
-    if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=like.device)
-    return workspace, workspace.numel() * workspace.element_size()
-
-
 def _lora_shapes(X, A, B, ids, scale):
-    torch = _torch()
-    if X.dim() != 2 or A.dim() != 3:
-        raise ValueError("rows must be [M, K] and A [L, r, K]")
-    if X.dtype not in (torch.float16, torch.bfloat16):
+    ty = _types()
+    if X.dim() != 2 or A.dim() != 3 or B.dim() != 3:
+        raise ValueError("rows must be [M, K], A [L, r, K] and B [L, N, r]")
+    code = ty.half.get(X.dtype)
+    if code is None:
         raise TypeError(f"unsupported dtype {X.dtype}")
-    M, (L, r, K) = X.shape[0], A.shape
-    N = B.shape[1] if B.dim() == 3 else -1
-    _on_current_device(X)
-    _expect(A, "A", (L, r, K), (X.dtype,), X)
-    _expect(B, "B", (L, N, r), (X.dtype,), X)
-    _expect(ids, "ids", (M,), (torch.int32,), X)
-    _expect(scale, "scale", (L,), (torch.float32,), X)
-    return M, K, N, r, L
+    dev = _device_of(X)
+    M = X.shape[0]
+    L, r, K = A.shape
+    N = B.shape[1]
+    same = ty.only[X.dtype]
+    _expect(X, "X", (M, K), same, dev)
+    _expect(A, "A", (L, r, K), same, dev)
+    _expect(B, "B", (L, N, r), same, dev)
+    _expect(ids, "ids", (M,), ty.i32, dev)
+    s, _ = _optional(scale, "scale", (L,), ty.f32, dev)
+    return ty, dev, code, M, K, N, r, L, qmm_lora_weights(A.data_ptr(), B.data_ptr(), s)
 
 
 def qmm_lora_add(X, A, B, ids, scale=None, base=None, out=None, out_dtype=None, T=None, workspace=None,
@@ -535,20 +594,15 @@ def qmm_lora_add(X, A, B, ids, scale=None, base=None, out=None, out_dtype=None, 
 
     X [M, K], A [L, r, K], B [L, N, r] fp16 or bf16; ids int32 [M]; scale fp32 [L]; base [M, N],
     for instance the fp32 output of qmm_nbits.  T (fp32 [M, r]) receives A[a] X[m] for qmm_lora_grad."""
-    torch = _torch()
-    M, K, N, r, L = _lora_shapes(X, A, B, ids, scale)
-    any_type = (torch.float32, torch.float16, torch.bfloat16)
-    _expect(X, "X", (M, K), (A.dtype,))
-    _expect(base, "base", (M, N), any_type, X)
-    _expect(T, "T", (M, r), (torch.float32,), X)
+    ty, dev, code, M, K, N, r, L, w = _lora_shapes(X, A, B, ids, scale)
+    base_p, base_t = _optional(base, "base", (M, N), ty.any, dev)
+    T_p, _ = _optional(T, "T", (M, r), ty.f32, dev)
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype or X.dtype, device=X.device)
-    _expect(out, "out", (M, N), any_type, X)
-    workspace, wsb = _workspace(workspace, lib().qmm_lora_add_workspace_bytes(M, K, N, r, L), X)
-    w = qmm_lora_weights(A.data_ptr(), B.data_ptr(), None if scale is None else scale.data_ptr())
-    st = lib().qmm_lora_add(_ptr(X), dtype_code(X), M, K, N, r, L, _ptr(ids), w, _ptr(base),
-                            QMM_F32 if base is None else dtype_code(base), _ptr(out), dtype_code(out), _ptr(T),
-                            _ptr(workspace), wsb, _stream(stream))
+        out = ty.torch.empty((M, N), dtype=out_dtype or X.dtype, device=X.device)
+    out_t = _expect(out, "out", (M, N), ty.any, dev)
+    keep, ws, wsb = _scratch(workspace, _bytes_of("qmm_lora_add_workspace_bytes", M, K, N, r, L), X)
+    st = lib().qmm_lora_add(X.data_ptr(), code, M, K, N, r, L, ids.data_ptr(), w, base_p, base_t, out.data_ptr(),
+                            out_t, T_p, ws, wsb, _handle(stream, dev))
     _check("qmm_lora_add", st)
     return out
 
@@ -560,31 +614,25 @@ def qmm_lora_grad(dY, X, A, B, ids, scale=None, T=None, base=None, dX=None, dA=N
     dX[m] = base[m] + A[a]^T dT[m] with dT[m] = scale[a] B[a]^T dY[m]; dA[a] = sum dT[m] X[m]^T;
     dB[a] = scale[a] sum dY[m] T[m]^T.  T: kept from qmm_lora_add, or None (computed again).
     dX is of dx_dtype (default X's), dA and dB of grad_dtype (default fp32)."""
-    torch = _torch()
-    M, K, N, r, L = _lora_shapes(X, A, B, ids, scale)
-    any_type = (torch.float32, torch.float16, torch.bfloat16)
-    _expect(X, "X", (M, K), (A.dtype,))
-    _expect(dY, "dY", (M, N), (X.dtype,), X)
-    _expect(T, "T", (M, r), (torch.float32,), X)
-    _expect(base, "base", (M, K), any_type, X)
-
-    def output(t, wanted, name, shape, dtype):
-        if t is None and wanted:
-            t = torch.empty(shape, dtype=dtype, device=X.device)
-        return _expect(t, name, shape, any_type, X)
-
-    dX = output(dX, need[0], "dX", (M, K), dx_dtype or X.dtype)
-    dA = output(dA, need[1], "dA", (L, r, K), grad_dtype or torch.float32)
-    dB = output(dB, need[2], "dB", (L, N, r), grad_dtype or torch.float32)
-    if dA is not None and dB is not None and dA.dtype != dB.dtype:
+    ty, dev, code, M, K, N, r, L, w = _lora_shapes(X, A, B, ids, scale)
+    empty = ty.torch.empty
+    _expect(dY, "dY", (M, N), ty.only[X.dtype], dev)
+    T_p, _ = _optional(T, "T", (M, r), ty.f32, dev)
+    base_p, base_t = _optional(base, "base", (M, K), ty.any, dev)
+    if dX is None and need[0]:
+        dX = empty((M, K), dtype=dx_dtype or X.dtype, device=X.device)
+    if dA is None and need[1]:
+        dA = empty((L, r, K), dtype=grad_dtype or ty.torch.float32, device=X.device)
+    if dB is None and need[2]:
+        dB = empty((L, N, r), dtype=grad_dtype or ty.torch.float32, device=X.device)
+    dX_p, dX_t = _optional(dX, "dX", (M, K), ty.any, dev)
+    dA_p, dA_t = _optional(dA, "dA", (L, r, K), ty.any, dev)
+    dB_p, dB_t = _optional(dB, "dB", (L, N, r), ty.any, dev)
+    if dA is not None and dB is not None and dA_t != dB_t:
         raise TypeError("dA and dB differ in dtype")
-    g = dA if dA is not None else dB
-    workspace, wsb = _workspace(workspace, lib().qmm_lora_grad_workspace_bytes(M, K, N, r, L), X)
-    w = qmm_lora_weights(A.data_ptr(), B.data_ptr(), None if scale is None else scale.data_ptr())
-    st = lib().qmm_lora_grad(_ptr(dY), _ptr(X), dtype_code(X), M, K, N, r, L, _ptr(ids), w, _ptr(T), _ptr(base),
-                             QMM_F32 if base is None else dtype_code(base), _ptr(dX),
-                             QMM_F32 if dX is None else dtype_code(dX), _ptr(dA), _ptr(dB),
-                             QMM_F32 if g is None else dtype_code(g), _ptr(workspace), wsb, _stream(stream))
+    keep, ws, wsb = _scratch(workspace, _bytes_of("qmm_lora_grad_workspace_bytes", M, K, N, r, L), X)
+    st = lib().qmm_lora_grad(dY.data_ptr(), X.data_ptr(), code, M, K, N, r, L, ids.data_ptr(), w, T_p, base_p, base_t,
+                             dX_p, dX_t, dA_p, dB_p, dB_t if dA is None else dA_t, ws, wsb, _handle(stream, dev))
     _check("qmm_lora_grad", st)
     return dX, dA, dB
 
@@ -594,55 +642,54 @@ def qmm_lora_grad(dY, X, A, B, ids, scale=None, T=None, base=None, dX=None, dA=N
 # ---------------------------------------------------------------------------
 
 def _dgrad_shapes(dY, W, K, block, bits, out, out_dtype):
-    """Checks dY [M, N] and the packed weights W [N, nblk, block * bits / 8]; returns M, N, out."""
-    torch = _torch()
-    any_type = (torch.float32, torch.float16, torch.bfloat16)
+    """Checks dY [M, N] and the packed weights W [N, nblk, block * bits / 8]."""
+    ty = _types()
     if dY.dim() != 2:
         raise ValueError("dY must be [M, N]")
     M, N = dY.shape
-    _on_current_device(dY)
-    _expect(dY, "dY", (M, N), any_type)
+    dev = _device_of(dY)
+    code = _expect(dY, "dY", (M, N), ty.any, dev)
     if W.shape[0] != N or W.numel() != N * nblocks(K, block) * (block * bits // 8):
         raise ValueError(f"W does not hold {N} rows of {K} codes of {bits} bits in blocks of {block}")
-    _expect(W, "W", W.shape, (torch.uint8,), dY)
+    _expect(W, "W", W.shape, ty.u8, dev)
     if out is None:
-        out = torch.empty((M, K), dtype=out_dtype or dY.dtype, device=dY.device)
-    return M, N, _expect(out, "out", (M, K), any_type, dY)
+        out = ty.torch.empty((M, K), dtype=out_dtype or dY.dtype, device=dY.device)
+    return dev, code, M, N, out, _expect(out, "out", (M, K), ty.any, dev)
 
 
-def _sized(t, name, count, like):
-    """A dense tensor of at least `count` elements on like's device."""
+def _sized(t, name, count, dev):
+    """Address of a dense tensor of at least `count` elements on device `dev`."""
     if t.numel() < count:
         raise ValueError(f"{name} must hold {count} elements, got {t.numel()}")
-    if t.device != like.device:
+    if t.get_device() != dev:
         raise ValueError(f"{name} must be on the device of the call")
-    return _contig(t, name)
+    return _contig(t, name).data_ptr()
 
 
 def qmm_nbits_dgrad(dY, W, scales, K, bits, block, zp=None, zp_kind=QMM_ZP_NONE, uniform_zp=0.0, out=None,
                     out_dtype=None, workspace=None, stream=None):
     """dX[M, K] = dY[M, N] . dequant(W): the input gradient of qmm_nbits, from the same weight buffers."""
-    M, N, out = _dgrad_shapes(dY, W, K, block, bits, out, out_dtype)
+    dev, code, M, N, out, out_t = _dgrad_shapes(dY, W, K, block, bits, out, out_dtype)
     nblk = nblocks(K, block)
-    _sized(scales, "scales", N * nblk, dY)
+    s_p = _sized(scales, "scales", N * nblk, dev)
+    z_p = None
     if zp is not None and zp_kind in (QMM_ZP_PACKED, QMM_ZP_F16):
-        _sized(zp, "zp", N * ((nblk * bits + 7) // 8 if zp_kind == QMM_ZP_PACKED else nblk), dY)
-    workspace, wsb = _workspace(workspace, lib().qmm_dgrad_workspace_bytes(M, K, N), dY)
-    st = lib().qmm_nbits_dgrad(_ptr(dY), dtype_code(dY), M, K, N, _ptr(W), bits, block, _ptr(scales), _ptr(zp),
-                               zp_kind, float(uniform_zp), _ptr(out), dtype_code(out), _ptr(workspace), wsb,
-                               _stream(stream))
+        z_p = _sized(zp, "zp", N * ((nblk * bits + 7) // 8 if zp_kind == QMM_ZP_PACKED else nblk), dev)
+    keep, ws, wsb = _scratch(workspace, _bytes_of("qmm_dgrad_workspace_bytes", M, K, N), dY)
+    st = lib().qmm_nbits_dgrad(dY.data_ptr(), code, M, K, N, W.data_ptr(), bits, block, s_p, z_p, zp_kind,
+                               float(uniform_zp), out.data_ptr(), out_t, ws, wsb, _handle(stream, dev))
     _check("qmm_nbits_dgrad", st)
     return out
 
 
 def qmm_codebook4_dgrad(dY, W, absmax, codebook, K, block=64, out=None, out_dtype=None, workspace=None, stream=None):
     """dX[M, K] = dY[M, N] . (codebook[q] * absmax): the input gradient of qmm_codebook4."""
-    M, N, out = _dgrad_shapes(dY, W, K, block, 4, out, out_dtype)
-    _sized(absmax, "absmax", N * nblocks(K, block), dY)
-    _sized(codebook, "codebook", 16, dY)
-    workspace, wsb = _workspace(workspace, lib().qmm_dgrad_workspace_bytes(M, K, N), dY)
-    st = lib().qmm_codebook4_dgrad(_ptr(dY), dtype_code(dY), M, K, N, _ptr(W), block, _ptr(absmax), _ptr(codebook),
-                                   _ptr(out), dtype_code(out), _ptr(workspace), wsb, _stream(stream))
+    dev, code, M, N, out, out_t = _dgrad_shapes(dY, W, K, block, 4, out, out_dtype)
+    a_p = _sized(absmax, "absmax", N * nblocks(K, block), dev)
+    c_p = _sized(codebook, "codebook", 16, dev)
+    keep, ws, wsb = _scratch(workspace, _bytes_of("qmm_dgrad_workspace_bytes", M, K, N), dY)
+    st = lib().qmm_codebook4_dgrad(dY.data_ptr(), code, M, K, N, W.data_ptr(), block, a_p, c_p, out.data_ptr(), out_t,
+                                   ws, wsb, _handle(stream, dev))
     _check("qmm_codebook4_dgrad", st)
     return out
 
@@ -652,31 +699,33 @@ def qmm_codebook4_dgrad(dY, W, absmax, codebook, K, block=64, out=None, out_dtyp
 # ---------------------------------------------------------------------------
 
 def _grouped_shapes(X, W, row_offsets):
-    torch = _torch()
+    ty = _types()
     if X.dim() != 2 or W.dim() != 3:
         raise ValueError("rows must be [R, K] and W [E, N, K]")
-    if X.dtype not in (torch.float16, torch.bfloat16):
+    code = ty.half.get(X.dtype)
+    if code is None:
         raise TypeError(f"unsupported dtype {X.dtype}")
-    R, (E, N, K) = X.shape[0], W.shape
-    _on_current_device(X)
-    _expect(X, "X", (R, K), (X.dtype,))
-    _expect(W, "W", (E, N, K), (X.dtype,), X)
-    _expect(row_offsets, "row_offsets", (E + 1,), (torch.int32,), X)
-    return R, K, N, E
+    dev = _device_of(X)
+    R = X.shape[0]
+    E, N, K = W.shape
+    same = ty.only[X.dtype]
+    _expect(X, "X", (R, K), same, dev)
+    _expect(W, "W", (E, N, K), same, dev)
+    _expect(row_offsets, "row_offsets", (E + 1,), ty.i32, dev)
+    return ty, dev, code, R, K, N, E
 
 
 def qmoe_grouped_mm(X, row_offsets, W, bias=None, out=None, out_dtype=None, stream=None):
     """Y[r] = X[r] W[e]^T (+ bias[e]) for the rows row_offsets[e] .. row_offsets[e+1] of expert e.
 
     X [R, K], W [E, N, K] fp16 or bf16; bias [E, N] of the output's dtype (default X's)."""
-    torch = _torch()
-    R, K, N, E = _grouped_shapes(X, W, row_offsets)
+    ty, dev, code, R, K, N, E = _grouped_shapes(X, W, row_offsets)
     if out is None:
-        out = torch.empty((R, N), dtype=out_dtype or X.dtype, device=X.device)
-    _expect(out, "out", (R, N), (torch.float32, torch.float16, torch.bfloat16), X)
-    _expect(bias, "bias", (E, N), (out.dtype,), X)
-    st = lib().qmoe_grouped_mm(_ptr(X), dtype_code(X), R, K, N, E, _ptr(row_offsets), _ptr(W), _ptr(bias), _ptr(out),
-                               dtype_code(out), _stream(stream))
+        out = ty.torch.empty((R, N), dtype=out_dtype or X.dtype, device=X.device)
+    out_t = _expect(out, "out", (R, N), ty.any, dev)
+    b_p, _ = _optional(bias, "bias", (E, N), ty.only[out.dtype], dev)
+    st = lib().qmoe_grouped_mm(X.data_ptr(), code, R, K, N, E, row_offsets.data_ptr(), W.data_ptr(), b_p,
+                               out.data_ptr(), out_t, _handle(stream, dev))
     _check("qmoe_grouped_mm", st)
     return out
 
@@ -687,25 +736,23 @@ def qmoe_grouped_mm_grad(dY, X, row_offsets, W, dX=None, dW=None, dbias=None, dx
 
     dX[r] = dY[r] W[e] of dx_dtype (default X's); dW[e] = sum dY[r]^T X[r] and dbias[e] = sum dY[r]
     over the rows of expert e, of dw_dtype (default X's)."""
-    torch = _torch()
-    R, K, N, E = _grouped_shapes(X, W, row_offsets)
-    any_type = (torch.float32, torch.float16, torch.bfloat16)
-    _expect(dY, "dY", (R, N), (X.dtype,), X)
-
-    def output(t, wanted, name, shape, dtype):
-        if t is None and wanted:
-            t = torch.empty(shape, dtype=dtype, device=X.device)
-        return _expect(t, name, shape, any_type, X)
-
-    dX = output(dX, need[0], "dX", (R, K), dx_dtype or X.dtype)
-    dW = output(dW, need[1], "dW", (E, N, K), dw_dtype or X.dtype)
-    dbias = output(dbias, need_dbias, "dbias", (E, N), dw_dtype or (X.dtype if dW is None else dW.dtype))
-    if dW is not None and dbias is not None and dW.dtype != dbias.dtype:
+    ty, dev, code, R, K, N, E = _grouped_shapes(X, W, row_offsets)
+    empty = ty.torch.empty
+    _expect(dY, "dY", (R, N), ty.only[X.dtype], dev)
+    if dX is None and need[0]:
+        dX = empty((R, K), dtype=dx_dtype or X.dtype, device=X.device)
+    if dW is None and need[1]:
+        dW = empty((E, N, K), dtype=dw_dtype or X.dtype, device=X.device)
+    if dbias is None and need_dbias:
+        dbias = empty((E, N), dtype=dw_dtype or (X.dtype if dW is None else dW.dtype), device=X.device)
+    dX_p, dX_t = _optional(dX, "dX", (R, K), ty.any, dev)
+    dW_p, dW_t = _optional(dW, "dW", (E, N, K), ty.any, dev)
+    db_p, db_t = _optional(dbias, "dbias", (E, N), ty.any, dev)
+    if dW is not None and dbias is not None and dW_t != db_t:
         raise TypeError("dW and dbias differ in dtype")
-    g = dW if dW is not None else dbias
-    st = lib().qmoe_grouped_mm_grad(_ptr(dY), _ptr(X), dtype_code(X), R, K, N, E, _ptr(row_offsets), _ptr(W),
-                                    _ptr(dX), QMM_F32 if dX is None else dtype_code(dX), _ptr(dW), _ptr(dbias),
-                                    QMM_F32 if g is None else dtype_code(g), _stream(stream))
+    st = lib().qmoe_grouped_mm_grad(dY.data_ptr(), X.data_ptr(), code, R, K, N, E, row_offsets.data_ptr(),
+                                    W.data_ptr(), dX_p, dX_t, dW_p, db_p, db_t if dW is None else dW_t,
+                                    _handle(stream, dev))
     _check("qmoe_grouped_mm_grad", st)
     return dX, dW, dbias
 
