@@ -40,6 +40,7 @@ struct LoraArgs {
   LoraPlan plan;
   int use_plan;        // 0: the kernels group the rows (M <= kLoraInlineRows)
   int slots;           // tile slots (grid)
+  int slices;          // column slices of the expand kernels (set by their launch)
   float* part;         // fp32 partial products [splits][M][rp], by position
   int splits;
   int64_t split_len;   // contraction elements per split (a multiple of 256)
