@@ -28,6 +28,8 @@ namespace qmm {
 
 namespace {
 
+constexpr int kStage = 32;  // rows of W per stage
+
 // The 16 codes of one thread and stage, with their scale and zero point.
 template <int BITS>
 struct Codes {
@@ -95,11 +97,11 @@ __global__ __launch_bounds__(WM* WN * 64) void dgrad_kernel(DgradArgs p) {
     __syncthreads();
   }
 
-  TileLoad<BM, NW, false, true> la;
+  TileLoad<BM, NW, kStage, false, true> la;
   la.init(p.dY16 + m0 * p.lda, p.lda, p.M - m0, p.n16, wave, lane);
   const int wm = wave / WN, wn = wave % WN;
-  TileRead<BM, false> ra;
-  TileRead<BN, true> rb;
+  TileRead<BM, kStage, false> ra;
+  TileRead<BN, kStage, true> rb;
   ra.init(wm * FM * 32, lane);
   rb.init(wn * FN * 32, lane);
 

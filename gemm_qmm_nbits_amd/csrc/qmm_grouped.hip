@@ -6,9 +6,8 @@
 // for the rows r of expert e, offsets[e] <= r < offsets[e + 1].
 //
 // One kernel: a work-group computes a BM x BN tile of one expert's output with
-// v_mfma_f32_32x32x16, fp32 sums, contraction stages of 32 through a ring of four LDS
-// buffers per operand (copies run three stages ahead of the arithmetic; one barrier a
-// stage).  The sums' order depends only on the contraction length.
+// v_mfma_f32_32x32x16, fp32 sums, contraction stages of 32 or 64 through a ring of LDS buffers
+// (copies run ahead of the arithmetic; one barrier a stage).  The sums' order depends only on the contraction length.
 #include "qmm_device.h"
 #include "qmm_grouped.h"
 #include "qmm_internal.h"
@@ -19,8 +18,6 @@
 namespace qmm {
 
 namespace {
-
-constexpr int kRing = 4;
 
 // offsets clamped into [0, R] and made nondecreasing pairwise, so every row index stays in range
 __device__ __forceinline__ int clamp_off(const int32_t* o, int64_t e, int R) {
@@ -96,16 +93,18 @@ __device__ __forceinline__ void store_tile(const GroupedArgs& p, const f32x16 (&
   }
 }
 
-template <int TY, int BM, int BN, int WM, int WN, int OP, bool VEC>
+// KS, NS: contraction values per stage and stages of the ring, 64 x 2 or 32 x 4.
+template <int TY, int BM, int BN, int WM, int WN, int KS, int NS, int OP, bool VEC>
 __global__ __launch_bounds__(WM* WN * 64) void grouped_kernel(GroupedArgs p) {
   constexpr int NW = WM * WN;
   constexpr bool AX = OP == GROUPED_DW;   // a across
   constexpr bool BX = OP != GROUPED_MM;   // b across
   constexpr int FM = BM / WM / 32, FN = BN / WN / 32;
-  // the ring: four objects of their own (not one array), so that the compiler knows that a
-  // read of one does not depend on the copies under way into the others
-  constexpr int kBytes = (BM + BN) * 64;
-  __shared__ __attribute__((aligned(1024))) uint8_t t0[kBytes], t1[kBytes], t2[kBytes], t3[kBytes];
+  // the ring: objects of their own (not one array), so that the compiler knows that a read of
+  // one does not depend on the copies under way into the others
+  constexpr int kBytes = (BM + BN) * 2 * KS;
+  __shared__ __attribute__((aligned(1024))) uint8_t t0[kBytes], t1[kBytes];
+  __shared__ __attribute__((aligned(1024))) uint8_t t2[NS == 4 ? kBytes : 16], t3[NS == 4 ? kBytes : 16];
   __shared__ int found[2];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -139,8 +138,8 @@ __global__ __launch_bounds__(WM* WN * 64) void grouped_kernel(GroupedArgs p) {
   const int64_t I = OP == GROUPED_DW ? p.I : o1 - o0;  // rows of this expert's output
   const int64_t C = OP == GROUPED_DW ? o1 - o0 : p.C;
 
-  TileLoad<BM, NW, AX, VEC> la;
-  TileLoad<BN, NW, BX, VEC> lb;
+  TileLoad<BM, NW, KS, AX, VEC> la;
+  TileLoad<BN, NW, KS, BX, VEC> lb;
   const uint16_t* a = (const uint16_t*)p.a;
   const uint16_t* b = (const uint16_t*)p.b;
   if constexpr (OP == GROUPED_DW) {
@@ -152,8 +151,8 @@ __global__ __launch_bounds__(WM* WN * 64) void grouped_kernel(GroupedArgs p) {
     else lb.init(b + e * C * p.J + j0, p.J, p.J - j0, C, wave, lane);
   }
   const int wm = wave / WN, wn = wave % WN;
-  TileRead<BM, AX> ra;
-  TileRead<BN, BX> rb;
+  TileRead<BM, KS, AX> ra;
+  TileRead<BN, KS, BX> rb;
   ra.init(wm * FM * 32, lane);
   rb.init(wn * FN * 32, lane);
 
@@ -163,15 +162,15 @@ __global__ __launch_bounds__(WM* WN * 64) void grouped_kernel(GroupedArgs p) {
 #pragma unroll
     for (int g = 0; g < FN; ++g) acc[f][g] = f32x16{};
 
-  const int nst = (int)((C + kStage - 1) / kStage);
+  const int nst = (int)((C + KS - 1) / KS);
   auto copy = [&](int s, uint8_t* t) {
     la.stage(s, t, wave, lane);
-    lb.stage(s, t + BM * 64, wave, lane);
+    lb.stage(s, t + BM * 2 * KS, wave, lane);
   };
   auto compute = [&](const uint8_t* ta) {
-    const uint8_t* tb = ta + BM * 64;
+    const uint8_t* tb = ta + BM * 2 * KS;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < KS / 16; ++h) {
       uint4 fa[FM], fb[FN];
 #pragma unroll
       for (int f = 0; f < FM; ++f) fa[f] = ra.get(ta, f, h, lane);
@@ -183,27 +182,35 @@ __global__ __launch_bounds__(WM* WN * 64) void grouped_kernel(GroupedArgs p) {
         for (int g = 0; g < FN; ++g) acc[f][g] = mfma32<TY>(fa[f], fb[g], acc[f][g]);
     }
   };
-  // copies of one stage per wave: after the copies of stage s + 2 are issued, stage s has
-  // landed when at most two stages' copies are outstanding
+  // copies of one stage per wave.  Copies run NS - 1 stages ahead: when stage s begins, those of
+  // the NS - 2 stages behind it may still be on their way.
   constexpr int kPer = VEC ? la.kPer + lb.kPer : 0;
-  copy(0, t0);
-  copy(1, t1);
-  copy(2, t2);
   auto step = [&](int s, uint8_t* read, uint8_t* fill) {
-    stage_barrier<2 * kPer>();
-    copy(s + 3, fill);  // stages past the end copy zeros
+    stage_barrier<(NS - 2) * kPer>();
+    copy(s + NS - 1, fill);  // stages past the end copy zeros
     compute(read);
   };
+  copy(0, t0);
   int s = 0;
-  for (; s + kRing <= nst; s += kRing) {
-    step(s, t0, t3);
-    step(s + 1, t1, t0);
-    step(s + 2, t2, t1);
-    step(s + 3, t3, t2);
+  if constexpr (NS == 4) {
+    copy(1, t1);
+    copy(2, t2);
+    for (; s + 4 <= nst; s += 4) {
+      step(s, t0, t3);
+      step(s + 1, t1, t0);
+      step(s + 2, t2, t1);
+      step(s + 3, t3, t2);
+    }
+    if (s < nst) step(s, t0, t3);
+    if (s + 1 < nst) step(s + 1, t1, t0);
+    if (s + 2 < nst) step(s + 2, t2, t1);
+  } else {
+    for (; s + 2 <= nst; s += 2) {
+      step(s, t0, t1);
+      step(s + 1, t1, t0);
+    }
+    if (s < nst) step(s, t0, t1);
   }
-  if (s < nst) step(s, t0, t3);
-  if (s + 1 < nst) step(s + 1, t1, t0);
-  if (s + 2 < nst) step(s + 2, t2, t1);
   // no copy may still be on its way when the work-group gives its LDS back
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 
@@ -265,8 +272,10 @@ void go_tile(GroupedArgs p, hipStream_t st) {
   p.jgroup = std::min(p.jtiles, 8);
   const int64_t units = (int64_t)p.itiles * ((p.jtiles + p.jgroup - 1) / p.jgroup);
   const dim3 grid((unsigned)((units + 7) / 8 * 8 * p.jgroup));
-  if (p.vec) launch((grouped_kernel<TY, BM, BN, WM, WN, OP, true>), grid, dim3(WM * WN * 64), 0, st, p);
-  else launch((grouped_kernel<TY, BM, BN, WM, WN, OP, false>), grid, dim3(WM * WN * 64), 0, st, p);
+  // whole lines where both operands lie along the contraction, else the deeper ring
+  constexpr int KS = OP == GROUPED_MM ? 64 : 32, NS = OP == GROUPED_MM ? 2 : 4;
+  if (p.vec) launch((grouped_kernel<TY, BM, BN, WM, WN, KS, NS, OP, true>), grid, dim3(WM * WN * 64), 0, st, p);
+  else launch((grouped_kernel<TY, BM, BN, WM, WN, KS, NS, OP, false>), grid, dim3(WM * WN * 64), 0, st, p);
 }
 
 template <int TY, int OP>

@@ -42,6 +42,9 @@ struct LoraArgs {
   int slots;           // tile slots (grid)
   int slices;          // column slices of the expand kernels (set by their launch)
   float* part;         // fp32 partial products [splits][M][rp], by position
+  uint8_t* pieces;     // 16-bit pieces of scale_a t by position (lora_piece_bytes each), or NULL
+  float* factor;       // fp16: the power of two of each position's pieces
+  int few;             // the expand kernel sums and splits the parts itself (lora_few_rows)
   int splits;
   int64_t split_len;   // contraction elements per split (a multiple of 256)
   const void* base;
@@ -55,20 +58,25 @@ hipError_t launch_lora_plan(const LoraArgs& p, hipStream_t st);
 // part = X A_a^T (contraction over K), or dY B_a (contraction over N)
 hipError_t launch_lora_shrink_x(const LoraArgs& p, hipStream_t st);
 hipError_t launch_lora_shrink_dy(const LoraArgs& p, hipStream_t st);
-// T[row] = sum over the splits of part (x scale_a when `scaled`)
-hipError_t launch_lora_finalize(const LoraArgs& p, bool scaled, float* T, hipStream_t st);
-// out = base + scale_a * (sum of part) B_a^T; writes T when it is given
+// T[row] (rows of ldt) = sum over the splits of part (x scale_a when `scaled`), T may be NULL;
+// and p.pieces, p.factor when given.
+hipError_t launch_lora_finalize(const LoraArgs& p, bool scaled, float* T, int64_t ldt, hipStream_t st);
+// Whether the expand kernel sums and splits the parts itself.
+bool lora_few_rows(int64_t M, int64_t N, int r, int splits);
+// Bytes of the pieces of one position.
+int lora_piece_bytes(int type, int r);
+// out = base + scale_a * t B_a^T, t from p.pieces (outputs below 64 columns: from the parts)
 hipError_t launch_lora_expand(const LoraArgs& p, hipStream_t st);
-// out = base + dT A_a (dT [M][r] by row)
+// out = base + dt A_a, dt from p.pieces (outputs below 64 columns: dT [M][rp] by row)
 hipError_t launch_lora_expand_dx(const LoraArgs& p, const float* dT, hipStream_t st);
-
 // out[a] = sum over the rows m of adapter a of Z[m][c] * t[m][rank]: [P][r] (rank_major 0)
 // or [r][P] (rank_major 1), times scale[a] when given.  The two sides are dB (Z = dY) and
 // dA (Z = X); one that is not wanted has no blocks.
 struct LoraSide {
   const void* Z;  // [M][P]
   int64_t P;
-  const float* t;  // [M][r] by row
+  const float* t;  // [M][ldt] by row
+  int64_t ldt;
   const float* scale;
   void* out;
   int rank_major;

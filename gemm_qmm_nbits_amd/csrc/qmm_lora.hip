@@ -14,14 +14,15 @@
 // kernels sort by a ballot instead, which saves the launch.
 //
 // Numbers: t and dt stay in fp32.  Products of two 16-bit operands use the 16-bit matrix
-// instructions (exact products, fp32 sums); products with t or dt use the fp32 matrix
-// instruction v_mfma_f32_16x16x4_f32 on the 16-bit operand widened, so no value is rounded
-// before the output.  Every sum has a fixed order (no atomics): repeated calls give the
+// instructions (exact products, fp32 sums).  Products with t or dt take them as sums of 16-bit
+// pieces (expand) or the 16-bit operand widened to fp32 (outer sums), so nothing is rounded
+// below fp32 before the output.  Every sum has a fixed order (no atomics): repeated calls give the
 // same bits.
 #include "qmm_device.h"
 #include "qmm_internal.h"
 #include "qmm_lora.h"
 
+#include <algorithm>
 #include <type_traits>
 
 namespace qmm {
@@ -341,62 +342,47 @@ __global__ __launch_bounds__(LT) void lora_shrink_kernel(LoraArgs p) {
   }
 }
 
-// Sum of the splits' parts at q (in split order), sixteen loads at a time.
-__device__ __forceinline__ float sum_parts(const LoraArgs& p, const float* q) {
+// Sum of the splits' parts at q (four ranks, in split order), eight loads at a time.
+__device__ __forceinline__ f32x4 sum_parts(const LoraArgs& p, const float* q) {
   const int64_t stride = p.M * p.rp;
-  float v = 0.0f;
-  for (int s = 0; s < p.splits; s += 16) {
-    float u[16];
+  f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int s = 0; s < p.splits; s += 8) {
+    f32x4 u[8];
 #pragma unroll
-    for (int e = 0; e < 16; ++e) u[e] = q[(s + e < p.splits ? s + e : p.splits - 1) * stride];
+    for (int e = 0; e < 8; ++e) u[e] = *(const f32x4*)(q + (s + e < p.splits ? s + e : p.splits - 1) * stride);
 #pragma unroll
-    for (int e = 0; e < 16; ++e) v += s + e < p.splits ? u[e] : 0.0f;
+    for (int e = 0; e < 8; ++e)
+      if (s + e < p.splits) v += u[e];
   }
   return v;
 }
 
-// T[row][rank] = sum over the splits of part, in split order, times scale_a; rows without
-// an adapter get zeros.
-__global__ __launch_bounds__(LT) void lora_finalize_kernel(LoraArgs p, int scaled, float* T) {
-  __shared__ int rows[kLoraTile];
-  const Tile t = find_tile(p, rows, (int)blockIdx.x);
-  const float sc = scaled && p.scale && t.a < p.L ? p.scale[t.a] : 1.0f;
-  for (int i = threadIdx.x; i < t.count * p.r; i += LT) {
-    const int row = i / p.r, c = i - row * p.r;
-    float v = 0.0f;
-    if (t.a < p.L) {
-      v = sc * sum_parts(p, p.part + position(p, t, rows, row) * p.rp + c);
-    }
-    T[(int64_t)rows[row] * p.r + c] = v;
-  }
-}
-
 // ---- expand: out = base + t B_a^T, and of the gradient: out = base + dt A_a (DX) ---------
 //
-// One work-group: a tile and, per wave, every (4 gridDim.y)-th group of 64 output columns.
-// t is staged in LDS.  v_mfma_f32_16x16x4_f32 with the columns as its rows: a lane gives
-// B_a (or A_a) at one of 16 columns and 4 ranks for four steps and 16-column parts, and t of
-// row lane % 16 at the same ranks.
-//   forward  column 16 f + i is row i of part f: lane l loads B[16 f + l % 16][16 c + 4 (l / 16) ..]
-//            (ranks along the row), and ends with columns 16 f + 4 (l / 16) ..
-//   DX       column 4 i + f is row i of part f: lane l loads A[16 c + 4 (l / 16) + j][4 (l % 16) ..]
-//            (columns along the row), and ends with columns 16 (l / 16) + 4 v ..
-// NR: the 16-rank steps whose operands a wave keeps in registers over the tile's rows (up to
-// 64 ranks), or 0: any number, loaded again (from L1) for every 16 rows.
-//
-// Bound by base and out, so those are accessed by whole rows: 16 lanes x 4 columns, 4 rows at
-// a time, the next 16 rows' base on its way during the current ones'; the sums change places
-// through a wave's own piece of LDS.  BB: bytes of a base element (0: no base).
+// One work-group: a tile and, per wave, every (4 slices)-th group of 64 output columns.
+// Bound by base and out, so those are accessed by whole rows (16 lanes x 4 columns, 4 rows at
+// a time, the next 16 rows' base on its way during the current ones'), and the arithmetic is
+// kept off the vector units: v_mfma_f32_16x16x32 in the operands' own 16-bit type with the
+// columns as its rows, B_a (or A_a) as it was loaded, and t as a sum of 16-bit pieces:
+//   bf16  three truncations, t = p0 + p1 + p2 exactly (8 + 8 + 8 bits)
+//   fp16  t 2^s = p0 + p1 with one power of two per row that puts the row's largest magnitude
+//         in [2^14, 2^15); p1 rounds the remainder, 2^-22 of the element at most
+// so t loses nothing that fp32 sums keep.  A contraction step of 32 holds four chunks of 8
+// ranks, one per 16 lanes: with r <= 8, 16 or 32 the four are 4, 2 or 1 pieces of the same
+// ranks, so one loaded operand serves every piece; beyond, the steps are (32 ranks, piece).
+//   forward  column 16 f + i is row i of part f; lane l loads 8 ranks of B[16 f + l % 16]
+//   DX       A_a's ranks run down its columns: a wave copies 32 ranks x 64 columns into its
+//            piece of LDS and reads them transposed (ds_read_b64_tr_b16)
+// The sums change from the matrix layout to rows through the wave's piece of LDS.
+// BB: bytes of a base element (0: no base).  RB: 32-rank blocks whose operands a wave keeps in
+// registers over the tile's rows (1 or 2), or 0: any number, loaded again for every 16 rows.
 //
 // Rows need no alignment (a vector access may start at any element).  The last group of a
 // width that is no multiple of 64 starts at width - 64 and stores its new columns only.
-template <int TY>
-__device__ __forceinline__ void widen4(u32x2 u, float (&v)[4]) {
-  v[0] = widen<TY>(u[0] & 0xffffu);
-  v[1] = widen<TY>(u[0] >> 16);
-  v[2] = widen<TY>(u[1] & 0xffffu);
-  v[3] = widen<TY>(u[1] >> 16);
-}
+//
+// (fp32 matrix instructions on widened operands: 280 us for 4096 x 35840 at rank 32, most of
+// it vector instructions; a copy of that base and output alone takes 150 to 175.)
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 // Four elements of base as loaded.
 template <int BB>
@@ -415,11 +401,18 @@ template <int BB>
 __device__ __forceinline__ f32x4 base_values(u32x4 v, int type) {
   if constexpr (BB == 4) return __builtin_bit_cast(f32x4, v);
   if constexpr (BB == 0) return f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  float f[4];
-  const u32x2 u = {v[0], v[1]};
-  if (type == QMM_F16) widen4<QMM_F16>(u, f);
-  else widen4<QMM_BF16>(u, f);
-  return f32x4{f[0], f[1], f[2], f[3]};
+  if (type == QMM_F16)
+    return f32x4{widen<QMM_F16>(v[0] & 0xffffu), widen<QMM_F16>(v[0] >> 16), widen<QMM_F16>(v[1] & 0xffffu),
+                 widen<QMM_F16>(v[1] >> 16)};
+  return f32x4{__uint_as_float(v[0] << 16), __uint_as_float(v[0] & 0xffff0000u), __uint_as_float(v[1] << 16),
+               __uint_as_float(v[1] & 0xffff0000u)};
+}
+
+// Two values rounded to nearest even in 16 bits.
+__device__ __forceinline__ uint32_t round_pair(float a, float b, int type) {
+  const f32x2 v = {a, b};
+  if (type == QMM_F16) return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, f16x2));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
 }
 
 // Elements i .. i + 3 of out, those from `from` on.
@@ -433,102 +426,178 @@ __device__ __forceinline__ void store_out4(void* out, int type, int64_t i, int f
         if (e >= from) p[e] = v[e];
     return;
   }
-  uint32_t h[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) h[e] = type == QMM_F16 ? f32_to_f16(v[e]) : f32_to_bf16(v[e]);
+  const u32x2 h = {round_pair(v[0], v[1], type), round_pair(v[2], v[3], type)};
   uint16_t* p = (uint16_t*)out + i;
-  if (from <= 0) ((H4*)p)->v = u32x2{h[0] | (h[1] << 16), h[2] | (h[3] << 16)};
+  if (from <= 0) ((H4*)p)->v = h;
   else
 #pragma unroll
     for (int e = 1; e < 4; ++e)
-      if (e >= from) p[e] = (uint16_t)h[e];
+      if (e >= from) p[e] = (uint16_t)(h[e / 2] >> (16 * (e & 1)));
 }
 
-constexpr int kXp = 68;  // floats of a row of 64 columns in the wave's piece of LDS
+constexpr int kXp = 68;           // floats of a row of 64 columns in the wave's piece of LDS
+constexpr int kAp = 72;           // 16-bit elements of a rank's 64 columns there (DX)
+constexpr int kWaveLds = 4608;    // bytes of that piece: 16 rows of sums, or 32 ranks of A
+static_assert(16 * kXp * 4 <= kWaveLds && 32 * kAp * 2 <= kWaveLds, "");
 
-// The operands of one 16-rank step c of the 64 columns from n0: [part] (forward) or [rank step]
-// (DX), four elements each; zeros past r.
-template <bool DX>
-__device__ __forceinline__ void load_ranks(const uint16_t* Bm, int64_t W, int r, int64_t n0, int c, int ln, int lg,
-                                           u32x2 (&u)[4]) {
-  const int rank = 16 * c + 4 * lg;
+// How t lies in LDS: rows of `steps` contraction steps of four 16-byte chunks, and one chunk of
+// padding (an odd number of chunks, so 16 rows read at one chunk meet every bank once).
+template <int TY>
+struct Pieces {
+  static constexpr int kCount = TY == QMM_F16 ? 2 : 3;
+  int chunks;  // chunks of 8 ranks of one piece: 1, 2 or a multiple of 4
+  int steps;
+  __host__ __device__ __forceinline__ explicit Pieces(int r) {
+    chunks = r <= 8 ? 1 : r <= 16 ? 2 : (r + 31) / 32 * 4;
+    steps = (chunks * kCount + 3) / 4;
+  }
+  __host__ __device__ __forceinline__ int row_bytes() const { return steps * 64 + 16; }
+  // step and chunk place of piece k's chunk c
+  __device__ __forceinline__ int place(int k, int c) const {
+    return chunks <= 4 ? k * chunks + c : (((c >> 2) * kCount + k) << 2) + (c & 3);
+  }
+};
+
+// Splits the rows tf [n][ld] of t (zeros from rank r on) into pieces, row i at out + i * row_bytes;
+// factor[i] takes the inverse of row i's power of two (fp16).  `top` [n]: LDS scratch (fp16).
+// The whole work-group of NT threads calls it, between barriers.
+template <int TY, int NT>
+__device__ __forceinline__ void split_rows(const float* tf, int ld, int n, const Pieces<TY>& pc, uint8_t* out,
+                                           int64_t row_bytes, float* factor, uint32_t* top) {
+  if constexpr (TY == QMM_F16) {
+    for (int i = threadIdx.x; i < n; i += NT) top[i] = 0u;
+    __syncthreads();
+    for (int i = threadIdx.x; i < n * pc.chunks; i += NT) {
+      const float* v = tf + i / pc.chunks * ld + i % pc.chunks * 8;
+      float m = 0.0f;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    u[k] = u32x2{0u, 0u};
-    if constexpr (DX) {
-      if (rank + k < r) u[k] = ((const H4*)(Bm + (int64_t)(rank + k) * W + n0 + 4 * ln))->v;
+      for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(v[e]));
+      atomicMax(top + i / pc.chunks, __float_as_uint(m));  // a maximum: any order gives it
+    }
+    __syncthreads();
+  }
+  for (int i = threadIdx.x; i < n * pc.chunks; i += NT) {
+    const int row = i / pc.chunks, c = i % pc.chunks;
+    const float* v = tf + row * ld + c * 8;
+    uint32_t h[Pieces<TY>::kCount][4];
+    if constexpr (TY == QMM_F16) {
+      const float m = __uint_as_float(top[row]);
+      int E = 0;
+      if (m > 0.0f && m <= 3.402823466e38f) {
+        (void)frexpf(m, &E);
+        E = 15 - E;
+        E = E < 120 ? E : 120;
+      }
+#pragma unroll
+      for (int e = 0; e < 8; e += 2) {
+        const float a = ldexpf(v[e], E), b = ldexpf(v[e + 1], E);
+        const uint32_t hi = round_pair(a, b, QMM_F16);
+        const float ra = a - f16_to_f32((uint16_t)hi), rb = b - f16_to_f32((uint16_t)(hi >> 16));
+        h[0][e / 2] = hi;
+        // a value that is not finite stays in the first piece
+        h[1][e / 2] = round_pair(fabsf(ra) < 1e30f ? ra : 0.0f, fabsf(rb) < 1e30f ? rb : 0.0f, QMM_F16);
+      }
+      if (c == 0) factor[row] = ldexpf(1.0f, -E);
     } else {
-      const uint16_t* q = Bm + (n0 + 16 * k + ln) * r + rank;
-      if (rank + 4 <= r) u[k] = ((const H4*)q)->v;
-      else
 #pragma unroll
-        for (int e = 0; e < 3; ++e)
-          if (rank + e < r) u[k][e / 2] |= (uint32_t)q[e] << (16 * (e & 1));
+      for (int e = 0; e < 8; e += 2) {
+        float x[2] = {v[e], v[e + 1]};
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+          const uint32_t a = __float_as_uint(x[0]) & 0xffff0000u, b = __float_as_uint(x[1]) & 0xffff0000u;
+          h[k][e / 2] = (a >> 16) | b;
+          x[0] -= __uint_as_float(a);  // exact: the low bits
+          x[1] -= __uint_as_float(b);
+          if (k == 0) {  // a value that is not finite stays in the first piece
+            x[0] = fabsf(x[0]) < 1e38f ? x[0] : 0.0f;
+            x[1] = fabsf(x[1]) < 1e38f ? x[1] : 0.0f;
+          }
+        }
+      }
+    }
+    uint8_t* to = out + row * row_bytes;
+#pragma unroll
+    for (int k = 0; k < Pieces<TY>::kCount; ++k)
+      *(uint4*)(to + pc.place(k, c) * 16) = make_uint4(h[k][0], h[k][1], h[k][2], h[k][3]);
+    // chunks that no piece fills
+    if (c == 0)
+      for (int k = Pieces<TY>::kCount * pc.chunks; k < pc.steps * 4; ++k)
+        *(uint4*)(to + k * 16) = make_uint4(0u, 0u, 0u, 0u);
+  }
+}
+
+// Sums the splits of a tile's parts, 16 rows per work-group (blockIdx.y), and writes what the
+// later passes read: T (fp32 by row, ldt apart, times scale_a when `scaled`; zeros for rows
+// without an adapter) and the pieces of scale_a t by position (when p.pieces is given).
+template <int TY>
+__global__ __launch_bounds__(LT) void lora_finalize_kernel(LoraArgs p, int scaled, float* T, int64_t ldt) {
+  extern __shared__ __attribute__((aligned(16))) float tf[];  // [16][rp + 32]
+  __shared__ uint32_t top[16];
+  __shared__ float factor[16];
+  __shared__ int rows[kLoraTile];
+  const Tile t = find_tile(p, rows, (int)blockIdx.x);
+  const int i0 = (int)blockIdx.y * 16;
+  if (i0 >= t.count) return;
+  const int n = t.count - i0 < 16 ? t.count - i0 : 16, quads = p.rp / 4, ld = p.rp + 32;
+  const bool none = t.a == p.L;
+  if (none && !T) return;
+  const float sc = p.scale && !none ? p.scale[t.a] : 1.0f;
+  for (int i = threadIdx.x; i < 16 * (ld / 4); i += LT) {  // chunks past rp read zeros
+    const int row = i / (ld / 4), c = i % (ld / 4);
+    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (!none && row < n && c < quads) v = sum_parts(p, p.part + position(p, t, rows, i0 + row) * p.rp + 4 * c);
+    const f32x4 vs = v * sc;
+    if (T && row < n && c < quads)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (4 * c + e < ldt) T[(int64_t)rows[i0 + row] * ldt + 4 * c + e] = scaled ? vs[e] : v[e];
+    *(f32x4*)(tf + row * ld + 4 * c) = vs;
+  }
+  if (none || !p.pieces) return;
+  __syncthreads();
+  const Pieces<TY> pc(p.r);
+  uint8_t* out = p.pieces + position(p, t, rows, i0) * (pc.steps * 64);
+  if (p.use_plan) {
+    split_rows<TY, LT>(tf, ld, n, pc, out, pc.steps * 64, factor, top);
+    __syncthreads();
+    if (TY == QMM_F16 && (int)threadIdx.x < n) p.factor[t.start + i0 + threadIdx.x] = factor[threadIdx.x];
+  } else {
+    // rows of the inline form are not neighbours: one after another
+    for (int k = 0; k < n; ++k) {
+      split_rows<TY, LT>(tf + k * ld, ld, 1, pc, p.pieces + (int64_t)rows[i0 + k] * (pc.steps * 64), 0, factor, top);
+      __syncthreads();
+      if (TY == QMM_F16 && threadIdx.x == 0) p.factor[rows[i0 + k]] = factor[0];
+      __syncthreads();
     }
   }
 }
 
-template <int TY, bool DX>
-__device__ __forceinline__ void rank_step(const u32x2 (&u)[4], f32x4 tv, f32x4 (&acc)[4]) {
-  float w[4][4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) widen4<TY>(u[k], w[k]);
-#pragma unroll
-  for (int f = 0; f < 4; ++f)
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      acc[f] = __builtin_amdgcn_mfma_f32_16x16x4f32(DX ? w[j][f] : w[f][j], tv[j], acc[f], 0, 0, 0);
-}
-
-// t of the tile's rows [i0, i1) (times scale_a) into ts [64][rp + 4], zeros past the tile; the
-// forward form keeps it in p.T.
-template <bool DX>
-__device__ __forceinline__ void stage_t(const LoraArgs& p, const float* dT, const Tile& t, const int* rows, float* ts,
-                                        int i0, int i1, bool first_slice) {
-  const int r = p.r, rp = p.rp, ld = rp + 4;
-  const bool none = t.a == p.L;
-  const bool keep_t = !DX && p.T && first_slice;
-  const float sc = !DX && p.scale && !none ? p.scale[t.a] : 1.0f;
-  if (!none || keep_t)
-    for (int i = i0 * rp + threadIdx.x; i < i1 * rp; i += LT) {
-      const int row = i / rp, c = i - row * rp;
-      float v = 0.0f;
-      if (row < t.count && c < r) {
-        if (DX) v = dT[(int64_t)rows[row] * r + c];
-        else if (!none) v = sum_parts(p, p.part + position(p, t, rows, row) * rp + c);
-        if (keep_t) p.T[(int64_t)rows[row] * r + c] = v;
-      }
-      ts[row * ld + c] = v * sc;
-    }
-  __syncthreads();
-}
-
 // One wave's group of 64 columns for the tile's 16-row parts [s0, s1).  The loads of the first
 // part's base and of the ranks' operands are issued by begin(), before t is needed.
-template <int TY, bool DX, int BB, int NR>
+template <int TY, bool DX, int BB, int RB>
 struct ColumnGroup {
   const LoraArgs& p;
   const Tile& t;
   const int* rows;
-  const float* ts;
-  float* x;
+  const uint8_t* ts;
+  const float* factor;
+  uint8_t* x;  // this wave's piece of LDS
   const uint16_t* Bm;
+  const Pieces<TY> pc;
   int64_t W, n0;
-  int r, ld, steps, ln, lg, from, s0, s1;
+  int r, ln, lg, from, s0, s1;
   bool none;
-  u32x2 keep[NR ? NR : 1][4];
+  uint4 keep[RB ? RB : 1][4];
   u32x4 even[4];
 
-  __device__ __forceinline__ ColumnGroup(const LoraArgs& args, const Tile& tile, const int* rows_, const float* ts_,
-                                         float* x_, int first, int last)
-      : p(args), t(tile), rows(rows_), ts(ts_), x(x_), s0(first), s1(last) {
+  __device__ __forceinline__ ColumnGroup(const LoraArgs& args, const Tile& tile, const int* rows_, const uint8_t* ts_,
+                                         const float* factor_, uint8_t* x_, int first, int last)
+      : p(args), t(tile), rows(rows_), ts(ts_), factor(factor_), x(x_), pc(args.r), s0(first), s1(last) {
     const int lane = threadIdx.x & 63;
     ln = lane & 15;
     lg = lane >> 4;
     W = DX ? p.K : p.N;
     r = p.r;
-    ld = p.rp + 4;
-    steps = p.rp / 16;
     none = t.a == p.L;
     Bm = (const uint16_t*)(DX ? p.A : p.B) + (none ? 0 : t.a * W * r);
   }
@@ -539,45 +608,90 @@ struct ColumnGroup {
       raw[i] = load_base4<BB>(p.base, (int64_t)rows[row < t.count ? row : t.count - 1] * W + n0 + 4 * ln);
     }
   }
+  // Operands of the 32-rank block b for the four 16-column parts.
+  __device__ __forceinline__ void load_ranks(int b, uint4 (&u)[4]) const {
+    const int chunk = pc.chunks < 4 ? lg & (pc.chunks - 1) : lg;  // this lane's chunk in the block
+    const int rank = 32 * b + 8 * chunk;
+    if constexpr (DX) {
+      const int lane = threadIdx.x & 63;
+      uint4 w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {  // rank row 8 j + lane / 8, columns 8 (lane % 8) ..
+        const int row = 32 * b + 8 * j + (lane >> 3);
+        w[j] = make_uint4(0u, 0u, 0u, 0u);
+        if (row < r) w[j] = load_h8(Bm + (int64_t)row * W + n0 + 8 * (lane & 7));
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) *(uint4*)(x + (8 * j + (lane >> 3)) * (kAp * 2) + (lane & 7) * 16) = w[j];
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+      for (int f = 0; f < 4; ++f) {
+        const uint16_t* at = (const uint16_t*)x + (8 * chunk + (ln >> 2)) * kAp + 16 * f + (ln & 3) * 4;
+        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)at);
+        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(at + 4 * kAp));
+        const uint2 l2 = __builtin_bit_cast(uint2, lo), h2 = __builtin_bit_cast(uint2, hi);
+        u[f] = make_uint4(l2.x, l2.y, h2.x, h2.y);
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    } else {
+#pragma unroll
+      for (int f = 0; f < 4; ++f) u[f] = load8<false>(Bm + (n0 + 16 * f + ln) * r, rank, r);
+    }
+  }
   __device__ __forceinline__ void begin(int64_t g0) {
     n0 = g0 + 64 <= W ? g0 : W - 64;
     from = (int)(g0 - n0) - 4 * ln;  // first of this lane's four columns to store
     load_base(s0, even);
-    if constexpr (NR > 0) {
+    if constexpr (RB > 0) {
       if (!none)
 #pragma unroll
-        for (int c = 0; c < NR; ++c) load_ranks<DX>(Bm, W, r, n0, c, ln, lg, keep[c]);
+        for (int b = 0; b < RB; ++b) load_ranks(b, keep[b]);
     }
   }
-  __device__ __forceinline__ void part(int s, const u32x4 (&raw)[4]) const {  // rows 16 s ..
+  __device__ __forceinline__ void steps(const uint4 (&u)[4], const uint8_t* at, int count, f32x4 (&acc)[4]) const {
+    for (int k = 0; k < count; ++k) {
+      const uint4 tv = *(const uint4*)(at + k * 64);
+#pragma unroll
+      for (int f = 0; f < 4; ++f) acc[f] = mfma16<TY>(u[f], tv, acc[f]);
+    }
+  }
+  __device__ __forceinline__ void part(int s, const u32x4 (&raw)[4]) {  // rows 16 s ..
     f32x4 acc[4];
 #pragma unroll
     for (int f = 0; f < 4; ++f) acc[f] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     if (!none) {
-      const float* trow = ts + (s * 16 + ln) * ld + 4 * lg;
-      if constexpr (NR > 0) {
-#pragma unroll
-        for (int c = 0; c < NR; ++c)
-          if (c < steps) rank_step<TY, DX>(keep[c], *(const f32x4*)(trow + 16 * c), acc);
+      const uint8_t* at = ts + ((s - s0) * 16 + ln) * pc.row_bytes() + lg * 16;
+      constexpr int kP = Pieces<TY>::kCount;
+      if constexpr (RB == 1) {
+        steps(keep[0], at, pc.steps, acc);
+      } else if constexpr (RB == 2) {
+        steps(keep[0], at, kP, acc);
+        steps(keep[1], at + kP * 64, kP, acc);
       } else {
-        for (int c = 0; c < steps; ++c) {
-          u32x2 u[4];
-          load_ranks<DX>(Bm, W, r, n0, c, ln, lg, u);
-          rank_step<TY, DX>(u, *(const f32x4*)(trow + 16 * c), acc);
+        for (int b = 0; b < pc.chunks / 4; ++b) {
+          uint4 u[4];
+          load_ranks(b, u);
+          steps(u, at + b * kP * 64, kP, acc);
         }
       }
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const f32x4 d = DX ? f32x4{acc[0][q], acc[1][q], acc[2][q], acc[3][q]} : acc[q];
-        *(f32x4*)(x + ln * kXp + (DX ? 16 * lg + 4 * q : 16 * q + 4 * lg)) = d;
-      }
+      for (int f = 0; f < 4; ++f) *(f32x4*)((float*)x + ln * kXp + 16 * f + 4 * lg) = acc[f];
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int row = 16 * s + 4 * i + lg;
       f32x4 v = base_values<BB>(raw[i], p.base_type);
-      if (!none) v += *(const f32x4*)(x + (4 * i + lg) * kXp + 4 * ln);
+      if (!none) {
+        const f32x4 d = *(const f32x4*)((const float*)x + (4 * i + lg) * kXp + 4 * ln);
+        if constexpr (TY == QMM_F16) {
+          const float k = factor[row - 16 * s0];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = fmaf(d[e], k, v[e]);
+        } else {
+          v += d;
+        }
+      }
       if (row < t.count && from < 4) store_out4(p.out, p.out_type, (int64_t)rows[row] * W + n0 + 4 * ln, from, v);
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -597,25 +711,69 @@ struct ColumnGroup {
   }
 };
 
-template <int TY, bool DX, int BB, int NR>
-__global__ __launch_bounds__(LT) void lora_expand_kernel(LoraArgs p, const float* dT) {
-  extern __shared__ __attribute__((aligned(16))) float ts[];  // [64][rp + 4]
-  __shared__ __attribute__((aligned(16))) float xp[4][16 * kXp];
+// FEW (few rows): the parts are summed and split here, every load under way at once (one value per
+// thread), instead of by lora_finalize_kernel: at 1 x 7680 the launch saved is worth more than the
+// repetition per column slice (4.5 us).
+template <int TY, bool DX, int BB, int RB, bool FEW>
+__global__ __launch_bounds__(LT) void lora_expand_kernel(LoraArgs p) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t ts[];
+  __shared__ __attribute__((aligned(16))) uint8_t xp[4][kWaveLds];
+  __shared__ float factor[kLoraTile];
   __shared__ int rows[kLoraTile];
-  // the column slices of one tile are consecutive work-groups: rows of base and out are walked
-  // in long pieces at any time
-  const int slice = (int)(blockIdx.x % (unsigned)p.slices);
-  const Tile t = find_tile(p, rows, (int)(blockIdx.x / (unsigned)p.slices));
+  // one column slice of all tiles after another (slices of one tile next to each other: 20%
+  // slower, the adapters' operands then leave the L2s)
+  const int slice = (int)(blockIdx.x / (unsigned)p.slots);
+  const Tile t = find_tile(p, rows, (int)(blockIdx.x % (unsigned)p.slots));
   // this work-group's 16-row parts of the tile
   const int parts = (t.count + 15) / 16, per = 4 / (int)gridDim.y;
   const int s0 = (int)blockIdx.y * per, s1 = s0 + per < parts ? s0 + per : parts;
   if (s0 >= s1) return;
   const int wave = threadIdx.x >> 6;
   const int64_t W = DX ? p.K : p.N;  // output columns, at least 64
-  ColumnGroup<TY, DX, BB, NR> g(p, t, rows, ts, xp[wave], s0, s1);
+  ColumnGroup<TY, DX, BB, RB> g(p, t, rows, ts, factor, xp[wave], s0, s1);
   int64_t g0 = ((int64_t)slice * 4 + wave) * 64;
   if (g0 < W) g.begin(g0);
-  stage_t<DX>(p, dT, t, rows, ts, 16 * s0, 16 * s1, slice == 0);
+  if constexpr (FEW) {
+    // [splits][rows][rp] sums, then [rows][rp + 32] of t, behind the pieces
+    const Pieces<TY> pc(p.r);
+    const int n = (t.count < 16 * s1 ? t.count : 16 * s1) - 16 * s0, rp = p.rp, quads = rp / 4, ld = rp + 32;
+    const bool keep = p.T && slice == 0;
+    float* sums = (float*)(ts + kLoraTile / (int)gridDim.y * pc.row_bytes());
+    float* tf = sums + p.splits * n * rp;
+    uint32_t* top = (uint32_t*)xp;
+    if (t.a < p.L) {
+      for (int i = threadIdx.x; i < p.splits * n * quads; i += LT) {
+        const int s = i / (n * quads), k = i % (n * quads);
+        const float* q = p.part + (s * p.M + position(p, t, rows, 16 * s0 + k / quads)) * rp + k % quads * 4;
+        *(f32x4*)(sums + i * 4) = *(const f32x4*)q;
+      }
+      __syncthreads();
+      const float sc = p.scale ? p.scale[t.a] : 1.0f;
+      for (int i = threadIdx.x; i < n * ld; i += LT) {
+        const int row = i / ld, c = i % ld;
+        float v = 0.0f;
+        if (c < rp)
+          for (int s = 0; s < p.splits; ++s) v += sums[(s * n + row) * rp + c];
+        if (keep && c < p.r) p.T[(int64_t)rows[16 * s0 + row] * p.r + c] = v;
+        tf[i] = v * sc;
+      }
+      __syncthreads();
+      split_rows<TY, LT>(tf, ld, n, pc, ts, pc.row_bytes(), factor, top);
+    } else if (keep) {
+      for (int i = threadIdx.x; i < n * p.r; i += LT) p.T[(int64_t)rows[16 * s0 + i / p.r] * p.r + i % p.r] = 0.0f;
+    }
+  } else if (t.a < p.L) {  // the rows' pieces of t (rows past the tile: those of its last row, unused)
+    const Pieces<TY> pc(p.r);
+    const int per_row = pc.steps * 4;
+    for (int i = threadIdx.x; i < (s1 - s0) * 16 * per_row; i += LT) {
+      const int k = i / per_row, c = i - k * per_row;
+      const int row = 16 * s0 + k < t.count ? 16 * s0 + k : t.count - 1;
+      const uint8_t* from = p.pieces + position(p, t, rows, row) * (per_row * 16);
+      *(uint4*)(ts + k * pc.row_bytes() + c * 16) = *(const uint4*)(from + c * 16);
+      if (TY == QMM_F16 && c == 0) factor[k] = p.factor[position(p, t, rows, row)];
+    }
+  }
+  __syncthreads();
   while (g0 < W) {
     g.run();
     g0 += (int64_t)p.slices * 256;
@@ -623,23 +781,30 @@ __global__ __launch_bounds__(LT) void lora_expand_kernel(LoraArgs p, const float
   }
 }
 
-// Outputs narrower than 64 columns: one thread per element, ranks in order.
+// Outputs narrower than 64 columns: one thread per element, splits and ranks in order (DX: dT
+// [M][rp] by row).
 template <int TY, bool DX>
 __global__ __launch_bounds__(LT) void lora_expand_narrow_kernel(LoraArgs p, const float* dT) {
-  extern __shared__ __attribute__((aligned(16))) float ts[];
   __shared__ int rows[kLoraTile];
   const Tile t = find_tile(p, rows, (int)blockIdx.x);
   if (t.count == 0) return;
-  const int W = (int)(DX ? p.K : p.N), r = p.r, ld = p.rp + 4;
-  stage_t<DX>(p, dT, t, rows, ts, 0, kLoraTile, true);
+  const int W = (int)(DX ? p.K : p.N), r = p.r, rp = p.rp;
   const bool none = t.a == p.L;
+  const float sc = !DX && p.scale && !none ? p.scale[t.a] : 1.0f;
   const uint16_t* Bm = (const uint16_t*)(DX ? p.A : p.B) + (none ? 0 : t.a * W * r);
   for (int i = threadIdx.x; i < t.count * W; i += LT) {
     const int row = i / W, n = i - row * W;
     const int64_t at = (int64_t)rows[row] * W + n;
     float v = 0.0f;
-    if (!none)
-      for (int c = 0; c < r; ++c) v = fmaf(ts[row * ld + c], widen<TY>(DX ? Bm[c * W + n] : Bm[n * r + c]), v);
+    if (!none) {
+      const float* q = DX ? dT + (int64_t)rows[row] * rp : p.part + position(p, t, rows, row) * rp;
+      for (int c = 0; c < r; c += 4) {
+        const f32x4 x = DX ? *(const f32x4*)(q + c) : sum_parts(p, q + c) * sc;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (c + e < r) v = fmaf(x[e], widen<TY>(DX ? Bm[(c + e) * W + n] : Bm[n * r + c + e]), v);
+      }
+    }
     if (p.base) v += load_elem_rt(p.base, p.base_type, at);
     store_elem_rt(p.out, p.out_type, at, v);
   }
@@ -719,7 +884,7 @@ __global__ __launch_bounds__(LT, NF == 1 ? 4 : NF == 2 ? 3 : 2) void lora_outer_
 #pragma unroll
       for (int q = 0; q < NF; ++q) {
         const int rank = r0 + q * 16 + ln;
-        tv[k][q] = in && rank < r ? tt[row[k] * r + rank] : 0.0f;
+        tv[k][q] = in && rank < r ? tt[row[k] * sd.ldt + rank] : 0.0f;
       }
     }
 #pragma unroll
@@ -824,46 +989,67 @@ void outer_nf(const LoraOuterArgs& p, dim3 grid, hipStream_t st) {
   else launch((lora_outer_kernel<TY, 4>), grid, dim3(LT), 0, st, p);
 }
 
-// Column slices of the expand kernels (of the groups of 64 columns, four per work-group at
-// least): about four work-groups per compute unit over all tiles.
-int expand_slices(const LoraArgs& p, int64_t width) {
-  const int64_t most = (width + 255) / 256;
-  const int64_t tiles = p.use_plan ? (p.M + kLoraTile - 1) / kLoraTile : 1;
-  const int64_t want = (1024 + tiles - 1) / tiles;
-  return (int)(want < most ? want : most);
+// Runs f with the base's element size as a constant.
+template <typename F>
+hipError_t by_base(const LoraArgs& p, F f) {
+  if (!p.base) return f(std::integral_constant<int, 0>{});
+  if (p.base_type == QMM_F32) return f(std::integral_constant<int, 4>{});
+  return f(std::integral_constant<int, 2>{});
 }
 
 template <int TY, bool DX>
 hipError_t expand(LoraArgs p, const float* dT, hipStream_t st) {
   const int64_t W = DX ? p.K : p.N;
-  const uint32_t lds = (uint32_t)(kLoraTile * (p.rp + 4) * 4);
-  auto go = [&](auto kern, dim3 grid) {
+  if (W < 64) {
+    launch((lora_expand_narrow_kernel<TY, DX>), dim3((unsigned)p.slots), dim3(LT), 0, st, p, dT);
+    return hipSuccess;
+  }
+  // column slices (of the groups of 64 columns, four per work-group at least): about sixteen
+  // work-groups per compute unit over all tiles, so that the last ones do not run alone
+  const int64_t most = (W + 255) / 256;
+  const int64_t tiles = p.use_plan ? (p.M + kLoraTile - 1) / kLoraTile : 1;
+  p.slices = (int)std::min<int64_t>((4096 + tiles - 1) / tiles, most);
+  // a tile's 16-row parts go apart where the tiles' slices alone leave compute units idle
+  // (333 x 5755: 24.6 -> 15.1 us), and where 64 rows of t would not fit in LDS
+  const int apart = (tiles * p.slices < 1024 && p.M > 16) || p.r > 64 ? 4 : 1;
+  const dim3 grid((unsigned)p.slots * (unsigned)p.slices, apart);
+  uint32_t lds = (uint32_t)(kLoraTile / apart * Pieces<TY>(p.r).row_bytes());
+  if (p.few) {
+    const int rows = std::min<int>((int)p.M, kLoraTile / apart);
+    lds += (uint32_t)(rows * (p.splits * p.rp + p.rp + 32) * 4);
+  }
+  auto go = [&](auto kern) {
     if (lds > 32 * 1024) {
       const hipError_t e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
       if (e != hipSuccess) return e;
     }
-    launch(kern, grid, dim3(LT), lds, st, p, dT);
+    launch(kern, grid, dim3(LT), lds, st, p);
     return hipSuccess;
   };
-  if (W < 64) return go(lora_expand_narrow_kernel<TY, DX>, dim3((unsigned)p.slots));
-  p.slices = expand_slices(p, W);
-  // where the tiles' slices alone leave compute units idle, a tile's 16-row parts go apart
-  // (333 x 5755: 24.6 -> 15.1 us)
-  const int64_t tiles = p.use_plan ? (p.M + kLoraTile - 1) / kLoraTile : 1;
-  const dim3 grid((unsigned)p.slots * (unsigned)p.slices, tiles * p.slices < 1024 && p.M > 16 ? 4 : 1);
-  auto go_base = [&](auto bb) {
+  return by_base(p, [&](auto bb) {
     constexpr int BB = decltype(bb)::value;
-    if (p.r <= 16) return go(lora_expand_kernel<TY, DX, BB, 1>, grid);
-    if (p.r <= 32) return go(lora_expand_kernel<TY, DX, BB, 2>, grid);
-    if (p.r <= 64) return go(lora_expand_kernel<TY, DX, BB, 4>, grid);
-    return go(lora_expand_kernel<TY, DX, BB, 0>, grid);
-  };
-  if (!p.base) return go_base(std::integral_constant<int, 0>{});
-  if (p.base_type == QMM_F32) return go_base(std::integral_constant<int, 4>{});
-  return go_base(std::integral_constant<int, 2>{});
+    if constexpr (!DX) {
+      if (p.few && p.r <= 32) return go(lora_expand_kernel<TY, DX, BB, 1, true>);
+      if (p.few) return go(lora_expand_kernel<TY, DX, BB, 2, true>);
+    }
+    if (p.r <= 32) return go(lora_expand_kernel<TY, DX, BB, 1, false>);
+    if (p.r <= 64) return go(lora_expand_kernel<TY, DX, BB, 2, false>);
+    return go(lora_expand_kernel<TY, DX, BB, 0, false>);
+  });
 }
 
 }  // namespace
+
+bool lora_few_rows(int64_t M, int64_t N, int r, int splits) {
+  // no plan, operands in registers, and 16 rows' parts within 64 KB of LDS
+  const int rp = lora_rank_pad(r);
+  return M <= kLoraInlineRows && N >= 64 && r <= 64 &&
+         std::min<int64_t>(M, 16) * (splits * rp + rp + 32) * 4 <= 64 * 1024;
+}
+
+int lora_piece_bytes(int type, int r) {
+  return type == QMM_F16 ? Pieces<QMM_F16>(r).steps * 64 : Pieces<QMM_BF16>(r).steps * 64;
+}
 
 hipError_t launch_lora_plan(const LoraArgs& p, hipStream_t st) {
   launch(lora_plan_kernel, dim3((unsigned)(p.L + 1)), dim3(kPlanThreads), 0, st, p.ids, p.M, p.L, p.plan);
@@ -880,8 +1066,11 @@ hipError_t launch_lora_shrink_dy(const LoraArgs& p, hipStream_t st) {
   return hipSuccess;
 }
 
-hipError_t launch_lora_finalize(const LoraArgs& p, bool scaled, float* T, hipStream_t st) {
-  launch(lora_finalize_kernel, dim3((unsigned)p.slots), dim3(LT), 0, st, p, scaled ? 1 : 0, T);
+hipError_t launch_lora_finalize(const LoraArgs& p, bool scaled, float* T, int64_t ldt, hipStream_t st) {
+  const dim3 grid((unsigned)p.slots, 4);
+  const uint32_t lds = (uint32_t)(16 * (p.rp + 32) * 4);
+  if (p.type == QMM_F16) launch(lora_finalize_kernel<QMM_F16>, grid, dim3(LT), lds, st, p, scaled ? 1 : 0, T, ldt);
+  else launch(lora_finalize_kernel<QMM_BF16>, grid, dim3(LT), lds, st, p, scaled ? 1 : 0, T, ldt);
   return hipSuccess;
 }
 

@@ -33,7 +33,7 @@ int splits(int64_t M, int64_t C) {
 }
 
 struct Layout {
-  size_t off = 0, perm = 0, tiles = 0, part = 0, t = 0, dt = 0, db = 0, da = 0, total = 0;
+  size_t off = 0, perm = 0, tiles = 0, part = 0, pieces = 0, factor = 0, t = 0, dt = 0, db = 0, da = 0, total = 0;
   int chunk = 0;  // rows per chunk of the outer sums
 };
 
@@ -56,11 +56,16 @@ Layout layout(int64_t M, int64_t K, int64_t N, int r, int64_t L, bool grad) {
   const int s = grad ? std::max(splits(M, K), splits(M, N)) : splits(M, K);
   w.part = at;
   at += up256((size_t)s * (size_t)M * rp * 4);
+  // (the longer of the two types' pieces: the query has no type)
+  w.pieces = at;
+  at += up256((size_t)M * (size_t)std::max(lora_piece_bytes(QMM_F16, r), lora_piece_bytes(QMM_BF16, r)));
+  w.factor = at;
+  at += up256((size_t)M * 4);
   if (grad) {
     w.t = at;
-    at += up256((size_t)M * (size_t)r * 4);
+    at += up256((size_t)M * rp * 4);
     w.dt = at;
-    at += up256((size_t)M * (size_t)r * 4);
+    at += up256((size_t)M * rp * 4);
     // partial outer sums of both sides (a function of the shape, whatever is asked for)
     w.chunk = lora_outer_chunk(M, col_blocks(K) + col_blocks(N));
     const size_t slots = (size_t)(2 * M / w.chunk + 1);
@@ -195,8 +200,14 @@ qmm_status qmm_lora_add(const void* X, int type, int64_t M, int64_t K, int64_t N
   p.out_type = y_type;
   p.T = T;
   set_split(p, K);
+  p.few = lora_few_rows(M, N, r, p.splits);
   hipError_t e = p.use_plan ? launch_lora_plan(p, st) : hipSuccess;
   if (e == hipSuccess) e = launch_lora_shrink_x(p, st);
+  if (!p.few) {
+    p.pieces = (uint8_t*)workspace + l.pieces;
+    p.factor = (float*)((uint8_t*)workspace + l.factor);
+    if (e == hipSuccess) e = launch_lora_finalize(p, false, T, r, st);
+  }
   if (e == hipSuccess) e = launch_lora_expand(p, st);
   if (e != hipSuccess) return (qmm_status)e;
   return (qmm_status)hipGetLastError();
@@ -222,13 +233,17 @@ qmm_status qmm_lora_grad(const void* dY, const void* X, int type, int64_t M, int
     p.X = X;
     set_split(p, K);
     if (e == hipSuccess) e = launch_lora_shrink_x(p, st);
-    if (e == hipSuccess) e = launch_lora_finalize(p, false, t, st);
+    if (e == hipSuccess) e = launch_lora_finalize(p, false, t, p.rp, st);
   }
   if (M > 0 && (dX || dA)) {
     p.dY = dY;
     set_split(p, N);
     if (e == hipSuccess) e = launch_lora_shrink_dy(p, st);
-    if (e == hipSuccess) e = launch_lora_finalize(p, true, dt, st);
+    if (dX) {
+      p.pieces = ws + l.pieces;
+      p.factor = (float*)(ws + l.factor);
+    }
+    if (e == hipSuccess) e = launch_lora_finalize(p, true, dt, p.rp, st);
   }
   if (dA || dB) {
     LoraOuterArgs o{};
@@ -239,8 +254,8 @@ qmm_status qmm_lora_grad(const void* dY, const void* X, int type, int64_t M, int
     o.plan = p.plan;
     o.out_type = g_type;
     o.chunk = l.chunk;
-    if (dB) o.side[0] = {dY, N, T ? T : t, w.scale, dB, 0, col_blocks(N), (float*)(ws + l.db)};
-    if (dA) o.side[1] = {X, K, dt, nullptr, dA, 1, col_blocks(K), (float*)(ws + l.da)};  // dt holds the scale
+    if (dB) o.side[0] = {dY, N, T ? T : t, T ? r : p.rp, w.scale, dB, 0, col_blocks(N), (float*)(ws + l.db)};
+    if (dA) o.side[1] = {X, K, dt, p.rp, nullptr, dA, 1, col_blocks(K), (float*)(ws + l.da)};  // dt holds the scale
     if (e == hipSuccess) e = launch_lora_outer(o, st);
   }
   if (dX && M > 0) {

@@ -1,17 +1,18 @@
-// Tiles of 16-bit operands in LDS for the matrix cores: how a stage of 32 contraction
-// values is copied in and read back as operands of v_mfma_f32_32x32x16.
+// Tiles of 16-bit operands in LDS for the matrix cores: how a stage of KS contraction values
+// (32 or 64) is copied in and read back as operands of v_mfma_f32_32x32x16.
 //
-// An operand tile holds T rows (output rows or columns) by 32 contraction values, in one of
+// An operand tile holds T rows (output rows or columns) by KS contraction values, in one of
 // two forms, by how the operand lies in memory:
-//   along   the contraction runs along memory rows: [T][32], 64 bytes per tile row.  A lane's
-//           operand (8 consecutive contraction values of one row) is one 16-byte read.
-//   across  the contraction runs down memory columns: [32][T], 2 T bytes per contraction
+//   along   the contraction runs along memory rows: [T][KS], 2 KS bytes per tile row.  A lane's
+//           operand (8 consecutive contraction values of one row) is one 16-byte read.  64 values
+//           are whole 128-byte lines; 32 values fetch every line twice.
+//   across  the contraction runs down memory columns: [KS][T], 2 T bytes per contraction
 //           value.  A lane's operand is two ds_read_b64_tr_b16, each of which hands a group
 //           of 16 lanes a 4 x 16 block transposed.
 // Either way tiles are filled by direct global->LDS copies of 16 bytes per lane, which write
 // LDS in lane order, so the bank swizzle is applied by choosing which 16 bytes a lane fetches:
-//   along   piece p (of 4) of row r sits at p ^ ((r / 4) % 4): 16 rows read at one piece cover
-//           the 16 bank groups of a 256-byte line.
+//   along   KS = 32: piece p (of 4) of row r sits at p ^ ((r / 4) % 4); KS = 64: piece p (of 8) at
+//           p ^ ((r / 2) % 8): 16 rows read at one piece cover the 16 bank groups of 256 bytes.
 //   across  the 64-byte segment s of contraction row c sits at s ^ (c % 4) (T = 64, two segments:
 //           s ^ ((c / 2) % 2)): the four rows of a transposed read lie in four bank quarters.
 // Bytes outside the operand (rows past the end, contraction values past the end) read as zero:
@@ -25,7 +26,6 @@ namespace qmm {
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kStage = 32;                       // contraction values per stage
 constexpr uint32_t kPastRange = 0x80000000u;     // an offset past every descriptor's range
 constexpr uint32_t kTileRange = 0x7fffffffu;
 
@@ -42,9 +42,9 @@ __device__ __forceinline__ f32x16 mfma32(const uint4& a, const uint4& b, f32x16 
 
 // Copies one operand's tiles.  T: tile rows; NW: waves; ACROSS: the form; VEC: 16-byte
 // copies (else element loads through registers).
-template <int T, int NW, bool ACROSS, bool VEC>
+template <int T, int NW, int KS, bool ACROSS, bool VEC>
 struct TileLoad {
-  static constexpr int kPer = T * 64 / 1024 / NW;  // copies per wave and stage
+  static constexpr int kPer = T * KS * 2 / 1024 / NW;  // copies per wave and stage
   static_assert(kPer >= 1, "every wave copies, so that all wait for the same count");
   const uint8_t* base;  // first row (along) or first contraction row (across)
   int64_t ld;           // bytes between memory rows
@@ -71,7 +71,8 @@ struct TileLoad {
         crow[q] = c;
         off[q] = piece * 8 < width ? (uint32_t)(c * ld) + (uint32_t)piece * 16u : kPastRange;
       } else {
-        const int r = at / 64, piece = ((at % 64) / 16) ^ ((r >> 2) & 3);
+        const int r = at / (2 * KS), pos = (at % (2 * KS)) / 16;
+        const int piece = pos ^ (KS == 32 ? (r >> 2) & 3 : (r >> 1) & 7);
         crow[q] = piece * 8;
         off[q] = r < rows ? (uint32_t)(r * ld) + (uint32_t)piece * 16u : kPastRange;
       }
@@ -80,7 +81,7 @@ struct TileLoad {
 
   // Stage s of the contraction into dst.
   __device__ __forceinline__ void stage(int s, uint8_t* dst, int wave, int lane) const {
-    const int c0 = s * kStage;
+    const int c0 = s * KS;
     if constexpr (VEC) {
       const uint8_t* p = ACROSS ? base + (int64_t)c0 * ld : base + (int64_t)c0 * 2;
       const __amdgpu_buffer_rsrc_t r = make_rsrc(p, kTileRange);
@@ -95,21 +96,25 @@ struct TileLoad {
       for (int q = 0; q < kPer; ++q) {
         const int at = (wave * kPer + q) * 1024 + lane * 16;
         uint32_t w[4] = {0u, 0u, 0u, 0u};
-        if (off[q] != kPastRange) {
+        if (off[q] != kPastRange && c0 + crow[q] < left) {
+          // this lane's 8 elements, by whole vectors where all exist (any address will do)
+          const uint16_t* src;
+          int n;
+          if constexpr (ACROSS) {
+            const int pos = (at % (2 * T)) / 16;
+            const int piece = pos ^ (T == 64 ? ((crow[q] >> 1) & 1) << 2 : (crow[q] & 3) << 2);
+            src = (const uint16_t*)(base + (int64_t)(c0 + crow[q]) * ld) + piece * 8;
+            n = width - piece * 8;
+          } else {
+            src = (const uint16_t*)(base + (int64_t)(at / (2 * KS)) * ld) + c0 + crow[q];
+            n = left - c0 - crow[q];
+          }
+          if (n >= 8) {
+            __builtin_memcpy(w, src, 16);
+          } else {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            bool ok;
-            const uint16_t* src;
-            if constexpr (ACROSS) {
-              const int pos = (at % (2 * T)) / 16;
-              const int piece = pos ^ (T == 64 ? ((crow[q] >> 1) & 1) << 2 : (crow[q] & 3) << 2);
-              ok = piece * 8 + e < width && c0 + crow[q] < left;
-              src = (const uint16_t*)(base + (int64_t)(c0 + crow[q]) * ld) + piece * 8 + e;
-            } else {
-              ok = c0 + crow[q] + e < left;
-              src = (const uint16_t*)(base + (int64_t)(at / 64) * ld) + c0 + crow[q] + e;
-            }
-            if (ok) w[e / 2] |= (uint32_t)*src << (16 * (e & 1));
+            for (int e = 0; e < 7; ++e)
+              if (e < n) w[e / 2] |= (uint32_t)src[e] << (16 * (e & 1));
           }
         }
         *(uint4*)(dst + at) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -119,11 +124,11 @@ struct TileLoad {
 };
 
 // Reads operands of one 32-row fragment.  The lane part of the address is fixed; `row` (a
-// multiple of 32) and the half (contraction values 16 half ..) are constants of the code.
-template <int T, bool ACROSS>
+// multiple of 32) and the 16 contraction values are constants of the code.
+template <int T, int KS, bool ACROSS>
 struct TileRead {
   uint32_t at;     // along: byte of row lane % 32;  across: byte of this lane's block row
-  uint32_t sw;     // along: (row / 4) % 4;  across: the segment exclusive-or
+  uint32_t sw;     // along: the piece exclusive-or;  across: the segment exclusive-or
 
   __device__ __forceinline__ void init(int row0, int lane) {
     if constexpr (ACROSS) {
@@ -133,14 +138,14 @@ struct TileRead {
       at = (uint32_t)(c * 2 * T + ((g & 1) * 16 + 4 * (i & 3)) * 2);
     } else {
       const int r = lane & 31;
-      sw = (uint32_t)((r >> 2) & 3);
-      at = (uint32_t)((row0 + r) * 64);
+      sw = (uint32_t)(KS == 32 ? (r >> 2) & 3 : (r >> 1) & 7);
+      at = (uint32_t)((row0 + r) * 2 * KS);
     }
     seg0 = row0 / 32;
   }
   int seg0;
 
-  // fragment f (rows row0 + 32 f ..), half h (0 or 1)
+  // fragment f (rows row0 + 32 f ..), contraction values 16 h ..
   __device__ __forceinline__ uint4 get(const uint8_t* tile, int f, int h, int lane) const {
     if constexpr (ACROSS) {
       const uint32_t o = at + (uint32_t)(h * 16 * 2 * T) + ((uint32_t)(seg0 + f) ^ sw) * 64u;
@@ -153,7 +158,7 @@ struct TileRead {
       return make_uint4(l2.x, l2.y, h2.x, h2.y);
     } else {
       const uint32_t piece = (uint32_t)(2 * h + (lane >> 5)) ^ sw;
-      return *(const uint4*)(tile + at + (uint32_t)f * 32u * 64u + piece * 16u);
+      return *(const uint4*)(tile + at + (uint32_t)f * 32u * 2u * KS + piece * 16u);
     }
   }
 };
