@@ -6,8 +6,8 @@
 // for the rows r of expert e, offsets[e] <= r < offsets[e + 1].
 //
 // One kernel: a work-group computes a BM x BN tile of one expert's output with
-// v_mfma_f32_32x32x16, fp32 sums, contraction stages of 32 or 64 through a ring of LDS buffers
-// (copies run ahead of the arithmetic; one barrier a stage).  The sums' order depends only on the contraction length.
+// v_mfma_f32_32x32x16, fp32 sums, contraction stages of 32 through a ring of four LDS buffers
+// (copies run three stages ahead of the arithmetic; one barrier a stage).  The sums' order depends only on the contraction length.
 #include "qmm_device.h"
 #include "qmm_grouped.h"
 #include "qmm_internal.h"
@@ -93,18 +93,18 @@ __device__ __forceinline__ void store_tile(const GroupedArgs& p, const f32x16 (&
   }
 }
 
-// KS, NS: contraction values per stage and stages of the ring, 64 x 2 or 32 x 4.
-template <int TY, int BM, int BN, int WM, int WN, int KS, int NS, int OP, bool VEC>
+// ROT: each work-group begins the contraction at a stage of its own and goes round, so that
+// work-groups that stream rows of one pitch do not ask the same memory channels at once.
+template <int TY, int BM, int BN, int WM, int WN, int OP, bool VEC, bool ROT>
 __global__ __launch_bounds__(WM* WN * 64) void grouped_kernel(GroupedArgs p) {
-  constexpr int NW = WM * WN;
+  constexpr int NW = WM * WN, KS = 32;
   constexpr bool AX = OP == GROUPED_DW;   // a across
   constexpr bool BX = OP != GROUPED_MM;   // b across
   constexpr int FM = BM / WM / 32, FN = BN / WN / 32;
   // the ring: objects of their own (not one array), so that the compiler knows that a read of
   // one does not depend on the copies under way into the others
   constexpr int kBytes = (BM + BN) * 2 * KS;
-  __shared__ __attribute__((aligned(1024))) uint8_t t0[kBytes], t1[kBytes];
-  __shared__ __attribute__((aligned(1024))) uint8_t t2[NS == 4 ? kBytes : 16], t3[NS == 4 ? kBytes : 16];
+  __shared__ __attribute__((aligned(1024))) uint8_t t0[kBytes], t1[kBytes], t2[kBytes], t3[kBytes];
   __shared__ int found[2];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -163,7 +163,10 @@ __global__ __launch_bounds__(WM* WN * 64) void grouped_kernel(GroupedArgs p) {
     for (int g = 0; g < FN; ++g) acc[f][g] = f32x16{};
 
   const int nst = (int)((C + KS - 1) / KS);
-  auto copy = [&](int s, uint8_t* t) {
+  const int first = ROT && nst > 0 ? (int)((blockIdx.x * 2654435761u) >> 8) % nst : 0;
+  auto copy = [&](int i, uint8_t* t) {  // the i-th stage this work-group takes
+    int s = i;
+    if (ROT && i < nst) s = i + first < nst ? i + first : i + first - nst;
     la.stage(s, t, wave, lane);
     lb.stage(s, t + BM * 2 * KS, wave, lane);
   };
@@ -182,35 +185,27 @@ __global__ __launch_bounds__(WM* WN * 64) void grouped_kernel(GroupedArgs p) {
         for (int g = 0; g < FN; ++g) acc[f][g] = mfma32<TY>(fa[f], fb[g], acc[f][g]);
     }
   };
-  // copies of one stage per wave.  Copies run NS - 1 stages ahead: when stage s begins, those of
-  // the NS - 2 stages behind it may still be on their way.
+  // Copies run three stages ahead: when stage s begins, those of the two behind it may still be
+  // on their way.
   constexpr int kPer = VEC ? la.kPer + lb.kPer : 0;
   auto step = [&](int s, uint8_t* read, uint8_t* fill) {
-    stage_barrier<(NS - 2) * kPer>();
-    copy(s + NS - 1, fill);  // stages past the end copy zeros
+    stage_barrier<2 * kPer>();
+    copy(s + 3, fill);  // stages past the end copy zeros
     compute(read);
   };
   copy(0, t0);
+  copy(1, t1);
+  copy(2, t2);
   int s = 0;
-  if constexpr (NS == 4) {
-    copy(1, t1);
-    copy(2, t2);
-    for (; s + 4 <= nst; s += 4) {
-      step(s, t0, t3);
-      step(s + 1, t1, t0);
-      step(s + 2, t2, t1);
-      step(s + 3, t3, t2);
-    }
-    if (s < nst) step(s, t0, t3);
-    if (s + 1 < nst) step(s + 1, t1, t0);
-    if (s + 2 < nst) step(s + 2, t2, t1);
-  } else {
-    for (; s + 2 <= nst; s += 2) {
-      step(s, t0, t1);
-      step(s + 1, t1, t0);
-    }
-    if (s < nst) step(s, t0, t1);
+  for (; s + 4 <= nst; s += 4) {
+    step(s, t0, t3);
+    step(s + 1, t1, t0);
+    step(s + 2, t2, t1);
+    step(s + 3, t3, t2);
   }
+  if (s < nst) step(s, t0, t3);
+  if (s + 1 < nst) step(s + 1, t1, t0);
+  if (s + 2 < nst) step(s + 2, t2, t1);
   // no copy may still be on its way when the work-group gives its LDS back
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 
@@ -269,21 +264,40 @@ template <int TY, int BM, int BN, int WM, int WN, int OP>
 void go_tile(GroupedArgs p, hipStream_t st) {
   p.jtiles = (int)((p.J + BN - 1) / BN);
   p.itiles = OP == GROUPED_DW ? (int)(p.E * ((p.I + BM - 1) / BM)) : (int)((p.R + BM - 1) / BM + std::min(p.E, p.R));
-  p.jgroup = std::min(p.jtiles, 8);
-  const int64_t units = (int64_t)p.itiles * ((p.jtiles + p.jgroup - 1) / p.jgroup);
+  // column tiles in units of up to 8, evenly: units dealt to the XCDs in turn must not differ
+  // (12 tiles as 8 + 4 gave every other XCD half the work: 548 against 436 us)
+  const int groups = (p.jtiles + 7) / 8;
+  p.jgroup = (p.jtiles + groups - 1) / groups;
+  const int64_t units = (int64_t)p.itiles * groups;
   const dim3 grid((unsigned)((units + 7) / 8 * 8 * p.jgroup));
-  // whole lines where both operands lie along the contraction, else the deeper ring
-  constexpr int KS = OP == GROUPED_MM ? 64 : 32, NS = OP == GROUPED_MM ? 2 : 4;
-  if (p.vec) launch((grouped_kernel<TY, BM, BN, WM, WN, KS, NS, OP, true>), grid, dim3(WM * WN * 64), 0, st, p);
-  else launch((grouped_kernel<TY, BM, BN, WM, WN, KS, NS, OP, false>), grid, dim3(WM * WN * 64), 0, st, p);
+  constexpr bool ROT = OP == GROUPED_MM && BM == 64;
+  if (p.vec) launch((grouped_kernel<TY, BM, BN, WM, WN, OP, true, ROT>), grid, dim3(WM * WN * 64), 0, st, p);
+  else launch((grouped_kernel<TY, BM, BN, WM, WN, OP, false, ROT>), grid, dim3(WM * WN * 64), 0, st, p);
 }
 
+// Tile by the mean rows of an expert (bf16, us; 32 experts of 5760 x 2880, even routing):
+//   mean rows          32        64        96       128
+//   MM  64 x 128      232       312       402       475
+//       128 x 256     218       226       282       322
+//       256 x 256     240       252       262       280
+//   DX  64 x 128      190       282       349       420
+//       128 x 256     206       227       249       322
+//       256 x 256     279       275       278       287
+//   DW  128 x 128     369       422       509       634
+//       256 x 256     400       409       458       495
+// (128 experts of 1536 x 2048, mean 32: MM 160 / 195 / 210, DX 161 / 152 / 181, DW 280 / 304.)
 template <int TY, int OP>
 void go_op(const GroupedArgs& p, hipStream_t st) {
-  const int64_t mean = OP == GROUPED_DW ? p.I : (p.R + p.E - 1) / p.E;
-  if (mean <= 64) go_tile<TY, 64, 128, 1, 4, OP>(p, st);
-  else if (mean <= 256) go_tile<TY, 128, 128, 2, 2, OP>(p, st);
-  else go_tile<TY, 256, 256, 4, 2, OP>(p, st);
+  const int64_t mean = (p.R + p.E - 1) / p.E;
+  if constexpr (OP == GROUPED_DW) {
+    // (outputs up to 128 wide or high would leave half of the larger tile unused)
+    if (mean <= 48 || p.I <= 128 || p.J <= 128) go_tile<TY, 128, 128, 2, 2, OP>(p, st);
+    else go_tile<TY, 256, 256, 4, 2, OP>(p, st);
+  } else {
+    if (mean <= 32) go_tile<TY, 64, 128, 1, 4, OP>(p, st);
+    else if (mean <= 96) go_tile<TY, 128, 256, 2, 4, OP>(p, st);
+    else go_tile<TY, 256, 256, 4, 2, OP>(p, st);
+  }
 }
 
 template <int TY>
