@@ -44,7 +44,7 @@ __device__ __forceinline__ uint32_t range_left(int64_t total, int64_t from) {
   return left <= 0 ? 0u : left >= 0x7fffffff ? 0x7fffffffu : (uint32_t)left;
 }
 
-template <int OT, int FM, int FN>
+template <int OT, bool PAIRS, int FM, int FN>
 __device__ __forceinline__ void dgrad_store(void* out, const float* rs, const f32x16 (&acc)[FM][FN], int64_t M,
                                             int64_t K, int64_t m0, int64_t k0, int wm, int wn, int lane) {
   constexpr int ES = OT == QMM_F32 ? 4 : 2;
@@ -53,19 +53,19 @@ __device__ __forceinline__ void dgrad_store(void* out, const float* rs, const f3
 #pragma unroll
   for (int f = 0; f < FM; ++f) {
     const int r0 = (wm * FM + f) * 32 + 4 * (lane >> 5);
+    const int left = M - m0 - r0 > 32 ? 32 : (int)(M - m0 - r0);
+    float s[16];
 #pragma unroll
     for (int v = 0; v < 16; ++v) {
-      const int row = r0 + 8 * (v >> 2) + (v & 3);
-      const bool in = m0 + row < M;
-      const float s = rs && in ? rs[m0 + row] : 1.0f;
+      const int dr = 8 * (v >> 2) + (v & 3);
+      s[v] = rs && dr < left ? rs[m0 + r0 + dr] : 1.0f;
+    }
 #pragma unroll
-      for (int g = 0; g < FN; ++g) {
-        const int c = (wn * FN + g) * 32 + (lane & 31);
-        const uint32_t o = in && k0 + c < K ? (uint32_t)row * ld + (uint32_t)c * ES : kPastRange;
-        const float x = acc[f][g][v] * s;
-        if constexpr (OT == QMM_F32) __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x), r, (int)o, 0, 0);
-        else __builtin_amdgcn_raw_buffer_store_b16(OT == QMM_F16 ? f32_to_f16(x) : f32_to_bf16(x), r, (int)o, 0, 0);
-      }
+    for (int g = 0; g < FN; ++g) {
+      const int c = (wn * FN + g) * 32 + (lane & 31);
+      const int cols = K - k0 - c > 32 ? 32 : (int)(K - k0 - c);
+      store_block<OT, PAIRS>(r, (uint32_t)r0 * ld + (uint32_t)c * ES, ld, left, cols, lane,
+                             [&](int v) { return acc[f][g][v] * s[v]; });
     }
   }
 }
@@ -230,11 +230,15 @@ __global__ __launch_bounds__(WM* WN * 64) void dgrad_kernel(DgradArgs p) {
   // no copy may still be on its way when the work-group gives its LDS back
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 
+  const bool pairs = p.K % 2 == 0 && (uintptr_t)p.out % 4 == 0;
   if (p.splits > 1)
-    dgrad_store<QMM_F32, FM, FN>(p.partials + (int64_t)ks * p.M * p.K, nullptr, acc, p.M, p.K, m0, k0, wm, wn, lane);
-  else if (p.out_type == QMM_F32) dgrad_store<QMM_F32, FM, FN>(p.out, p.row_scale, acc, p.M, p.K, m0, k0, wm, wn, lane);
-  else if (p.out_type == QMM_F16) dgrad_store<QMM_F16, FM, FN>(p.out, p.row_scale, acc, p.M, p.K, m0, k0, wm, wn, lane);
-  else dgrad_store<QMM_BF16, FM, FN>(p.out, p.row_scale, acc, p.M, p.K, m0, k0, wm, wn, lane);
+    dgrad_store<QMM_F32, false, FM, FN>(p.partials + (int64_t)ks * p.M * p.K, nullptr, acc, p.M, p.K, m0, k0, wm, wn, lane);
+  else if (p.out_type == QMM_F32) dgrad_store<QMM_F32, false, FM, FN>(p.out, p.row_scale, acc, p.M, p.K, m0, k0, wm, wn, lane);
+  else if (p.out_type == QMM_F16 && pairs)
+    dgrad_store<QMM_F16, true, FM, FN>(p.out, p.row_scale, acc, p.M, p.K, m0, k0, wm, wn, lane);
+  else if (p.out_type == QMM_F16) dgrad_store<QMM_F16, false, FM, FN>(p.out, p.row_scale, acc, p.M, p.K, m0, k0, wm, wn, lane);
+  else if (pairs) dgrad_store<QMM_BF16, true, FM, FN>(p.out, p.row_scale, acc, p.M, p.K, m0, k0, wm, wn, lane);
+  else dgrad_store<QMM_BF16, false, FM, FN>(p.out, p.row_scale, acc, p.M, p.K, m0, k0, wm, wn, lane);
 }
 
 struct TileSize {

@@ -62,10 +62,8 @@ __device__ __forceinline__ void find_slot(const GroupedArgs& p, int slot, int* f
   __syncthreads();
 }
 
-// Stores a tile: rows orow .. of the output, `rows` of them exist.  Offsets are 32-bit from the
-// tile's first element; elements past the tile's end address past the descriptor's range,
-// which drops the store.
-template <int OT, int BM, int FM, int FN>
+// Stores a tile: rows orow .. of the output, `rows` of them exist.
+template <int OT, bool PAIRS, int FM, int FN>
 __device__ __forceinline__ void store_tile(const GroupedArgs& p, const f32x16 (&acc)[FM][FN], int64_t orow, int rows,
                                            int64_t j0, int64_t e, int wm, int wn, int lane) {
   constexpr int ES = OT == QMM_F32 ? 4 : 2;
@@ -74,21 +72,14 @@ __device__ __forceinline__ void store_tile(const GroupedArgs& p, const f32x16 (&
 #pragma unroll
   for (int g = 0; g < FN; ++g) {
     const int c = (wn * FN + g) * 32 + (lane & 31);
-    const bool in = j0 + c < p.J;
+    const int cols = p.J - j0 - c > 32 ? 32 : (int)(p.J - j0 - c);
     float bias = 0.0f;
-    if (p.bias && in) bias = load_elem<OT>(p.bias, e * p.J + j0 + c);
+    if (p.bias && cols > 0) bias = load_elem<OT>(p.bias, e * p.J + j0 + c);
 #pragma unroll
     for (int f = 0; f < FM; ++f) {
       const int r0 = (wm * FM + f) * 32 + 4 * (lane >> 5);
-      const uint32_t o0 = (uint32_t)r0 * ld + (uint32_t)c * ES;
-#pragma unroll
-      for (int v = 0; v < 16; ++v) {
-        const int dr = 8 * (v >> 2) + (v & 3);
-        const uint32_t o = in && r0 + dr < rows ? o0 + (uint32_t)dr * ld : kPastRange;
-        const float x = acc[f][g][v] + bias;
-        if constexpr (OT == QMM_F32) __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x), r, (int)o, 0, 0);
-        else __builtin_amdgcn_raw_buffer_store_b16(OT == QMM_F16 ? f32_to_f16(x) : f32_to_bf16(x), r, (int)o, 0, 0);
-      }
+      store_block<OT, PAIRS>(r, (uint32_t)r0 * ld + (uint32_t)c * ES, ld, rows - r0, cols, lane,
+                             [&](int v) { return acc[f][g][v] + bias; });
     }
   }
 }
@@ -212,9 +203,12 @@ __global__ __launch_bounds__(WM* WN * 64) void grouped_kernel(GroupedArgs p) {
   // accumulator v of lane l: row 8 (v / 4) + 4 (l / 32) + v % 4, column l % 32
   const int64_t orow = (OP == GROUPED_DW ? e * p.I : o0) + i0;
   const int rows = (int)(I - i0 < BM ? I - i0 : BM);
-  if (p.out_type == QMM_F32) store_tile<QMM_F32, BM, FM, FN>(p, acc, orow, rows, j0, e, wm, wn, lane);
-  else if (p.out_type == QMM_F16) store_tile<QMM_F16, BM, FM, FN>(p, acc, orow, rows, j0, e, wm, wn, lane);
-  else store_tile<QMM_BF16, BM, FM, FN>(p, acc, orow, rows, j0, e, wm, wn, lane);
+  const bool pairs = p.J % 2 == 0 && (uintptr_t)p.out % 4 == 0;
+  if (p.out_type == QMM_F32) store_tile<QMM_F32, false, FM, FN>(p, acc, orow, rows, j0, e, wm, wn, lane);
+  else if (p.out_type == QMM_F16 && pairs) store_tile<QMM_F16, true, FM, FN>(p, acc, orow, rows, j0, e, wm, wn, lane);
+  else if (p.out_type == QMM_F16) store_tile<QMM_F16, false, FM, FN>(p, acc, orow, rows, j0, e, wm, wn, lane);
+  else if (pairs) store_tile<QMM_BF16, true, FM, FN>(p, acc, orow, rows, j0, e, wm, wn, lane);
+  else store_tile<QMM_BF16, false, FM, FN>(p, acc, orow, rows, j0, e, wm, wn, lane);
 }
 
 // out[e][n] = sum of dY[r][n] over the rows of expert e: a work-group takes 64 columns, 32

@@ -163,6 +163,47 @@ struct TileRead {
   }
 };
 
+// One 32 x 32 block of sums (accumulator v of lane l: row 8 (v / 4) + 4 (l / 32) + v % 4, column
+// l % 32) through f(v, sum), stored at byte offset `at` (row 0, this lane's column) of r, rows
+// `ld` bytes apart; `left` rows exist below this lane's first, `cols` columns from this lane's own.
+// PAIRS (16-bit outputs whose rows keep 4-byte alignment): neighbouring lanes exchange one of
+// every two rows, so that each stores two columns at once: half the store instructions.
+// Elements past the end address past the descriptor's range, which drops the store.
+template <int OT, bool PAIRS, typename F>
+__device__ __forceinline__ void store_block(__amdgpu_buffer_rsrc_t r, uint32_t at, uint32_t ld, int left, int cols,
+                                            int lane, F f) {
+  auto half = [](float x) { return OT == QMM_F16 ? f32_to_f16(x) : f32_to_bf16(x); };
+  if constexpr (OT == QMM_F32) {
+#pragma unroll
+    for (int v = 0; v < 16; ++v) {
+      const int dr = 8 * (v >> 2) + (v & 3);
+      const uint32_t o = dr < left && cols > 0 ? at + (uint32_t)dr * ld : kPastRange;
+      __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(f(v)), r, (int)o, 0, 0);
+    }
+  } else if constexpr (PAIRS) {
+    const bool odd = lane & 1;
+    // columns exist in pairs (even widths): a pair's lanes agree
+    const uint32_t base = odd ? at - 2u + ld : at;
+#pragma unroll
+    for (int v = 0; v < 16; v += 2) {
+      const int dr = 8 * (v >> 2) + (v & 3) + (odd ? 1 : 0);
+      const float a = f(v), b = f(v + 1);
+      const float other = dpp_f<kDppXor1>(odd ? a : b);  // even lanes get the odd one's a, odd ones the even one's b
+      const float lo = odd ? other : a, hi = odd ? b : other;
+      const uint32_t w = (uint32_t)half(lo) | ((uint32_t)half(hi) << 16);
+      const uint32_t o = dr < left && cols > 0 ? base + (uint32_t)(8 * (v >> 2) + (v & 3)) * ld : kPastRange;
+      __builtin_amdgcn_raw_buffer_store_b32(w, r, (int)o, 0, 0);
+    }
+  } else {
+#pragma unroll
+    for (int v = 0; v < 16; ++v) {
+      const int dr = 8 * (v >> 2) + (v & 3);
+      const uint32_t o = dr < left && cols > 0 ? at + (uint32_t)dr * ld : kPastRange;
+      __builtin_amdgcn_raw_buffer_store_b16(half(f(v)), r, (int)o, 0, 0);
+    }
+  }
+}
+
 // Waits until this wave's copies into LDS but the newest N, and all its LDS accesses, are
 // done, then for the other waves of the work-group: after it, every wave's copies older than
 // those are in LDS, and no wave still reads what they had read before.
