@@ -29,7 +29,7 @@ struct DgradArgs {
   int out_type;
   float* partials;  // fp32 [splits][M][K], or NULL
   // set by the launch
-  int mtiles, ktiles, tiles_grid, splits, stages;  // stages: per split
+  int mtiles, ktiles, kgroup, tiles_grid, splits, stages;  // stages: per split
 };
 
 // Splits of the contraction (a function of the shape only).

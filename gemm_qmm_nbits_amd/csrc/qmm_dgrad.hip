@@ -13,13 +13,12 @@
 // matrix instructions.
 //
 // When the tiles do not fill the chip the contraction is split; fp32 partial sums are added
-// in split order by the forward path's reduction kernel.  The sums' order depends only on
+// in split order by a second kernel.  The sums' order depends only on
 // the shape.
 #include "qmm_dequant8.h"
 #include "qmm_device.h"
 #include "qmm_dgrad.h"
 #include "qmm_internal.h"
-#include "qmm_skinny.h"
 #include "qmm_tile.h"
 
 #include <algorithm>
@@ -82,12 +81,15 @@ __global__ __launch_bounds__(WM* WN * 64) void dgrad_kernel(DgradArgs p) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
 
-  // work-groups are dealt round-robin over the 8 XCDs: the row tiles of one column tile stay
-  // on one XCD, whose L2 then reads the packed weights once
+  // work-groups are dealt round-robin over the 8 XCDs: a unit of `kgroup` column tiles of one row
+  // tile stays on one XCD, whose L2 then reads that piece of dY16 once (every row tile of a
+  // column tile on one XCD instead: dY16 was read anew for every column tile)
   const int ks = (int)blockIdx.x / p.tiles_grid;
   const int i = (int)blockIdx.x - ks * p.tiles_grid;
-  const int kt = ((i >> 3) / p.mtiles) * 8 + (i & 7), mt = (i >> 3) % p.mtiles;
-  if (kt >= p.ktiles) return;
+  const int groups = (p.ktiles + p.kgroup - 1) / p.kgroup;
+  const int unit = (i >> 3) / p.kgroup * 8 + (i & 7);
+  const int mt = unit / groups, kt = unit % groups * p.kgroup + (i >> 3) % p.kgroup;
+  if (kt >= p.ktiles || mt >= p.mtiles) return;
   const int64_t m0 = (int64_t)mt * BM, k0 = (int64_t)kt * BN;
   const int total = (int)((p.N + kStage - 1) / kStage);
   const int s0 = ks * p.stages;
@@ -241,6 +243,44 @@ __global__ __launch_bounds__(WM* WN * 64) void dgrad_kernel(DgradArgs p) {
   else dgrad_store<QMM_BF16, false, FM, FN>(p.out, p.row_scale, acc, p.M, p.K, m0, k0, wm, wn, lane);
 }
 
+// out = rs[m] * (((P[0] + P[1]) + ...) + P[S - 1]): four columns per thread, eight splits' loads
+// under way at once.
+__global__ __launch_bounds__(256) void dgrad_reduce_kernel(const float* P, int S, int64_t M, int64_t K, const float* rs,
+                                                           void* out, int out_type) {
+  const int64_t total = M * K, quads = (total + 3) / 4;
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (i >= quads * 4) return;
+  const int n = total - i < 4 ? (int)(total - i) : 4;
+  float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (n == 4 && total % 4 == 0) {
+    for (int s = 0; s < S; s += 8) {
+      f32x4 u[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) u[e] = *(const f32x4*)(P + (s + e < S ? s + e : S - 1) * total + i);
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (s + e < S)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) v[k] += u[e][k];
+    }
+  } else {
+    for (int k = 0; k < n; ++k)
+      for (int s = 0; s < S; ++s) v[k] += P[s * total + i + k];
+  }
+  if (rs)
+    for (int k = 0; k < n; ++k) v[k] *= rs[(i + k) / K];
+  if (n == 4 && out_type == QMM_F32 && (uintptr_t)out % 16 == 0) {
+    *(f32x4*)((float*)out + i) = f32x4{v[0], v[1], v[2], v[3]};
+  } else if (n == 4 && out_type != QMM_F32 && (uintptr_t)out % 8 == 0) {
+    uint32_t h[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) h[k] = out_type == QMM_F16 ? f32_to_f16(v[k]) : f32_to_bf16(v[k]);
+    *(uint2*)((uint16_t*)out + i) = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+  } else {
+    for (int k = 0; k < n; ++k) store_elem_rt(out, out_type, i + k, v[k]);
+  }
+}
+
 struct TileSize {
   int m, k;
 };
@@ -294,7 +334,8 @@ hipError_t launch_dgrad(DgradArgs p, hipStream_t st) {
   const TileSize t = tile_size(p.M);
   p.mtiles = (int)((p.M + t.m - 1) / t.m);
   p.ktiles = (int)((p.K + t.k - 1) / t.k);
-  p.tiles_grid = (p.ktiles + 7) / 8 * 8 * p.mtiles;
+  p.kgroup = unit_tiles(p.mtiles, p.ktiles);
+  p.tiles_grid = (int)unit_slots(p.mtiles, p.ktiles, p.kgroup);
   p.splits = p.partials ? dgrad_splits(p.M, p.K, p.N) : 1;
   const int64_t stages = (p.N + kStage - 1) / kStage;
   p.stages = (int)((stages + p.splits - 1) / p.splits);
@@ -305,7 +346,8 @@ hipError_t launch_dgrad(DgradArgs p, hipStream_t st) {
   else if (p.bits == 8) go_zk<8>(p, st);
   else go_zk<4>(p, st);
   if (p.splits > 1)
-    return launch_reduce_splits(p.partials, p.splits, p.M, p.K, p.K, p.row_scale, nullptr, p.out, p.out_type, st);
+    launch(dgrad_reduce_kernel, dim3((unsigned)((p.M * p.K + 1023) / 1024)), dim3(256), 0, st, p.partials, p.splits, p.M,
+           p.K, p.row_scale, p.out, p.out_type);
   return hipSuccess;
 }
 
