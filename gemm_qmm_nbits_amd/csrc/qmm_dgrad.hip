@@ -180,7 +180,10 @@ __global__ __launch_bounds__(WM* WN * 64) void dgrad_kernel(DgradArgs p) {
   for (int f = 0; f < FM; ++f)
 #pragma unroll
     for (int g = 0; g < FN; ++g) acc[f][g] = f32x16{};
+  // a wave whose part of the tile holds no output only copies, dequantizes and keeps the barriers
+  const bool active = wm * FM * 32 < p.M - m0 && wn * FN * 32 < p.K - k0;
   auto half_stage = [&](const uint8_t* ta, const uint8_t* tb, int h) {
+    if (!active) return;
     uint4 fa[FM], fb[FN];
 #pragma unroll
     for (int f = 0; f < FM; ++f) fa[f] = ra.get(ta, f, h, lane);
@@ -232,6 +235,7 @@ __global__ __launch_bounds__(WM* WN * 64) void dgrad_kernel(DgradArgs p) {
   // no copy may still be on its way when the work-group gives its LDS back
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 
+  if (!active) return;
   const bool pairs = p.K % 2 == 0 && (uintptr_t)p.out % 4 == 0;
   if (p.splits > 1)
     dgrad_store<QMM_F32, false, FM, FN>(p.partials + (int64_t)ks * p.M * p.K, nullptr, acc, p.M, p.K, m0, k0, wm, wn, lane);

@@ -161,7 +161,11 @@ __global__ __launch_bounds__(WM* WN * 64) void grouped_kernel(GroupedArgs p) {
     la.stage(s, t, wave, lane);
     lb.stage(s, t + BM * 2 * KS, wave, lane);
   };
+  // a wave whose part of the tile holds no output only copies and keeps the barriers: a tile of
+  // few rows then takes a few waves' time
+  const bool active = wm * FM * 32 < I - i0 && wn * FN * 32 < p.J - j0;
   auto compute = [&](const uint8_t* ta) {
+    if (!active) return;
     const uint8_t* tb = ta + BM * 2 * KS;
 #pragma unroll
     for (int h = 0; h < KS / 16; ++h) {
@@ -200,7 +204,7 @@ __global__ __launch_bounds__(WM* WN * 64) void grouped_kernel(GroupedArgs p) {
   // no copy may still be on its way when the work-group gives its LDS back
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 
-  // accumulator v of lane l: row 8 (v / 4) + 4 (l / 32) + v % 4, column l % 32
+  if (!active) return;
   const int64_t orow = (OP == GROUPED_DW ? e * p.I : o0) + i0;
   const int rows = (int)(I - i0 < BM ? I - i0 : BM);
   const bool pairs = p.J % 2 == 0 && (uintptr_t)p.out % 4 == 0;
@@ -211,12 +215,15 @@ __global__ __launch_bounds__(WM* WN * 64) void grouped_kernel(GroupedArgs p) {
   else store_tile<QMM_BF16, false, FM, FN>(p, acc, orow, rows, j0, e, wm, wn, lane);
 }
 
-// out[e][n] = sum of dY[r][n] over the rows of expert e: a work-group takes 64 columns, 32
-// threads down the rows (each sums every 32nd row, in order), then adds the 32 sums in order.
+// out[e][n] = sum of dY[r][n] over the rows of expert e: a work-group takes 64 columns, 128
+// threads down the rows (each sums every 128th row, in order), then adds the 128 sums in order.
+constexpr int kBiasThreads = 1024, kBiasRows = kBiasThreads / 8;
+
 template <int TY, bool VEC>
-__global__ __launch_bounds__(256) void bias_grad_kernel(const uint16_t* dY, int64_t R, int64_t N, const int32_t* offsets,
-                                                       void* out, int out_type) {
-  __shared__ float red[32][65];
+__global__ __launch_bounds__(kBiasThreads) void bias_grad_kernel(const uint16_t* dY, int64_t R, int64_t N,
+                                                                const int32_t* offsets, void* out, int out_type) {
+  __shared__ float red[kBiasRows][65];
+  __shared__ float part[16][64];
   const int64_t e = blockIdx.y;
   const int o0 = clamp_off(offsets, e, (int)R), o1 = clamp_off(offsets, e + 1, (int)R);
   const int c8 = threadIdx.x & 7, rr = threadIdx.x >> 3;
@@ -226,7 +233,7 @@ __global__ __launch_bounds__(256) void bias_grad_kernel(const uint16_t* dY, int6
   for (int i = 0; i < 8; ++i) sum[i] = 0.0f;
   if (col < N) {
 #pragma unroll 4
-    for (int64_t r = o0 + rr; r < o1; r += 32) {
+    for (int64_t r = o0 + rr; r < o1; r += kBiasRows) {
       const uint16_t* p = dY + r * N + col;
       if constexpr (VEC) {
         const uint4 u = *(const uint4*)p;
@@ -246,10 +253,19 @@ __global__ __launch_bounds__(256) void bias_grad_kernel(const uint16_t* dY, int6
 #pragma unroll
   for (int i = 0; i < 8; ++i) red[rr][c8 * 8 + i] = sum[i];
   __syncthreads();
+  {
+    const int c = threadIdx.x & 63, w = threadIdx.x >> 6;  // 16 waves, 8 sums each
+    float v = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kBiasRows / 16; ++i) v += red[w * (kBiasRows / 16) + i][c];
+    part[w][c] = v;
+  }
+  __syncthreads();
   if (threadIdx.x < 64) {
     const int64_t n = (int64_t)blockIdx.x * 64 + threadIdx.x;
     float v = 0.0f;
-    for (int i = 0; i < 32; ++i) v += red[i][threadIdx.x];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v += part[i][threadIdx.x];
     if (n < N) store_elem_rt(out, out_type, e * N + n, v);
   }
 }
@@ -267,15 +283,17 @@ void go_tile(GroupedArgs p, hipStream_t st) {
 
 // Tile by the mean rows of an expert (bf16, us; 32 experts of 5760 x 2880, even routing):
 //   mean rows          32        64        96       128
-//   MM  64 x 128      232       312       402       475
-//       128 x 256     218       226       282       322
-//       256 x 256     240       252       262       280
-//   DX  64 x 128      190       282       349       420
-//       128 x 256     206       227       249       322
-//       256 x 256     279       275       278       287
-//   DW  128 x 128     369       422       509       634
-//       256 x 256     400       409       458       495
-// (128 experts of 1536 x 2048, mean 32: MM 160 / 195 / 210, DX 161 / 152 / 181, DW 280 / 304.)
+//   MM  64 x 128      220       298       396       475
+//       128 x 256     218       224       240       316
+//       256 x 256     232       238       245       260
+//   DX  64 x 128      189       278       359       442
+//       128 x 256     204       223       246       328
+//       256 x 256     213       229       251       280
+//   DW  128 x 128     360       415       494       589
+//       256 x 256     399       404       469       495
+// (128 experts of 1536 x 2048, mean 32: MM 158 / 195 / 206, DX 161 / 150 / 161, DW 275 / 304; mean
+// 128: MM 364 / 238 / 225, DX 311 / 214 / 194, DW 457 / 351.)  One expert of 8192^3: MM 1068, DX
+// 1250, DW 1288 TFLOP/s; MM trails because its operands' rows come in 64-byte pieces.
 template <int TY, int OP>
 void go_op(const GroupedArgs& p, hipStream_t st) {
   const int64_t mean = (p.R + p.E - 1) / p.E;
@@ -288,7 +306,7 @@ void go_op(const GroupedArgs& p, hipStream_t st) {
     else go_tile<TY, 256, 256, 4, 2, OP>(p, st);
   } else {
     if (mean <= 32) go_tile<TY, 64, 128, 1, 4, OP>(p, st);
-    else if (mean <= 96) go_tile<TY, 128, 256, 2, 4, OP>(p, st);
+    else if (mean <= 80) go_tile<TY, 128, 256, 2, 4, OP>(p, st);
     else go_tile<TY, 256, 256, 4, 2, OP>(p, st);
   }
 }
@@ -311,7 +329,8 @@ hipError_t launch_grouped(GroupedArgs p, hipStream_t st) {
 hipError_t launch_grouped_bias_grad(const void* dY, int type, int64_t R, int64_t N, int64_t E, const int32_t* offsets,
                                     void* out, int out_type, int vec, hipStream_t st) {
   const dim3 grid((unsigned)((N + 63) / 64), (unsigned)E);
-  auto go = [&](auto kern) { launch(kern, grid, dim3(256), 0, st, (const uint16_t*)dY, R, N, offsets, out, out_type); };
+  auto go = [&](auto kern) { launch(kern, grid, dim3(kBiasThreads), 0, st, (const uint16_t*)dY, R, N, offsets, out, out_type);
+  };
   if (type == QMM_F16) vec ? go(bias_grad_kernel<QMM_F16, true>) : go(bias_grad_kernel<QMM_F16, false>);
   else vec ? go(bias_grad_kernel<QMM_BF16, true>) : go(bias_grad_kernel<QMM_BF16, false>);
   return hipSuccess;
