@@ -294,20 +294,33 @@ void go_tile(GroupedArgs p, hipStream_t st) {
 // (128 experts of 1536 x 2048, mean 32: MM 158 / 195 / 206, DX 161 / 150 / 161, DW 275 / 304; mean
 // 128: MM 364 / 238 / 225, DX 311 / 214 / 194, DW 457 / 351.)  One expert of 8192^3: MM 1068, DX
 // 1250, DW 1288 TFLOP/s; MM trails because its operands' rows come in 64-byte pieces.
+//
+// Few tiles: the largest tile of which about 128 work-groups come together, as half of the
+// compute units on a larger tile lose to all of them on a smaller one (us, 256 x 256 / 128 x 128 /
+// 64 x 128; tiles in brackets): 512 x 5120 x 5120 MM 119 (40) / 53 (160) / 78 (320); 2048 x 5120 x
+// 5120 MM 130 (160) / 147 / 234; 1024 x 4096 x 1024 MM 92 (16) / 39 (64) / 31 (128), DW 29 (64) / 17
+// (256) / 15; 4 experts, 1521 rows, 448 x 1408: DX 41 (16) / 20 (56) / 15 (104), DW 17 (48) / 10 / 9.
 template <int TY, int OP>
 void go_op(const GroupedArgs& p, hipStream_t st) {
+  constexpr int64_t kEnough = 128;
   const int64_t mean = (p.R + p.E - 1) / p.E;
+  auto tiles = [&](int64_t bm, int64_t bn) {
+    const int64_t rows = OP == GROUPED_DW ? p.E * ((p.I + bm - 1) / bm) : (p.R + bm - 1) / bm + std::min(p.E, p.R) / 2;
+    return rows * ((p.J + bn - 1) / bn);
+  };
   if constexpr (OP == GROUPED_DW) {
     // (outputs up to 128 wide or high would leave half of the larger tile unused; 16-bit outputs
     // are written in longer pieces by it at any mean: 2048 x 768 x 128 experts, mean 16, fp16 out:
     // 87 against 113 us)
-    const bool small = p.I <= 128 || p.J <= 128;
-    if (small || (mean <= 48 && p.out_type == QMM_F32)) go_tile<TY, 128, 128, 2, 2, OP>(p, st);
-    else go_tile<TY, 256, 256, 4, 2, OP>(p, st);
+    const bool narrow = p.I <= 128 || p.J <= 128 || (mean <= 48 && p.out_type == QMM_F32);
+    if (!narrow && tiles(256, 256) >= kEnough) go_tile<TY, 256, 256, 4, 2, OP>(p, st);
+    else if (tiles(128, 128) >= kEnough) go_tile<TY, 128, 128, 2, 2, OP>(p, st);
+    else go_tile<TY, 64, 128, 1, 4, OP>(p, st);
   } else {
-    if (mean <= 32) go_tile<TY, 64, 128, 1, 4, OP>(p, st);
-    else if (mean <= 80) go_tile<TY, 128, 256, 2, 4, OP>(p, st);
-    else go_tile<TY, 256, 256, 4, 2, OP>(p, st);
+    if (mean > 80 && tiles(256, 256) >= kEnough) go_tile<TY, 256, 256, 4, 2, OP>(p, st);
+    else if (mean > 80 && tiles(128, 128) >= kEnough) go_tile<TY, 128, 128, 2, 2, OP>(p, st);
+    else if (mean > 32 && mean <= 80 && tiles(128, 256) >= kEnough) go_tile<TY, 128, 256, 2, 4, OP>(p, st);
+    else go_tile<TY, 64, 128, 1, 4, OP>(p, st);
   }
 }
 

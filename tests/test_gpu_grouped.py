@@ -96,7 +96,11 @@ def test_misaligned(rows):
     check(p, "bf16", "bf16", "f32")
 
 
-@pytest.mark.parametrize("counts,K,N", [([17] * 32, 2880, 5760), ([200, 10, 0, 500], 2048, 1536)])
+# every tile height of the rule on the rows and tiles: 64 (few tiles, or few rows), 128 x 128, 128 x
+# 256 and 256 x 256, whole and with a few rows over
+@pytest.mark.parametrize("counts,K,N", [([17] * 32, 2880, 5760), ([200, 10, 0, 500], 2048, 1536), ([800], 2600, 2608),
+                                        ([60] * 24, 1032, 1544), ([1030, 3, 517, 900], 2904, 3000), ([800], 2601, 2603),
+                                        ([60] * 24, 1033, 1545), ([1500, 1, 900], 2901, 3001)])
 def test_layer_sizes(counts, K, N):
     """The expert layers' own sizes, a few rows per expert and skewed ones."""
     check(Problem(counts, K, N, "bf16", seed=11, out="bf16"), "bf16", "bf16", "bf16")
