@@ -18,13 +18,16 @@ constexpr int kLoraRankChunk = 64;  // ranks per work-group of the kernels that 
 inline int lora_rank_pad(int r) { return (r + 15) / 16 * 16; }
 
 // Rows sorted by adapter (rows without one last, as group L), and the tiles of that order.
-// Group a owns positions off[a] .. off[a+1]-1 and the tile slots off[a] / 64 + a + j for
-// j < ceil(rows / 64); the slots between are empty (count 0).
+// Group a owns positions off[a] .. off[a+1]-1 and the tile slots first + j, j < ceil(rows / 64),
+// with first = off[a] / 64 + a, or off[a] where that numbering has fewer slots (more adapters
+// loaded than rows in the batch); the slots between are empty (count 0).
 struct LoraPlan {
   int32_t* off;    // [L + 2]
   int32_t* perm;   // [M] row at each position
-  int32_t* tiles;  // [M / 64 + L + 2][4] group, first position, rows, 0
+  int32_t* tiles;  // [slots][4] group, first position, rows, 0
 };
+__host__ __device__ inline bool lora_slots_by_row(int64_t M, int64_t L) { return M <= M / kLoraTile + L + 2; }
+inline int64_t lora_tile_slots(int64_t M, int64_t L) { return lora_slots_by_row(M, L) ? M : M / kLoraTile + L + 2; }
 
 struct LoraArgs {
   int64_t M, K, N;

@@ -163,8 +163,11 @@ __global__ __launch_bounds__(kPlanThreads) void lora_plan_kernel(const int32_t* 
     if (a == L) plan.off[L + 1] = (int32_t)M;
   }
   // the group's tile slots, and the empty ones up to the next group's
-  const int64_t slot0 = first / kLoraTile + a;
-  const int64_t slot1 = a == L ? M / kLoraTile + L + 2 : (int64_t)(first + count) / kLoraTile + a + 1;
+  const bool by_row = lora_slots_by_row(M, L);
+  const int64_t slot0 = by_row ? first : first / kLoraTile + a;
+  const int64_t slot1 = by_row    ? first + count
+                        : a == L ? M / kLoraTile + L + 2
+                                 : (int64_t)(first + count) / kLoraTile + a + 1;
   for (int64_t s = slot0 + tid; s < slot1; s += kPlanThreads) {
     const int64_t at = (s - slot0) * kLoraTile;
     const int64_t left = count - at;
@@ -828,18 +831,20 @@ struct Chunk {
 };
 
 __device__ __forceinline__ Chunk find_chunk(const LoraOuterArgs& p, int64_t slot) {
-  // largest a with off[a] / chunk + a <= slot
+  // largest a whose first slot is not past `slot`
+  const bool by_row = lora_slots_by_row(p.M, p.L);
+  auto first = [&](int64_t a) { return by_row ? (int64_t)p.plan.off[a] : p.plan.off[a] / p.chunk + a; };
   int64_t lo = 0, hi = p.L;  // a in [0, L)
   while (lo + 1 < hi) {
     const int64_t mid = (lo + hi) >> 1;
-    if (p.plan.off[mid] / p.chunk + mid <= slot) lo = mid;
+    if (first(mid) <= slot) lo = mid;
     else hi = mid;
   }
   Chunk c;
   c.a = lo;
   const int o0 = p.plan.off[lo], o1 = p.plan.off[lo + 1];
   c.chunks = (o1 - o0 + p.chunk - 1) / p.chunk;
-  c.index = (int)(slot - (o0 / p.chunk + lo));
+  c.index = (int)(slot - first(lo));
   c.begin = o0 + c.index * p.chunk;
   c.end = c.begin + p.chunk < o1 ? c.begin + p.chunk : o1;
   return c;
@@ -1011,7 +1016,8 @@ hipError_t expand(LoraArgs p, const float* dT, hipStream_t st) {
   p.slices = (int)std::min<int64_t>((4096 + tiles - 1) / tiles, most);
   // a tile's 16-row parts go apart where the tiles' slices alone leave compute units idle
   // (333 x 5755: 24.6 -> 15.1 us), and where 64 rows of t would not fit in LDS
-  const int apart = (tiles * p.slices < 1024 && p.M > 16) || p.r > 64 ? 4 : 1;
+  // (FEW is planned for 16 rows' parts)
+  const int apart = (p.M > 16 && (p.few || tiles * p.slices < 1024)) || p.r > 64 ? 4 : 1;
   const dim3 grid((unsigned)p.slots * (unsigned)p.slices, apart);
   uint32_t lds = (uint32_t)(kLoraTile / apart * Pieces<TY>(p.r).row_bytes());
   if (p.few) {
@@ -1094,7 +1100,8 @@ int lora_outer_chunk(int64_t M, int64_t blocks) {
 
 hipError_t launch_lora_outer(const LoraOuterArgs& p, hipStream_t st) {
   if (p.M > 0) {
-    const dim3 grid((unsigned)(p.M / p.chunk + p.L + 1), (unsigned)(p.side[0].blocks + p.side[1].blocks),
+    const int64_t slots = lora_slots_by_row(p.M, p.L) ? p.M : p.M / p.chunk + p.L + 1;
+    const dim3 grid((unsigned)slots, (unsigned)(p.side[0].blocks + p.side[1].blocks),
                     (unsigned)((p.r + kLoraRankChunk - 1) / kLoraRankChunk));
     p.type == QMM_F16 ? outer_nf<QMM_F16>(p, grid, st) : outer_nf<QMM_BF16>(p, grid, st);
   }

@@ -39,8 +39,6 @@ struct Layout {
 
 int col_blocks(int64_t P) { return (int)((P + 127) / 128); }
 
-int64_t tile_slots(int64_t M, int64_t L) { return M / kLoraTile + L + 2; }
-
 Layout layout(int64_t M, int64_t K, int64_t N, int r, int64_t L, bool grad) {
   Layout w;
   size_t at = 0;
@@ -50,7 +48,7 @@ Layout layout(int64_t M, int64_t K, int64_t N, int r, int64_t L, bool grad) {
     w.perm = at;
     at += up256((size_t)M * 4);
     w.tiles = at;
-    at += up256((size_t)tile_slots(M, L) * 16);
+    at += up256((size_t)lora_tile_slots(M, L) * 16);
   }
   const size_t rp = (size_t)lora_rank_pad(r);
   const int s = grad ? std::max(splits(M, K), splits(M, N)) : splits(M, K);
@@ -140,7 +138,7 @@ LoraArgs make_args(int type, int64_t M, int64_t K, int64_t N, int r, int64_t L, 
   p.B = w.B;
   p.scale = w.scale;
   p.use_plan = plan ? 1 : 0;
-  p.slots = plan ? (int)tile_slots(M, L) : (int)M;
+  p.slots = plan ? (int)lora_tile_slots(M, L) : (int)M;
   p.plan.off = (int32_t*)(ws + l.off);
   p.plan.perm = (int32_t*)(ws + l.perm);
   p.plan.tiles = (int32_t*)(ws + l.tiles);

@@ -548,10 +548,19 @@ def _handle(stream, dev):
     return _types().current(dev) if stream is None else stream.cuda_stream
 
 
-def _scratch(workspace, need, like):
-    """Address and size of the workspace, allocated here when not given."""
+def _new(shape, dtype, like, stream):
+    """A tensor of the caching allocator for a call on `stream`: where that is not the stream the
+    allocator hands it out on, its memory is not reused before the call has run."""
+    t = _types().torch.empty(shape, dtype=dtype, device=like.device)
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
+def _scratch(workspace, need, like, stream):
+    """The workspace, allocated here when not given, its address and size."""
     if workspace is None:
-        workspace = _types().torch.empty(need, dtype=_types().torch.uint8, device=like.device)
+        workspace = _new(need, _types().torch.uint8, like, stream)
         return workspace, workspace.data_ptr(), need
     if not workspace.is_contiguous() or workspace.get_device() != like.get_device():
         raise ValueError("workspace must be contiguous and on the device of the call")
@@ -598,9 +607,9 @@ def qmm_lora_add(X, A, B, ids, scale=None, base=None, out=None, out_dtype=None, 
     base_p, base_t = _optional(base, "base", (M, N), ty.any, dev)
     T_p, _ = _optional(T, "T", (M, r), ty.f32, dev)
     if out is None:
-        out = ty.torch.empty((M, N), dtype=out_dtype or X.dtype, device=X.device)
+        out = _new((M, N), out_dtype or X.dtype, X, stream)
     out_t = _expect(out, "out", (M, N), ty.any, dev)
-    keep, ws, wsb = _scratch(workspace, _bytes_of("qmm_lora_add_workspace_bytes", M, K, N, r, L), X)
+    keep, ws, wsb = _scratch(workspace, _bytes_of("qmm_lora_add_workspace_bytes", M, K, N, r, L), X, stream)
     st = lib().qmm_lora_add(X.data_ptr(), code, M, K, N, r, L, ids.data_ptr(), w, base_p, base_t, out.data_ptr(),
                             out_t, T_p, ws, wsb, _handle(stream, dev))
     _check("qmm_lora_add", st)
@@ -615,22 +624,21 @@ def qmm_lora_grad(dY, X, A, B, ids, scale=None, T=None, base=None, dX=None, dA=N
     dB[a] = scale[a] sum dY[m] T[m]^T.  T: kept from qmm_lora_add, or None (computed again).
     dX is of dx_dtype (default X's), dA and dB of grad_dtype (default fp32)."""
     ty, dev, code, M, K, N, r, L, w = _lora_shapes(X, A, B, ids, scale)
-    empty = ty.torch.empty
     _expect(dY, "dY", (M, N), ty.only[X.dtype], dev)
     T_p, _ = _optional(T, "T", (M, r), ty.f32, dev)
     base_p, base_t = _optional(base, "base", (M, K), ty.any, dev)
     if dX is None and need[0]:
-        dX = empty((M, K), dtype=dx_dtype or X.dtype, device=X.device)
+        dX = _new((M, K), dx_dtype or X.dtype, X, stream)
     if dA is None and need[1]:
-        dA = empty((L, r, K), dtype=grad_dtype or ty.torch.float32, device=X.device)
+        dA = _new((L, r, K), grad_dtype or ty.torch.float32, X, stream)
     if dB is None and need[2]:
-        dB = empty((L, N, r), dtype=grad_dtype or ty.torch.float32, device=X.device)
+        dB = _new((L, N, r), grad_dtype or ty.torch.float32, X, stream)
     dX_p, dX_t = _optional(dX, "dX", (M, K), ty.any, dev)
     dA_p, dA_t = _optional(dA, "dA", (L, r, K), ty.any, dev)
     dB_p, dB_t = _optional(dB, "dB", (L, N, r), ty.any, dev)
     if dA is not None and dB is not None and dA_t != dB_t:
         raise TypeError("dA and dB differ in dtype")
-    keep, ws, wsb = _scratch(workspace, _bytes_of("qmm_lora_grad_workspace_bytes", M, K, N, r, L), X)
+    keep, ws, wsb = _scratch(workspace, _bytes_of("qmm_lora_grad_workspace_bytes", M, K, N, r, L), X, stream)
     st = lib().qmm_lora_grad(dY.data_ptr(), X.data_ptr(), code, M, K, N, r, L, ids.data_ptr(), w, T_p, base_p, base_t,
                              dX_p, dX_t, dA_p, dB_p, dB_t if dA is None else dA_t, ws, wsb, _handle(stream, dev))
     _check("qmm_lora_grad", st)
@@ -641,7 +649,7 @@ def qmm_lora_grad(dY, X, A, B, ids, scale=None, T=None, base=None, dX=None, dA=N
 # input gradients of low-bit projections
 # ---------------------------------------------------------------------------
 
-def _dgrad_shapes(dY, W, K, block, bits, out, out_dtype):
+def _dgrad_shapes(dY, W, K, block, bits, out, out_dtype, stream):
     """Checks dY [M, N] and the packed weights W [N, nblk, block * bits / 8]."""
     ty = _types()
     if dY.dim() != 2:
@@ -653,7 +661,7 @@ def _dgrad_shapes(dY, W, K, block, bits, out, out_dtype):
         raise ValueError(f"W does not hold {N} rows of {K} codes of {bits} bits in blocks of {block}")
     _expect(W, "W", W.shape, ty.u8, dev)
     if out is None:
-        out = ty.torch.empty((M, K), dtype=out_dtype or dY.dtype, device=dY.device)
+        out = _new((M, K), out_dtype or dY.dtype, dY, stream)
     return dev, code, M, N, out, _expect(out, "out", (M, K), ty.any, dev)
 
 
@@ -669,13 +677,13 @@ def _sized(t, name, count, dev):
 def qmm_nbits_dgrad(dY, W, scales, K, bits, block, zp=None, zp_kind=QMM_ZP_NONE, uniform_zp=0.0, out=None,
                     out_dtype=None, workspace=None, stream=None):
     """dX[M, K] = dY[M, N] . dequant(W): the input gradient of qmm_nbits, from the same weight buffers."""
-    dev, code, M, N, out, out_t = _dgrad_shapes(dY, W, K, block, bits, out, out_dtype)
+    dev, code, M, N, out, out_t = _dgrad_shapes(dY, W, K, block, bits, out, out_dtype, stream)
     nblk = nblocks(K, block)
     s_p = _sized(scales, "scales", N * nblk, dev)
     z_p = None
     if zp is not None and zp_kind in (QMM_ZP_PACKED, QMM_ZP_F16):
         z_p = _sized(zp, "zp", N * ((nblk * bits + 7) // 8 if zp_kind == QMM_ZP_PACKED else nblk), dev)
-    keep, ws, wsb = _scratch(workspace, _bytes_of("qmm_dgrad_workspace_bytes", M, K, N), dY)
+    keep, ws, wsb = _scratch(workspace, _bytes_of("qmm_dgrad_workspace_bytes", M, K, N), dY, stream)
     st = lib().qmm_nbits_dgrad(dY.data_ptr(), code, M, K, N, W.data_ptr(), bits, block, s_p, z_p, zp_kind,
                                float(uniform_zp), out.data_ptr(), out_t, ws, wsb, _handle(stream, dev))
     _check("qmm_nbits_dgrad", st)
@@ -684,10 +692,10 @@ def qmm_nbits_dgrad(dY, W, scales, K, bits, block, zp=None, zp_kind=QMM_ZP_NONE,
 
 def qmm_codebook4_dgrad(dY, W, absmax, codebook, K, block=64, out=None, out_dtype=None, workspace=None, stream=None):
     """dX[M, K] = dY[M, N] . (codebook[q] * absmax): the input gradient of qmm_codebook4."""
-    dev, code, M, N, out, out_t = _dgrad_shapes(dY, W, K, block, 4, out, out_dtype)
+    dev, code, M, N, out, out_t = _dgrad_shapes(dY, W, K, block, 4, out, out_dtype, stream)
     a_p = _sized(absmax, "absmax", N * nblocks(K, block), dev)
     c_p = _sized(codebook, "codebook", 16, dev)
-    keep, ws, wsb = _scratch(workspace, _bytes_of("qmm_dgrad_workspace_bytes", M, K, N), dY)
+    keep, ws, wsb = _scratch(workspace, _bytes_of("qmm_dgrad_workspace_bytes", M, K, N), dY, stream)
     st = lib().qmm_codebook4_dgrad(dY.data_ptr(), code, M, K, N, W.data_ptr(), block, a_p, c_p, out.data_ptr(), out_t,
                                    ws, wsb, _handle(stream, dev))
     _check("qmm_codebook4_dgrad", st)
@@ -721,7 +729,7 @@ def qmoe_grouped_mm(X, row_offsets, W, bias=None, out=None, out_dtype=None, stre
     X [R, K], W [E, N, K] fp16 or bf16; bias [E, N] of the output's dtype (default X's)."""
     ty, dev, code, R, K, N, E = _grouped_shapes(X, W, row_offsets)
     if out is None:
-        out = ty.torch.empty((R, N), dtype=out_dtype or X.dtype, device=X.device)
+        out = _new((R, N), out_dtype or X.dtype, X, stream)
     out_t = _expect(out, "out", (R, N), ty.any, dev)
     b_p, _ = _optional(bias, "bias", (E, N), ty.only[out.dtype], dev)
     st = lib().qmoe_grouped_mm(X.data_ptr(), code, R, K, N, E, row_offsets.data_ptr(), W.data_ptr(), b_p,
@@ -737,14 +745,13 @@ def qmoe_grouped_mm_grad(dY, X, row_offsets, W, dX=None, dW=None, dbias=None, dx
     dX[r] = dY[r] W[e] of dx_dtype (default X's); dW[e] = sum dY[r]^T X[r] and dbias[e] = sum dY[r]
     over the rows of expert e, of dw_dtype (default X's)."""
     ty, dev, code, R, K, N, E = _grouped_shapes(X, W, row_offsets)
-    empty = ty.torch.empty
     _expect(dY, "dY", (R, N), ty.only[X.dtype], dev)
     if dX is None and need[0]:
-        dX = empty((R, K), dtype=dx_dtype or X.dtype, device=X.device)
+        dX = _new((R, K), dx_dtype or X.dtype, X, stream)
     if dW is None and need[1]:
-        dW = empty((E, N, K), dtype=dw_dtype or X.dtype, device=X.device)
+        dW = _new((E, N, K), dw_dtype or X.dtype, X, stream)
     if dbias is None and need_dbias:
-        dbias = empty((E, N), dtype=dw_dtype or (X.dtype if dW is None else dW.dtype), device=X.device)
+        dbias = _new((E, N), dw_dtype or (X.dtype if dW is None else dW.dtype), X, stream)
     dX_p, dX_t = _optional(dX, "dX", (R, K), ty.any, dev)
     dW_p, dW_t = _optional(dW, "dW", (E, N, K), ty.any, dev)
     db_p, db_t = _optional(dbias, "dbias", (E, N), ty.any, dev)

@@ -101,6 +101,7 @@ SIZES = [
     (1, 256, 64, 16, 1), (1, 5120, 640, 16, 8), (2, 257, 33, 1, 3), (3, 1, 1, 1, 1), (5, 8, 4, 4, 2),
     (17, 320, 100, 8, 4), (63, 96, 130, 24, 70), (64, 512, 256, 32, 5), (65, 512, 256, 64, 5), (66, 77, 51, 5, 2),
     (16, 8200, 200, 64, 1), (8, 8200, 200, 32, 3), (40, 96, 300, 256, 3),
+    (70, 128, 192, 16, 900), (20, 64, 300000, 8, 2),
     (130, 1000, 300, 100, 6), (333, 264, 72, 48, 3), (500, 640, 200, 130, 2), (1100, 128, 64, 16, 40),
 ]
 
