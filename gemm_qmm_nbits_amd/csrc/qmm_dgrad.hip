@@ -12,6 +12,13 @@
 // s + 1 (loaded two stages ago) are dequantized between the two halves of the stage's
 // matrix instructions.
 //
+// 2048 x 5120 x 7680, 4-bit, block 64: 187 us, 861 TFLOP/s (the dense kernel of qmm_grouped.hip at
+// 8192^3: 1250), matrix units about half busy, the rest waits and dequantization (28% of the vector
+// issue slots), plus 20 us for the cast of dY and 32 for the three splits' sums; with every row
+// tile of a column tile on one XCD, so that dY16 was read anew per column tile, 258 us.  16 rows,
+// codebook, 4096 x 14336: 24 us against 6.6 for its bytes, bound by the codebook's LDS reads and the
+// dequantization's vector instructions (about 40% busy each) between barriers.
+//
 // When the tiles do not fill the chip the contraction is split; fp32 partial sums are added
 // in split order by a second kernel.  The sums' order depends only on
 // the shape.

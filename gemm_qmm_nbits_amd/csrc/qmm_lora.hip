@@ -15,9 +15,8 @@
 //
 // Numbers: t and dt stay in fp32.  Products of two 16-bit operands use the 16-bit matrix
 // instructions (exact products, fp32 sums).  Products with t or dt take them as sums of 16-bit
-// pieces (expand) or the 16-bit operand widened to fp32 (outer sums), so nothing is rounded
-// below fp32 before the output.  Every sum has a fixed order (no atomics): repeated calls give the
-// same bits.
+// pieces (expand: exact for bf16, 22 bits for fp16) or the 16-bit operand widened to fp32 (outer
+// sums).  Every sum has a fixed order (no atomics in them): repeated calls give the same bits.
 #include "qmm_device.h"
 #include "qmm_internal.h"
 #include "qmm_lora.h"
@@ -227,6 +226,10 @@ __device__ __forceinline__ int64_t position(const LoraArgs& p, const Tile& t, co
 // sums are added in wave order through LDS.  TR: B_a is [N][r], its ranks run along the
 // row, so a wave copies 64 rows into LDS and reads them back transposed
 // (ds_read_b64_tr_b16).  NF: 16-rank fragments (1, 2 or 4).
+//
+// 1 row of 5120: 3.7 us (20 splits: a launch's own time); 4096 x 5120, rank 32: 19 us for 42 MB; dY
+// of 8192 x 5120, rank 16: 26 us for 84 MB (3.2 TB/s).  The next step's loads issued ahead: slower
+// (22 us, rank 32), the registers cost a wave per SIMD.
 template <int TY, int NF, bool TR>
 __global__ __launch_bounds__(LT) void lora_shrink_kernel(LoraArgs p) {
   constexpr int RS = NF * 16 + 8;  // LDS row of the transposed operand (16-bit elements)
@@ -383,8 +386,10 @@ __device__ __forceinline__ f32x4 sum_parts(const LoraArgs& p, const float* q) {
 // Rows need no alignment (a vector access may start at any element).  The last group of a
 // width that is no multiple of 64 starts at width - 64 and stores its new columns only.
 //
-// (fp32 matrix instructions on widened operands: 280 us for 4096 x 35840 at rank 32, most of
-// it vector instructions; a copy of that base and output alone takes 150 to 175.)
+// 4096 x 35840, rank 32, fp32 base, bf16 out: 196 us for 881 MB (4.5 TB/s); a kernel that only copies
+// that base to that output takes 150 to 175.  dX of 8192 x 5120, rank 16: 64 us for 252 MB.  (Lanes
+// that keep their matrix layout and write 32-byte pieces of 16 rows: 485 us; t summed from the
+// splits in every work-group: 286.)
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 // Four elements of base as loaded.
@@ -824,6 +829,10 @@ __global__ __launch_bounds__(LT) void lora_expand_narrow_kernel(LoraArgs p, cons
 // written at once; the chunks of larger ones go to `part` (slot 2 off / chunk + j) and are
 // added in order by lora_outer_reduce_kernel, which also writes the zeros of adapters without
 // rows.
+//
+// 8192 rows, 5120 + 5120 columns, rank 16: 52 us for 168 MB read (3.2 TB/s), 5 us the reduction; the
+// matrix instructions take about 18 us of it.  Loading the next 16 rows during the arithmetic
+// costs a wave per SIMD in registers and is slower (68 us).
 struct Chunk {
   int64_t a;
   int begin, end;  // positions
@@ -851,7 +860,7 @@ __device__ __forceinline__ Chunk find_chunk(const LoraOuterArgs& p, int64_t slot
 }
 
 template <int TY, int NF>
-__global__ __launch_bounds__(LT, NF == 1 ? 4 : NF == 2 ? 3 : 2) void lora_outer_kernel(LoraOuterArgs p) {
+__global__ __launch_bounds__(LT, NF == 1 ? 4 : NF == 2 ? 3 : 1) void lora_outer_kernel(LoraOuterArgs p) {
   __shared__ __attribute__((aligned(16))) float red[2][8 * NF * 4 * 64];
   const Chunk ch = find_chunk(p, blockIdx.x);
   if (ch.index >= ch.chunks) return;

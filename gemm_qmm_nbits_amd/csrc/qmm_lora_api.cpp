@@ -11,7 +11,8 @@ using namespace qmm;
 
 namespace {
 
-constexpr int64_t kMaxM = 1LL << 24, kMaxDim = 1LL << 22, kMaxAdapters = 32768, kMaxRank = 512;
+// (the outer sums' grid has a work-group row per 128 columns of both sides, below 2^16)
+constexpr int64_t kMaxM = 1LL << 24, kMaxDim = 1LL << 21, kMaxAdapters = 32768, kMaxRank = 512;
 
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }

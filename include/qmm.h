@@ -468,9 +468,8 @@ qmm_status qmm_validate_grouped_mm_grad(const void* dY, const void* X, int type,
  *         qmm_lora_grad reads it, or computes it again from X when NULL.
  *   dX / dA / dB of qmm_lora_grad: each may be NULL (not computed).  dA [L][r][K] and dB
  *         [L][N][r] of g_type.
- *   M <= 2^24, 1 <= K, N <= 2^22, 1 <= r <= 512, 1 <= L <= 32768.  Any sizes and element
- *   alignment are served; rows of 16-byte multiples (K, N, r multiples of 8, 16-byte
- *   aligned tensors) take the vector loads.
+ *   M <= 2^24, 1 <= K, N <= 2^21, 1 <= r <= 512, 1 <= L <= 32768.  Any sizes and element
+ *   alignment are served; 16-byte aligned tensors with K, N, r multiples of 8 are the fastest.
  *   workspace: at least the bytes of the query, 256-byte aligned.  Calls that share a
  *   workspace must not overlap.  The sums' order depends only on the shape and the ids.
  * ------------------------------------------------------------------------- */

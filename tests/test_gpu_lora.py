@@ -101,7 +101,7 @@ SIZES = [
     (1, 256, 64, 16, 1), (1, 5120, 640, 16, 8), (2, 257, 33, 1, 3), (3, 1, 1, 1, 1), (5, 8, 4, 4, 2),
     (17, 320, 100, 8, 4), (63, 96, 130, 24, 70), (64, 512, 256, 32, 5), (65, 512, 256, 64, 5), (66, 77, 51, 5, 2),
     (16, 8200, 200, 64, 1), (8, 8200, 200, 32, 3), (40, 96, 300, 256, 3),
-    (70, 128, 192, 16, 900), (20, 64, 300000, 8, 2),
+    (70, 128, 192, 16, 900), (20, 64, 300000, 8, 2), (20, 64, 96, 512, 2), (90, 200, 72, 300, 2),
     (130, 1000, 300, 100, 6), (333, 264, 72, 48, 3), (500, 640, 200, 130, 2), (1100, 128, 64, 16, 40),
 ]
 
@@ -270,6 +270,10 @@ def test_repeats_streams_and_graph(M):
     side.synchronize()
     for v, want in zip(outs, ref):
         assert np.array_equal(host_bits(v), want)
+    side.wait_stream(t.cuda.current_stream())
+    y = Q.qmm_lora_add(p.X, p.A, p.B, p.ids, scale=p.scale, base=p.base, stream=side)   # the stream as an argument
+    side.synchronize()
+    assert np.array_equal(host_bits(y), ref[0])
     g = t.cuda.CUDAGraph()
     with t.cuda.graph(g):
         step(outs)

@@ -32,7 +32,7 @@ def test_common_refusals(f):
         assert f(**{k: -1}) == -5
     for k in ("K", "N", "r", "L"):
         assert f(**{k: 0}) == -5
-    assert f(M=(1 << 24) + 1) == -5 and f(K=(1 << 22) + 1) == -5 and f(r=513) == -5 and f(L=32769) == -5
+    assert f(M=(1 << 24) + 1) == -5 and f(K=(1 << 21) + 1) == -5 and f(N=(1 << 21) + 1) == -5 and f(r=513) == -5 and f(L=32769) == -5
     assert f(ids=None) == -1
     assert f(ids=FAKE + 2) == -6
     assert f(w=w(B=None)) == -1
