@@ -665,8 +665,10 @@ def _dgrad_shapes(dY, W, K, block, bits, out, out_dtype, stream):
     return dev, code, M, N, out, _expect(out, "out", (M, K), ty.any, dev)
 
 
-def _sized(t, name, count, dev):
-    """Address of a dense tensor of at least `count` elements on device `dev`."""
+def _sized(t, name, count, size, dev):
+    """Address of a dense tensor of at least `count` elements of `size` bytes on device `dev`."""
+    if t.element_size() != size:
+        raise TypeError(f"{name} must have elements of {size} bytes, got {t.dtype}")
     if t.numel() < count:
         raise ValueError(f"{name} must hold {count} elements, got {t.numel()}")
     if t.get_device() != dev:
@@ -679,10 +681,12 @@ def qmm_nbits_dgrad(dY, W, scales, K, bits, block, zp=None, zp_kind=QMM_ZP_NONE,
     """dX[M, K] = dY[M, N] . dequant(W): the input gradient of qmm_nbits, from the same weight buffers."""
     dev, code, M, N, out, out_t = _dgrad_shapes(dY, W, K, block, bits, out, out_dtype, stream)
     nblk = nblocks(K, block)
-    s_p = _sized(scales, "scales", N * nblk, dev)
+    s_p = _sized(scales, "scales", N * nblk, 2, dev)
     z_p = None
-    if zp is not None and zp_kind in (QMM_ZP_PACKED, QMM_ZP_F16):
-        z_p = _sized(zp, "zp", N * ((nblk * bits + 7) // 8 if zp_kind == QMM_ZP_PACKED else nblk), dev)
+    if zp is not None and zp_kind == QMM_ZP_PACKED:
+        z_p = _sized(zp, "zp", N * ((nblk * bits + 7) // 8), 1, dev)
+    elif zp is not None and zp_kind == QMM_ZP_F16:
+        z_p = _sized(zp, "zp", N * nblk, 2, dev)
     keep, ws, wsb = _scratch(workspace, _bytes_of("qmm_dgrad_workspace_bytes", M, K, N), dY, stream)
     st = lib().qmm_nbits_dgrad(dY.data_ptr(), code, M, K, N, W.data_ptr(), bits, block, s_p, z_p, zp_kind,
                                float(uniform_zp), out.data_ptr(), out_t, ws, wsb, _handle(stream, dev))
@@ -693,8 +697,8 @@ def qmm_nbits_dgrad(dY, W, scales, K, bits, block, zp=None, zp_kind=QMM_ZP_NONE,
 def qmm_codebook4_dgrad(dY, W, absmax, codebook, K, block=64, out=None, out_dtype=None, workspace=None, stream=None):
     """dX[M, K] = dY[M, N] . (codebook[q] * absmax): the input gradient of qmm_codebook4."""
     dev, code, M, N, out, out_t = _dgrad_shapes(dY, W, K, block, 4, out, out_dtype, stream)
-    a_p = _sized(absmax, "absmax", N * nblocks(K, block), dev)
-    c_p = _sized(codebook, "codebook", 16, dev)
+    a_p = _sized(absmax, "absmax", N * nblocks(K, block), 4, dev)
+    c_p = _sized(codebook, "codebook", 16, 4, dev)
     keep, ws, wsb = _scratch(workspace, _bytes_of("qmm_dgrad_workspace_bytes", M, K, N), dY, stream)
     st = lib().qmm_codebook4_dgrad(dY.data_ptr(), code, M, K, N, W.data_ptr(), block, a_p, c_p, out.data_ptr(), out_t,
                                    ws, wsb, _handle(stream, dev))

@@ -62,3 +62,20 @@ def test_workspace():
         rs = -(-M * 4 // 256) * 256
         extra = q(M, K, N) - a16 - rs
         assert extra >= 0 and extra % (M * K * 4) == 0        # whole partial sums
+
+
+def test_binding_refuses_short_or_wrong_side_tensors():
+    """A scale, zero-point or codebook tensor of too few bytes (fewer elements, or smaller ones)."""
+    import pytest
+    import torch
+
+    ok = torch.zeros(16, dtype=torch.float32)
+    assert Q._sized(ok, "codebook", 16, 4, -1) == ok.data_ptr()
+    with pytest.raises(TypeError):
+        Q._sized(ok.half(), "codebook", 16, 4, -1)
+    with pytest.raises(ValueError):
+        Q._sized(ok[:15], "codebook", 16, 4, -1)
+    with pytest.raises(ValueError):
+        Q._sized(ok, "codebook", 16, 4, 0)             # host memory for a device call
+    with pytest.raises(ValueError):
+        Q._sized(torch.zeros(32)[::2], "codebook", 16, 4, -1)

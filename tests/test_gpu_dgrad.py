@@ -222,6 +222,14 @@ def test_refusals():
         Q.qmm_nbits_dgrad(g, W, s, 128, 4, 32, z, Q.QMM_ZP_PACKED)
     with pytest.raises(ValueError):
         Q.qmm_nbits_dgrad(g, W, s[:3], 64, 4, 32, z, Q.QMM_ZP_PACKED)
+    with pytest.raises(TypeError):
+        Q.qmm_nbits_dgrad(g, W, s.float(), 64, 4, 32, z, Q.QMM_ZP_PACKED)
+    with pytest.raises(TypeError):
+        Q.qmm_nbits_dgrad(g, W, s, 64, 4, 32, z, Q.QMM_ZP_F16)
+    am, cb = t.ones(32 * 2, device="cuda"), t.ones(16, device="cuda")
+    for args in ((am.half(), cb), (am, cb.half())):
+        with pytest.raises(TypeError):
+            Q.qmm_codebook4_dgrad(g, W, *args, 64, 32)
     with pytest.raises(Q.QmmError) as e:
         Q.qmm_nbits_dgrad(g, W, s, 64, 4, 32, z, Q.QMM_ZP_PACKED, workspace=t.empty(64, dtype=t.uint8, device="cuda"))
     assert e.value.status == -7
