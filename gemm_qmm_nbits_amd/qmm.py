@@ -108,6 +108,15 @@ _SIGS = {
                                          c_void_p, c_int, c_void_p, c_int, c_void_p, c_size_t]),
     "qmm_validate_codebook4_dgrad": (c_int, [c_void_p, c_int, c_int64, c_int64, c_int64, c_void_p, c_int, c_void_p,
                                              c_void_p, c_void_p, c_int, c_void_p, c_size_t]),
+    "qmm_nbits_dgrad_f32": (c_int, [c_void_p, c_int, c_int64, c_int64, c_int64, c_void_p, c_int, c_int, c_void_p,
+                                    c_void_p, c_int, c_float, c_void_p, c_int, c_void_p, c_size_t, c_void_p]),
+    "qmm_codebook4_dgrad_f32": (c_int, [c_void_p, c_int, c_int64, c_int64, c_int64, c_void_p, c_int, c_void_p,
+                                        c_void_p, c_void_p, c_int, c_void_p, c_size_t, c_void_p]),
+    "qmm_dgrad_f32_workspace_bytes": (c_size_t, [c_int, c_int64, c_int64, c_int64]),
+    "qmm_validate_nbits_dgrad_f32": (c_int, [c_void_p, c_int, c_int64, c_int64, c_int64, c_void_p, c_int, c_int,
+                                             c_void_p, c_void_p, c_int, c_void_p, c_int, c_void_p, c_size_t]),
+    "qmm_validate_codebook4_dgrad_f32": (c_int, [c_void_p, c_int, c_int64, c_int64, c_int64, c_void_p, c_int,
+                                                 c_void_p, c_void_p, c_void_p, c_int, c_void_p, c_size_t]),
     "qmoe_grouped_mm": (c_int, [c_void_p, c_int, c_int64, c_int64, c_int64, c_int64, c_void_p, c_void_p, c_void_p,
                                 c_void_p, c_int, c_void_p]),
     "qmoe_grouped_mm_grad": (c_int, [c_void_p, c_void_p, c_int, c_int64, c_int64, c_int64, c_int64, c_void_p,
@@ -676,9 +685,19 @@ def _sized(t, name, count, size, dev):
     return _contig(t, name).data_ptr()
 
 
+def _dgrad_workspace(f32, workspace, code, M, K, N, dY, stream):
+    if f32:
+        need = _bytes_of("qmm_dgrad_f32_workspace_bytes", code, M, K, N)
+    else:
+        need = _bytes_of("qmm_dgrad_workspace_bytes", M, K, N)
+    return _scratch(workspace, need, dY, stream)
+
+
 def qmm_nbits_dgrad(dY, W, scales, K, bits, block, zp=None, zp_kind=QMM_ZP_NONE, uniform_zp=0.0, out=None,
-                    out_dtype=None, workspace=None, stream=None):
-    """dX[M, K] = dY[M, N] . dequant(W): the input gradient of qmm_nbits, from the same weight buffers."""
+                    out_dtype=None, workspace=None, stream=None, f32=False):
+    """dX[M, K] = dY[M, N] . dequant(W): the input gradient of qmm_nbits, from the same weight buffers.
+
+    f32: dY and the weights enter the products as they are (qmm_nbits_dgrad_f32), not rounded to fp16."""
     dev, code, M, N, out, out_t = _dgrad_shapes(dY, W, K, block, bits, out, out_dtype, stream)
     nblk = nblocks(K, block)
     s_p = _sized(scales, "scales", N * nblk, 2, dev)
@@ -687,22 +706,26 @@ def qmm_nbits_dgrad(dY, W, scales, K, bits, block, zp=None, zp_kind=QMM_ZP_NONE,
         z_p = _sized(zp, "zp", N * ((nblk * bits + 7) // 8), 1, dev)
     elif zp is not None and zp_kind == QMM_ZP_F16:
         z_p = _sized(zp, "zp", N * nblk, 2, dev)
-    keep, ws, wsb = _scratch(workspace, _bytes_of("qmm_dgrad_workspace_bytes", M, K, N), dY, stream)
-    st = lib().qmm_nbits_dgrad(dY.data_ptr(), code, M, K, N, W.data_ptr(), bits, block, s_p, z_p, zp_kind,
-                               float(uniform_zp), out.data_ptr(), out_t, ws, wsb, _handle(stream, dev))
-    _check("qmm_nbits_dgrad", st)
+    keep, ws, wsb = _dgrad_workspace(f32, workspace, code, M, K, N, dY, stream)
+    name = "qmm_nbits_dgrad_f32" if f32 else "qmm_nbits_dgrad"
+    st = getattr(lib(), name)(dY.data_ptr(), code, M, K, N, W.data_ptr(), bits, block, s_p, z_p, zp_kind,
+                              float(uniform_zp), out.data_ptr(), out_t, ws, wsb, _handle(stream, dev))
+    _check(name, st)
     return out
 
 
-def qmm_codebook4_dgrad(dY, W, absmax, codebook, K, block=64, out=None, out_dtype=None, workspace=None, stream=None):
-    """dX[M, K] = dY[M, N] . (codebook[q] * absmax): the input gradient of qmm_codebook4."""
+def qmm_codebook4_dgrad(dY, W, absmax, codebook, K, block=64, out=None, out_dtype=None, workspace=None, stream=None,
+                        f32=False):
+    """dX[M, K] = dY[M, N] . (codebook[q] * absmax): the input gradient of qmm_codebook4 (f32: as
+    qmm_nbits_dgrad)."""
     dev, code, M, N, out, out_t = _dgrad_shapes(dY, W, K, block, 4, out, out_dtype, stream)
     a_p = _sized(absmax, "absmax", N * nblocks(K, block), 4, dev)
     c_p = _sized(codebook, "codebook", 16, 4, dev)
-    keep, ws, wsb = _scratch(workspace, _bytes_of("qmm_dgrad_workspace_bytes", M, K, N), dY, stream)
-    st = lib().qmm_codebook4_dgrad(dY.data_ptr(), code, M, K, N, W.data_ptr(), block, a_p, c_p, out.data_ptr(), out_t,
-                                   ws, wsb, _handle(stream, dev))
-    _check("qmm_codebook4_dgrad", st)
+    keep, ws, wsb = _dgrad_workspace(f32, workspace, code, M, K, N, dY, stream)
+    name = "qmm_codebook4_dgrad_f32" if f32 else "qmm_codebook4_dgrad"
+    st = getattr(lib(), name)(dY.data_ptr(), code, M, K, N, W.data_ptr(), block, a_p, c_p, out.data_ptr(), out_t, ws,
+                              wsb, _handle(stream, dev))
+    _check(name, st)
     return out
 
 

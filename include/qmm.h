@@ -402,6 +402,23 @@ qmm_status qmm_codebook4_dgrad(const void* dY, int dy_type, int64_t M, int64_t K
                                size_t workspace_bytes, void* stream);
 size_t qmm_dgrad_workspace_bytes(int64_t M, int64_t K, int64_t N);
 
+/* The same gradients with dY and the dequantized weights as they are: only the fp32 sums and dX are
+ * rounded, as in the forward product with up to 8 rows.  For fp32 dX (relative L2 <= 1e-5), for weights
+ * that fp16 does not hold (below 6e-5 it loses their bits: small absmax or scales) and for gradients
+ * of a wide range in one row.  Costs about twice the matrix work for codes of up to 4 bits with
+ * integer zero points, three times it otherwise, twice that for fp16 dY and three times for fp32 dY;
+ * bf16 dY that is 16-byte aligned with N a multiple of 8 is read in place.
+ *   workspace: at least qmm_dgrad_f32_workspace_bytes(dy_type, M, K, N) bytes, 256-byte aligned. */
+qmm_status qmm_nbits_dgrad_f32(const void* dY, int dy_type, int64_t M, int64_t K, int64_t N,
+                               const uint8_t* W, int bits, int block, const uint16_t* scales,
+                               const void* zp, int zp_kind, float uniform_zp, void* dX, int dx_type,
+                               void* workspace, size_t workspace_bytes, void* stream);
+qmm_status qmm_codebook4_dgrad_f32(const void* dY, int dy_type, int64_t M, int64_t K, int64_t N,
+                                   const uint8_t* W, int block, const float* absmax,
+                                   const float* codebook, void* dX, int dx_type, void* workspace,
+                                   size_t workspace_bytes, void* stream);
+size_t qmm_dgrad_f32_workspace_bytes(int dy_type, int64_t M, int64_t K, int64_t N);
+
 /* Host-only checks of the arguments, as qmm_validate_nbits. */
 qmm_status qmm_validate_nbits_dgrad(const void* dY, int dy_type, int64_t M, int64_t K, int64_t N,
                                     const uint8_t* W, int bits, int block, const uint16_t* scales,
@@ -411,6 +428,15 @@ qmm_status qmm_validate_codebook4_dgrad(const void* dY, int dy_type, int64_t M, 
                                         const uint8_t* W, int block, const float* absmax,
                                         const float* codebook, const void* dX, int dx_type,
                                         const void* workspace, size_t workspace_bytes);
+qmm_status qmm_validate_nbits_dgrad_f32(const void* dY, int dy_type, int64_t M, int64_t K, int64_t N,
+                                        const uint8_t* W, int bits, int block, const uint16_t* scales,
+                                        const void* zp, int zp_kind, const void* dX, int dx_type,
+                                        const void* workspace, size_t workspace_bytes);
+qmm_status qmm_validate_codebook4_dgrad_f32(const void* dY, int dy_type, int64_t M, int64_t K,
+                                            int64_t N, const uint8_t* W, int block,
+                                            const float* absmax, const float* codebook,
+                                            const void* dX, int dx_type, const void* workspace,
+                                            size_t workspace_bytes);
 
 /* ---------------------------------------------------------------------------
  * qmoe_grouped_mm -- the ragged expert product of 16-bit weights, and its gradients (layers
