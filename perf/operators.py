@@ -324,11 +324,11 @@ def _own(s):
     if op == "dgrad":
         if c["fmt"] == "codebook":
             return Q.qmm_codebook4_dgrad(s["dY"], s["W"], s["absmax"], s["codebook"], c["K"], c["block"],
-                                         out_dtype=s["out"])
+                                         out_dtype=s["out"], f32=True)
         kind = {"none": Q.QMM_ZP_NONE, "packed": Q.QMM_ZP_PACKED, "f16": Q.QMM_ZP_F16,
                 "uniform": Q.QMM_ZP_UNIFORM}[c["zp"]]
         return Q.qmm_nbits_dgrad(s["dY"], s["W"], s["scales"], c["K"], c["bits"], c["block"], s["zp"], kind,
-                                 s["uniform"], out_dtype=s["out"])
+                                 s["uniform"], out_dtype=s["out"], f32=True)
     if op == "grouped":
         return Q.qmoe_grouped_mm(s["X"], s["offsets"], s["W"], bias=s["bias"], out_dtype=s["out"])
     dx, dw, db = Q.qmoe_grouped_mm_grad(s["dY"], s["X"], s["offsets"], s["W"], dw_dtype=s["out"],
