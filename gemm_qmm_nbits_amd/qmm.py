@@ -216,6 +216,32 @@ def _contig(t, name):
     return t
 
 
+# Memory of a call on a given stream comes from that stream's part of the caching allocator: a block
+# of the current stream's part may still be in use by work queued there, which the given stream does
+# not wait for.
+
+def _new(shape, dtype, like, stream):
+    """An output of a call on `stream`, which the caller will use on the current stream: its memory is not
+    handed out again before what is queued there by the time it is freed has run."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=like.device)
+    t.record_stream(torch.cuda.current_stream(like.device))
+    return t
+
+
+def _temporary(nbytes, like, stream, zeroed=False):
+    """Scratch memory that only a call on `stream` uses."""
+    torch = _torch()
+    make = torch.zeros if zeroed else torch.empty
+    if stream is None:
+        return make(nbytes, dtype=torch.uint8, device=like.device)
+    with torch.cuda.stream(stream):
+        return make(nbytes, dtype=torch.uint8, device=like.device)
+
+
 def nblocks(K, block):
     return (K + block - 1) // block
 
@@ -229,10 +255,10 @@ def qmm_nbits(A, W, scales, K, bits, block, zp=None, zp_kind=QMM_ZP_NONE, unifor
     N = W.shape[0]
     ctype = dtype_code(A) if out_dtype is None else dtype_code(torch.empty(0, dtype=out_dtype))
     if out is None:
-        out = torch.empty((M, N), dtype=torch_dtype(ctype), device=A.device)
+        out = _new((M, N), torch_dtype(ctype), A, stream)
     ws_bytes = lib().qmm_nbits_workspace_bytes(M, K, N, dtype_code(A))
     if ws_bytes and workspace is None:
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=A.device)
+        workspace = _temporary(ws_bytes, A, stream)
     st = lib().qmm_nbits(_ptr(A), dtype_code(A), M, K, N, _ptr(W), bits, block, _ptr(scales),
                          _ptr(zp), zp_kind, float(uniform_zp), _ptr(bias), _ptr(out),
                          dtype_code(out), _ptr(workspace),
@@ -250,10 +276,10 @@ def qmm_codebook4(A, W, absmax, codebook, K, block=64, bias=None, out=None, out_
     N = W.shape[0]
     ctype = dtype_code(A) if out_dtype is None else dtype_code(torch.empty(0, dtype=out_dtype))
     if out is None:
-        out = torch.empty((M, N), dtype=torch_dtype(ctype), device=A.device)
+        out = _new((M, N), torch_dtype(ctype), A, stream)
     ws_bytes = lib().qmm_codebook4_workspace_bytes(M, K, N, dtype_code(A))
     if ws_bytes and workspace is None:
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=A.device)
+        workspace = _temporary(ws_bytes, A, stream)
     st = lib().qmm_codebook4(_ptr(A), dtype_code(A), M, K, N, _ptr(W), block, _ptr(absmax),
                              _ptr(codebook), _ptr(bias), _ptr(out), dtype_code(out),
                              _ptr(workspace),
@@ -271,7 +297,7 @@ def _nested(na):
 
 def qmm_dequantize_absmax_nested(na, count, stream=None):
     torch = _torch()
-    out = torch.empty(count, dtype=torch.float32, device=na["codes"].device)
+    out = _new(count, torch.float32, na["codes"], stream)
     desc = _nested(na)
     _check("qmm_dequantize_absmax_nested", lib().qmm_dequantize_absmax_nested(ctypes.byref(desc), count, _ptr(out),
                                                                               _stream(stream)))
@@ -286,10 +312,10 @@ def qmm_codebook4_nested(A, W, na, codebook, K, block=64, bias=None, out=None, o
     N = W.shape[0]
     ctype = dtype_code(A) if out_dtype is None else dtype_code(torch.empty(0, dtype=out_dtype))
     if out is None:
-        out = torch.empty((M, N), dtype=torch_dtype(ctype), device=A.device)
+        out = _new((M, N), torch_dtype(ctype), A, stream)
     ws_bytes = lib().qmm_codebook4_nested_workspace_bytes(M, K, N, dtype_code(A), block)
     if ws_bytes and workspace is None:
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=A.device)
+        workspace = _temporary(ws_bytes, A, stream)
     desc = _nested(na)
     st = lib().qmm_codebook4_nested(_ptr(A), dtype_code(A), M, K, N, _ptr(W), block, ctypes.byref(desc),
                                     _ptr(codebook), _ptr(bias), _ptr(out), dtype_code(out), _ptr(workspace),
@@ -301,9 +327,8 @@ def qmm_codebook4_nested(A, W, na, codebook, K, block=64, bias=None, out=None, o
 
 def qmm_fp16_uniform_value(zp, scratch=None, stream=None):
     """(is_uniform, value) of an fp16 zero-point tensor (synchronizes the stream)."""
-    torch = _torch()
     if scratch is None:
-        scratch = torch.empty(lib().qmm_uniform_scratch_bytes(), dtype=torch.uint8, device=zp.device)
+        scratch = _temporary(lib().qmm_uniform_scratch_bytes(), zp, stream)
     flag = c_int(0)
     val = c_float(0.0)
     st = lib().qmm_fp16_uniform_value(_ptr(zp), zp.numel(), _ptr(scratch), scratch.numel(),
@@ -317,7 +342,7 @@ def qmm_dequantize_nbits(W, scales, K, bits, block, zp=None, zp_kind=QMM_ZP_NONE
     torch = _torch()
     out_dtype = out_dtype or torch.float32
     N = W.shape[0]
-    out = torch.empty((N, K), dtype=out_dtype, device=W.device)
+    out = _new((N, K), out_dtype, W, stream)
     st = lib().qmm_dequantize_nbits(_ptr(W), bits, block, _ptr(scales), _ptr(zp), zp_kind,
                                     float(uniform_zp), N, K, _ptr(out), dtype_code(out),
                                     _stream(stream))
@@ -329,7 +354,7 @@ def qmm_dequantize_codebook4(W, absmax, codebook, K, block=64, out_dtype=None, s
     torch = _torch()
     out_dtype = out_dtype or torch.float32
     N = W.shape[0]
-    out = torch.empty((N, K), dtype=out_dtype, device=W.device)
+    out = _new((N, K), out_dtype, W, stream)
     st = lib().qmm_dequantize_codebook4(_ptr(W), block, _ptr(absmax), _ptr(codebook), N, K,
                                         _ptr(out), dtype_code(out), _stream(stream))
     _check("qmm_dequantize_codebook4", st)
@@ -359,11 +384,11 @@ def qmoe_decode_fused(X, expert_ids, expert_w, fc1, fc2, H, I, E, block, mode=QM
     T = X.shape[0]
     k = expert_ids.shape[1]
     if out is None:
-        out = torch.empty((T, H), dtype=torch.float16, device=X.device)
+        out = _new((T, H), torch.float16, X, stream)
     sb = lib().qmoe_decode_scratch_bytes(T, H, I, k, mode)
     if scratch is None:
         # zeroed: the single-launch form's sync words must start at zero (calls leave them so)
-        scratch = torch.zeros(max(sb, 1), dtype=torch.uint8, device=X.device)
+        scratch = _temporary(max(sb, 1), X, stream, zeroed=True)
     st = lib().qmoe_decode_fused(_ptr(X), T, H, I, E, k, _ptr(expert_ids), _ptr(expert_w), _qw(fc1),
                                  _qw(fc2), bits, block, mode, _ptr(out), _ptr(scratch),
                                  scratch.numel() * scratch.element_size(), _stream(stream))
@@ -378,7 +403,7 @@ def qmoe_ragged_mm(X, row_offsets, w, N, E, block, bits=4, out=None, stream=None
     X = _contig(X, "X")
     R, K = X.shape
     if out is None:
-        out = torch.empty((R, N), dtype=torch.float16, device=X.device)
+        out = _new((R, N), torch.float16, X, stream)
     st = lib().qmoe_ragged_mm(_ptr(X), R, K, N, E, _ptr(row_offsets), _qw(w), bits, block, _ptr(out),
                               _stream(stream))
     _check("qmoe_ragged_mm", st)
@@ -426,10 +451,9 @@ def _code_dtype(bits):
 
 def quantize_linear(x, q, bits, out=None, stream=None):
     """uint8 / uint16 codes of x under the per-tensor (scale, zero_point) q."""
-    torch = _torch()
     x = _contig(x, "x")
     if out is None:
-        out = torch.empty(x.shape, dtype=_code_dtype(bits), device=x.device)
+        out = _new(x.shape, _code_dtype(bits), x, stream)
     _check("qmm_quantize_linear", lib().qmm_quantize_linear(_ptr(x), dtype_code(x), x.numel(), _qp(q), bits,
                                                             _ptr(out), _stream(stream)))
     return out
@@ -439,39 +463,36 @@ def dequantize_linear(codes, q, bits, out_dtype=None, out=None, stream=None):
     torch = _torch()
     codes = _contig(codes, "codes")
     if out is None:
-        out = torch.empty(codes.shape, dtype=out_dtype or torch.float32, device=codes.device)
+        out = _new(codes.shape, out_dtype or torch.float32, codes, stream)
     _check("qmm_dequantize_linear", lib().qmm_dequantize_linear(_ptr(codes), codes.numel(), _qp(q), bits,
                                                                 _ptr(out), dtype_code(out), _stream(stream)))
     return out
 
 
 def fake_quantize(x, q, bits, out=None, stream=None):
-    torch = _torch()
     x = _contig(x, "x")
     if out is None:
-        out = torch.empty_like(x)
+        out = _new(x.shape, x.dtype, x, stream)
     _check("qmm_fake_quantize", lib().qmm_fake_quantize(_ptr(x), dtype_code(x), x.numel(), _qp(q), bits,
                                                         _ptr(out), _stream(stream)))
     return out
 
 
 def qsigmoid(codes, q_in, q_out, bits, out=None, stream=None):
-    torch = _torch()
     codes = _contig(codes, "codes")
     if out is None:
-        out = torch.empty_like(codes)
+        out = _new(codes.shape, codes.dtype, codes, stream)
     _check("qmm_qsigmoid", lib().qmm_qsigmoid(_ptr(codes), codes.numel(), _qp(q_in), _qp(q_out), bits, _ptr(out),
                                               _stream(stream)))
     return out
 
 
 def qmul(a, qa, b, qb, qc, bits, out=None, stream=None):
-    torch = _torch()
     a, b = _contig(a, "a"), _contig(b, "b")
     if a.numel() != b.numel():
         raise ValueError("a and b differ in size")
     if out is None:
-        out = torch.empty_like(a)
+        out = _new(a.shape, a.dtype, a, stream)
     _check("qmm_qmul", lib().qmm_qmul(_ptr(a), _qp(qa), _ptr(b), _qp(qb), a.numel(), _qp(qc), bits, _ptr(out),
                                       _stream(stream)))
     return out
@@ -485,7 +506,7 @@ def qswiglu(gate, up, qparams, bits, out=None, stream=None):
     if gate.numel() != up.numel() or gate.dtype != up.dtype:
         raise ValueError("gate and up differ in size or dtype")
     if out is None:
-        out = torch.empty_like(gate)
+        out = _new(gate.shape, gate.dtype, gate, stream)
     arr = (qmm_qparams * 5)(*[_qp(q) for q in qparams])
     _check("qmm_qswiglu", lib().qmm_qswiglu(_ptr(gate), _ptr(up), dtype_code(gate), gate.numel(), bits, arr,
                                             _ptr(out), _stream(stream)))
@@ -554,22 +575,17 @@ def _device_of(t):
 
 
 def _handle(stream, dev):
-    return _types().current(dev) if stream is None else stream.cuda_stream
-
-
-def _new(shape, dtype, like, stream):
-    """A tensor of the caching allocator for a call on `stream`: where that is not the stream the
-    allocator hands it out on, its memory is not reused before the call has run."""
-    t = _types().torch.empty(shape, dtype=dtype, device=like.device)
-    if stream is not None:
-        t.record_stream(stream)
-    return t
+    if stream is None:
+        return _types().current(dev)
+    if stream.device_index != dev:
+        raise ValueError("the stream must be one of the tensors' device")
+    return stream.cuda_stream
 
 
 def _scratch(workspace, need, like, stream):
     """The workspace, allocated here when not given, its address and size."""
     if workspace is None:
-        workspace = _new(need, _types().torch.uint8, like, stream)
+        workspace = _temporary(need, like, stream)
         return workspace, workspace.data_ptr(), need
     if not workspace.is_contiguous() or workspace.get_device() != like.get_device():
         raise ValueError("workspace must be contiguous and on the device of the call")
