@@ -45,8 +45,7 @@ struct LoraArgs {
   int slots;           // tile slots (grid)
   int slices;          // column slices of the expand kernels (set by their launch)
   float* part;         // fp32 partial products [splits][M][rp], by position
-  uint8_t* pieces;     // 16-bit pieces of scale_a t by position (lora_piece_bytes each), or NULL
-  float* factor;       // fp16: the power of two of each position's pieces
+  uint8_t* pieces;     // bf16 pieces of scale_a t by position (lora_piece_bytes each), or NULL
   int few;             // the expand kernel sums and splits the parts itself (lora_few_rows)
   int splits;
   int64_t split_len;   // contraction elements per split (a multiple of 256)
@@ -62,12 +61,12 @@ hipError_t launch_lora_plan(const LoraArgs& p, hipStream_t st);
 hipError_t launch_lora_shrink_x(const LoraArgs& p, hipStream_t st);
 hipError_t launch_lora_shrink_dy(const LoraArgs& p, hipStream_t st);
 // T[row] (rows of ldt) = sum over the splits of part (x scale_a when `scaled`), T may be NULL;
-// and p.pieces, p.factor when given.
+// and p.pieces when given.
 hipError_t launch_lora_finalize(const LoraArgs& p, bool scaled, float* T, int64_t ldt, hipStream_t st);
 // Whether the expand kernel sums and splits the parts itself.
 bool lora_few_rows(int64_t M, int64_t N, int r, int splits);
 // Bytes of the pieces of one position.
-int lora_piece_bytes(int type, int r);
+int lora_piece_bytes(int r);
 // out = base + scale_a * t B_a^T, t from p.pieces (outputs below 64 columns: from the parts)
 hipError_t launch_lora_expand(const LoraArgs& p, hipStream_t st);
 // out = base + dt A_a, dt from p.pieces (outputs below 64 columns: dT [M][rp] by row)

@@ -14,9 +14,8 @@
 // kernels sort by a ballot instead, which saves the launch.
 //
 // Numbers: t and dt stay in fp32.  Products of two 16-bit operands use the 16-bit matrix
-// instructions (exact products, fp32 sums).  Products with t or dt take them as sums of 16-bit
-// pieces (expand: exact for bf16, 22 bits for fp16) or the 16-bit operand widened to fp32 (outer
-// sums).  Every sum has a fixed order (no atomics in them): repeated calls give the same bits.
+// instructions (exact products, fp32 sums).  Products with t or dt take them as exact sums of bf16
+// pieces (expand) or the 16-bit operand widened to fp32 (outer sums).  Every sum has a fixed order (no atomics in them): repeated calls give the same bits.
 #include "qmm_device.h"
 #include "qmm_internal.h"
 #include "qmm_lora.h"
@@ -368,14 +367,13 @@ __device__ __forceinline__ f32x4 sum_parts(const LoraArgs& p, const float* q) {
 // One work-group: a tile and, per wave, every (4 slices)-th group of 64 output columns.
 // Bound by base and out, so those are accessed by whole rows (16 lanes x 4 columns, 4 rows at
 // a time, the next 16 rows' base on its way during the current ones'), and the arithmetic is
-// kept off the vector units: v_mfma_f32_16x16x32 in the operands' own 16-bit type with the
-// columns as its rows, B_a (or A_a) as it was loaded, and t as a sum of 16-bit pieces:
-//   bf16  three truncations, t = p0 + p1 + p2 exactly (8 + 8 + 8 bits)
-//   fp16  t 2^s = p0 + p1 with one power of two per row that puts the row's largest magnitude
-//         in [2^14, 2^15); p1 rounds the remainder, 2^-22 of the element at most
-// so t loses nothing that fp32 sums keep.  A contraction step of 32 holds four chunks of 8
-// ranks, one per 16 lanes: with r <= 8, 16 or 32 the four are 4, 2 or 1 pieces of the same
-// ranks, so one loaded operand serves every piece; beyond, the steps are (32 ranks, piece).
+// kept off the vector units: v_mfma_f32_16x16x32_bf16 with the columns as its rows, B_a (or A_a) as it
+// was loaded (fp16: as two bf16 operands), and t as a sum of three bf16 pieces (Pieces), so t loses
+// nothing that fp32 holds, whatever the range of a row's ranks.  (fp16 t in two fp16 pieces, with one
+// power of two per row, kept 22 bits, and fewer of ranks below 2^-17 of the row's largest.)  A
+// contraction step of 32 holds four chunks of 8 ranks, one per 16 lanes: with r <= 8, 16 or 32 the
+// four are 4, 2 or 1 pieces of the same ranks, so one loaded operand serves every piece; beyond, the
+// steps are (32 ranks, piece).
 //   forward  column 16 f + i is row i of part f; lane l loads 8 ranks of B[16 f + l % 16]
 //   DX       A_a's ranks run down its columns: a wave copies 32 ranks x 64 columns into its
 //            piece of LDS and reads them transposed (ds_read_b64_tr_b16)
@@ -448,100 +446,81 @@ constexpr int kAp = 72;           // 16-bit elements of a rank's 64 columns ther
 constexpr int kWaveLds = 4608;    // bytes of that piece: 16 rows of sums, or 32 ranks of A
 static_assert(16 * kXp * 4 <= kWaveLds && 32 * kAp * 2 <= kWaveLds, "");
 
+// Pieces of t: truncations to bf16, t = p0 + p1 + p2 exactly (8 bits each), whatever its magnitude.
+// Every piece but the first also takes t 2^-40, so that no piece of a value other than 0 is 0 (down to
+// 2^-86) and an infinite weight times the pieces is what it is times t; all pieces of an infinite t are
+// infinite.  With up to 16 ranks a contraction step has places left: they take a fourth piece.
+//
 // How t lies in LDS: rows of `steps` contraction steps of four 16-byte chunks, and one chunk of
 // padding (an odd number of chunks, so 16 rows read at one chunk meet every bank once).
-template <int TY>
 struct Pieces {
-  static constexpr int kCount = TY == QMM_F16 ? 2 : 3;
   int chunks;  // chunks of 8 ranks of one piece: 1, 2 or a multiple of 4
+  int count;   // pieces
   int steps;
   __host__ __device__ __forceinline__ explicit Pieces(int r) {
     chunks = r <= 8 ? 1 : r <= 16 ? 2 : (r + 31) / 32 * 4;
-    steps = (chunks * kCount + 3) / 4;
+    count = chunks < 4 ? 4 : 3;
+    steps = chunks * count / 4;
   }
   __host__ __device__ __forceinline__ int row_bytes() const { return steps * 64 + 16; }
   // step and chunk place of piece k's chunk c
   __device__ __forceinline__ int place(int k, int c) const {
-    return chunks <= 4 ? k * chunks + c : (((c >> 2) * kCount + k) << 2) + (c & 3);
+    return chunks < 4 ? k * chunks + c : (((c >> 2) * count + k) << 2) + (c & 3);
   }
 };
 
-// Splits the rows tf [n][ld] of t (zeros from rank r on) into pieces, row i at out + i * row_bytes;
-// factor[i] takes the inverse of row i's power of two (fp16).  `top` [n]: LDS scratch (fp16).
+// Next piece of x, which is left of the value v; x becomes what is left.
+__device__ __forceinline__ uint32_t next_piece(float& x, float v) {
+#pragma clang fp contract(off)
+  const uint32_t a = __float_as_uint(x) & 0xffff0000u;
+  const float left = x - __uint_as_float(a);
+  x = fabsf(v) < __builtin_huge_valf() ? __fmaf_rn(v, 0x1p-40f, left) : v;
+  return a;
+}
+
+// Splits the rows tf [n][ld] of t (zeros from rank r on) into pieces, row i at out + i * row_bytes.
 // The whole work-group of NT threads calls it, between barriers.
-template <int TY, int NT>
-__device__ __forceinline__ void split_rows(const float* tf, int ld, int n, const Pieces<TY>& pc, uint8_t* out,
-                                           int64_t row_bytes, float* factor, uint32_t* top) {
-  if constexpr (TY == QMM_F16) {
-    for (int i = threadIdx.x; i < n; i += NT) top[i] = 0u;
-    __syncthreads();
-    for (int i = threadIdx.x; i < n * pc.chunks; i += NT) {
-      const float* v = tf + i / pc.chunks * ld + i % pc.chunks * 8;
-      float m = 0.0f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(v[e]));
-      atomicMax(top + i / pc.chunks, __float_as_uint(m));  // a maximum: any order gives it
-    }
-    __syncthreads();
-  }
+template <int NT>
+__device__ __forceinline__ void split_rows(const float* tf, int ld, int n, const Pieces& pc, uint8_t* out,
+                                           int64_t row_bytes) {
   for (int i = threadIdx.x; i < n * pc.chunks; i += NT) {
     const int row = i / pc.chunks, c = i % pc.chunks;
-    const float* v = tf + row * ld + c * 8;
-    uint32_t h[Pieces<TY>::kCount][4];
-    if constexpr (TY == QMM_F16) {
-      const float m = __uint_as_float(top[row]);
-      int E = 0;
-      if (m > 0.0f && m <= 3.402823466e38f) {
-        (void)frexpf(m, &E);
-        E = 15 - E;
-        E = E < 120 ? E : 120;
-      }
+    float v[8], x[8];
 #pragma unroll
-      for (int e = 0; e < 8; e += 2) {
-        const float a = ldexpf(v[e], E), b = ldexpf(v[e + 1], E);
-        const uint32_t hi = round_pair(a, b, QMM_F16);
-        const float ra = a - f16_to_f32((uint16_t)hi), rb = b - f16_to_f32((uint16_t)(hi >> 16));
-        h[0][e / 2] = hi;
-        // a value that is not finite stays in the first piece
-        h[1][e / 2] = round_pair(fabsf(ra) < 1e30f ? ra : 0.0f, fabsf(rb) < 1e30f ? rb : 0.0f, QMM_F16);
-      }
-      if (c == 0) factor[row] = ldexpf(1.0f, -E);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; e += 2) {
-        float x[2] = {v[e], v[e + 1]};
-#pragma unroll
-        for (int k = 0; k < 3; ++k) {
-          const uint32_t a = __float_as_uint(x[0]) & 0xffff0000u, b = __float_as_uint(x[1]) & 0xffff0000u;
-          h[k][e / 2] = (a >> 16) | b;
-          x[0] -= __uint_as_float(a);  // exact: the low bits
-          x[1] -= __uint_as_float(b);
-          if (k == 0) {  // a value that is not finite stays in the first piece
-            x[0] = fabsf(x[0]) < 1e38f ? x[0] : 0.0f;
-            x[1] = fabsf(x[1]) < 1e38f ? x[1] : 0.0f;
-          }
-        }
-      }
+    for (int e = 0; e < 8; ++e) {
+      const float t = tf[row * ld + c * 8 + e];
+      x[e] = v[e] = t == t ? t : __builtin_nanf("");  // a NaN whose upper half is one
     }
     uint8_t* to = out + row * row_bytes;
+    for (int k = 0; k < pc.count; ++k) {
+      uint32_t h[4];
 #pragma unroll
-    for (int k = 0; k < Pieces<TY>::kCount; ++k)
-      *(uint4*)(to + pc.place(k, c) * 16) = make_uint4(h[k][0], h[k][1], h[k][2], h[k][3]);
-    // chunks that no piece fills
-    if (c == 0)
-      for (int k = Pieces<TY>::kCount * pc.chunks; k < pc.steps * 4; ++k)
-        *(uint4*)(to + k * 16) = make_uint4(0u, 0u, 0u, 0u);
+      for (int e = 0; e < 8; e += 2) h[e / 2] = (next_piece(x[e], v[e]) >> 16) | next_piece(x[e + 1], v[e + 1]);
+      *(uint4*)(to + pc.place(k, c) * 16) = make_uint4(h[0], h[1], h[2], h[3]);
+    }
+  }
+}
+
+// Eight fp16 values as two bf16 operands (exactly; not 0 and infinite as the pieces of t).
+__device__ __forceinline__ void split_half(const uint4& u, uint4 (&out)[2]) {
+  float v[8], x[8];
+  widen8<QMM_F16>(u, v);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) x[e] = v[e];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    uint32_t h[4];
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) h[e / 2] = (next_piece(x[e], v[e]) >> 16) | next_piece(x[e + 1], v[e + 1]);
+    out[k] = make_uint4(h[0], h[1], h[2], h[3]);
   }
 }
 
 // Sums the splits of a tile's parts, 16 rows per work-group (blockIdx.y), and writes what the
 // later passes read: T (fp32 by row, ldt apart, times scale_a when `scaled`; zeros for rows
 // without an adapter) and the pieces of scale_a t by position (when p.pieces is given).
-template <int TY>
 __global__ __launch_bounds__(LT) void lora_finalize_kernel(LoraArgs p, int scaled, float* T, int64_t ldt) {
   extern __shared__ __attribute__((aligned(16))) float tf[];  // [16][rp + 32]
-  __shared__ uint32_t top[16];
-  __shared__ float factor[16];
   __shared__ int rows[kLoraTile];
   const Tile t = find_tile(p, rows, (int)blockIdx.x);
   const int i0 = (int)blockIdx.y * 16;
@@ -563,20 +542,13 @@ __global__ __launch_bounds__(LT) void lora_finalize_kernel(LoraArgs p, int scale
   }
   if (none || !p.pieces) return;
   __syncthreads();
-  const Pieces<TY> pc(p.r);
-  uint8_t* out = p.pieces + position(p, t, rows, i0) * (pc.steps * 64);
+  const Pieces pc(p.r);
+  const int64_t bytes = pc.steps * 64;
   if (p.use_plan) {
-    split_rows<TY, LT>(tf, ld, n, pc, out, pc.steps * 64, factor, top);
-    __syncthreads();
-    if (TY == QMM_F16 && (int)threadIdx.x < n) p.factor[t.start + i0 + threadIdx.x] = factor[threadIdx.x];
+    split_rows<LT>(tf, ld, n, pc, p.pieces + position(p, t, rows, i0) * bytes, bytes);
   } else {
     // rows of the inline form are not neighbours: one after another
-    for (int k = 0; k < n; ++k) {
-      split_rows<TY, LT>(tf + k * ld, ld, 1, pc, p.pieces + (int64_t)rows[i0 + k] * (pc.steps * 64), 0, factor, top);
-      __syncthreads();
-      if (TY == QMM_F16 && threadIdx.x == 0) p.factor[rows[i0 + k]] = factor[0];
-      __syncthreads();
-    }
+    for (int k = 0; k < n; ++k) split_rows<LT>(tf + k * ld, ld, 1, pc, p.pieces + (int64_t)rows[i0 + k] * bytes, 0);
   }
 }
 
@@ -588,19 +560,20 @@ struct ColumnGroup {
   const Tile& t;
   const int* rows;
   const uint8_t* ts;
-  const float* factor;
   uint8_t* x;  // this wave's piece of LDS
   const uint16_t* Bm;
-  const Pieces<TY> pc;
+  const Pieces pc;
   int64_t W, n0;
   int r, ln, lg, from, s0, s1;
   bool none;
-  uint4 keep[RB ? RB : 1][4];
+  // fp16 operands as two bf16 ones (11 bits as 8 and 3)
+  static constexpr int NB = TY == QMM_F16 ? 2 : 1;
+  uint4 keep[RB ? RB : 1][4][NB];
   u32x4 even[4];
 
   __device__ __forceinline__ ColumnGroup(const LoraArgs& args, const Tile& tile, const int* rows_, const uint8_t* ts_,
-                                         const float* factor_, uint8_t* x_, int first, int last)
-      : p(args), t(tile), rows(rows_), ts(ts_), factor(factor_), x(x_), pc(args.r), s0(first), s1(last) {
+                                         uint8_t* x_, int first, int last)
+      : p(args), t(tile), rows(rows_), ts(ts_), x(x_), pc(args.r), s0(first), s1(last) {
     const int lane = threadIdx.x & 63;
     ln = lane & 15;
     lg = lane >> 4;
@@ -617,7 +590,8 @@ struct ColumnGroup {
     }
   }
   // Operands of the 32-rank block b for the four 16-column parts.
-  __device__ __forceinline__ void load_ranks(int b, uint4 (&u)[4]) const {
+  __device__ __forceinline__ void load_ranks(int b, uint4 (&out)[4][NB]) const {
+    uint4 u[4];
     const int chunk = pc.chunks < 4 ? lg & (pc.chunks - 1) : lg;  // this lane's chunk in the block
     const int rank = 32 * b + 8 * chunk;
     if constexpr (DX) {
@@ -645,6 +619,11 @@ struct ColumnGroup {
 #pragma unroll
       for (int f = 0; f < 4; ++f) u[f] = load8<false>(Bm + (n0 + 16 * f + ln) * r, rank, r);
     }
+#pragma unroll
+    for (int f = 0; f < 4; ++f) {
+      if constexpr (TY == QMM_BF16) out[f][0] = u[f];
+      else split_half(u[f], out[f]);
+    }
   }
   __device__ __forceinline__ void begin(int64_t g0) {
     n0 = g0 + 64 <= W ? g0 : W - 64;
@@ -656,11 +635,13 @@ struct ColumnGroup {
         for (int b = 0; b < RB; ++b) load_ranks(b, keep[b]);
     }
   }
-  __device__ __forceinline__ void steps(const uint4 (&u)[4], const uint8_t* at, int count, f32x4 (&acc)[4]) const {
+  __device__ __forceinline__ void steps(const uint4 (&u)[4][NB], const uint8_t* at, int count, f32x4 (&acc)[4]) const {
     for (int k = 0; k < count; ++k) {
       const uint4 tv = *(const uint4*)(at + k * 64);
 #pragma unroll
-      for (int f = 0; f < 4; ++f) acc[f] = mfma16<TY>(u[f], tv, acc[f]);
+      for (int j = 0; j < NB; ++j)
+#pragma unroll
+        for (int f = 0; f < 4; ++f) acc[f] = mfma16<QMM_BF16>(u[f][j], tv, acc[f]);
     }
   }
   __device__ __forceinline__ void part(int s, const u32x4 (&raw)[4]) {  // rows 16 s ..
@@ -669,7 +650,7 @@ struct ColumnGroup {
     for (int f = 0; f < 4; ++f) acc[f] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     if (!none) {
       const uint8_t* at = ts + ((s - s0) * 16 + ln) * pc.row_bytes() + lg * 16;
-      constexpr int kP = Pieces<TY>::kCount;
+      constexpr int kP = 3;  // pieces of more than 16 ranks
       if constexpr (RB == 1) {
         steps(keep[0], at, pc.steps, acc);
       } else if constexpr (RB == 2) {
@@ -677,7 +658,7 @@ struct ColumnGroup {
         steps(keep[1], at + kP * 64, kP, acc);
       } else {
         for (int b = 0; b < pc.chunks / 4; ++b) {
-          uint4 u[4];
+          uint4 u[4][NB];
           load_ranks(b, u);
           steps(u, at + b * kP * 64, kP, acc);
         }
@@ -692,13 +673,7 @@ struct ColumnGroup {
       f32x4 v = base_values<BB>(raw[i], p.base_type);
       if (!none) {
         const f32x4 d = *(const f32x4*)((const float*)x + (4 * i + lg) * kXp + 4 * ln);
-        if constexpr (TY == QMM_F16) {
-          const float k = factor[row - 16 * s0];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) v[e] = fmaf(d[e], k, v[e]);
-        } else {
-          v += d;
-        }
+        v += d;
       }
       if (row < t.count && from < 4) store_out4(p.out, p.out_type, (int64_t)rows[row] * W + n0 + 4 * ln, from, v);
     }
@@ -726,7 +701,6 @@ template <int TY, bool DX, int BB, int RB, bool FEW>
 __global__ __launch_bounds__(LT) void lora_expand_kernel(LoraArgs p) {
   extern __shared__ __attribute__((aligned(16))) uint8_t ts[];
   __shared__ __attribute__((aligned(16))) uint8_t xp[4][kWaveLds];
-  __shared__ float factor[kLoraTile];
   __shared__ int rows[kLoraTile];
   // one column slice of all tiles after another (slices of one tile next to each other: 20%
   // slower, the adapters' operands then leave the L2s)
@@ -738,17 +712,16 @@ __global__ __launch_bounds__(LT) void lora_expand_kernel(LoraArgs p) {
   if (s0 >= s1) return;
   const int wave = threadIdx.x >> 6;
   const int64_t W = DX ? p.K : p.N;  // output columns, at least 64
-  ColumnGroup<TY, DX, BB, RB> g(p, t, rows, ts, factor, xp[wave], s0, s1);
+  ColumnGroup<TY, DX, BB, RB> g(p, t, rows, ts, xp[wave], s0, s1);
   int64_t g0 = ((int64_t)slice * 4 + wave) * 64;
   if (g0 < W) g.begin(g0);
   if constexpr (FEW) {
     // [splits][rows][rp] sums, then [rows][rp + 32] of t, behind the pieces
-    const Pieces<TY> pc(p.r);
+    const Pieces pc(p.r);
     const int n = (t.count < 16 * s1 ? t.count : 16 * s1) - 16 * s0, rp = p.rp, quads = rp / 4, ld = rp + 32;
     const bool keep = p.T && slice == 0;
     float* sums = (float*)(ts + kLoraTile / (int)gridDim.y * pc.row_bytes());
     float* tf = sums + p.splits * n * rp;
-    uint32_t* top = (uint32_t*)xp;
     if (t.a < p.L) {
       for (int i = threadIdx.x; i < p.splits * n * quads; i += LT) {
         const int s = i / (n * quads), k = i % (n * quads);
@@ -766,19 +739,18 @@ __global__ __launch_bounds__(LT) void lora_expand_kernel(LoraArgs p) {
         tf[i] = v * sc;
       }
       __syncthreads();
-      split_rows<TY, LT>(tf, ld, n, pc, ts, pc.row_bytes(), factor, top);
+      split_rows<LT>(tf, ld, n, pc, ts, pc.row_bytes());
     } else if (keep) {
       for (int i = threadIdx.x; i < n * p.r; i += LT) p.T[(int64_t)rows[16 * s0 + i / p.r] * p.r + i % p.r] = 0.0f;
     }
   } else if (t.a < p.L) {  // the rows' pieces of t (rows past the tile: those of its last row, unused)
-    const Pieces<TY> pc(p.r);
+    const Pieces pc(p.r);
     const int per_row = pc.steps * 4;
     for (int i = threadIdx.x; i < (s1 - s0) * 16 * per_row; i += LT) {
       const int k = i / per_row, c = i - k * per_row;
       const int row = 16 * s0 + k < t.count ? 16 * s0 + k : t.count - 1;
       const uint8_t* from = p.pieces + position(p, t, rows, row) * (per_row * 16);
       *(uint4*)(ts + k * pc.row_bytes() + c * 16) = *(const uint4*)(from + c * 16);
-      if (TY == QMM_F16 && c == 0) factor[k] = p.factor[position(p, t, rows, row)];
     }
   }
   __syncthreads();
@@ -1028,7 +1000,7 @@ hipError_t expand(LoraArgs p, const float* dT, hipStream_t st) {
   // (FEW is planned for 16 rows' parts)
   const int apart = (p.M > 16 && (p.few || tiles * p.slices < 1024)) || p.r > 64 ? 4 : 1;
   const dim3 grid((unsigned)p.slots * (unsigned)p.slices, apart);
-  uint32_t lds = (uint32_t)(kLoraTile / apart * Pieces<TY>(p.r).row_bytes());
+  uint32_t lds = (uint32_t)(kLoraTile / apart * Pieces(p.r).row_bytes());
   if (p.few) {
     const int rows = std::min<int>((int)p.M, kLoraTile / apart);
     lds += (uint32_t)(rows * (p.splits * p.rp + p.rp + 32) * 4);
@@ -1062,9 +1034,7 @@ bool lora_few_rows(int64_t M, int64_t N, int r, int splits) {
          std::min<int64_t>(M, 16) * (splits * rp + rp + 32) * 4 <= 64 * 1024;
 }
 
-int lora_piece_bytes(int type, int r) {
-  return type == QMM_F16 ? Pieces<QMM_F16>(r).steps * 64 : Pieces<QMM_BF16>(r).steps * 64;
-}
+int lora_piece_bytes(int r) { return Pieces(r).steps * 64; }
 
 hipError_t launch_lora_plan(const LoraArgs& p, hipStream_t st) {
   launch(lora_plan_kernel, dim3((unsigned)(p.L + 1)), dim3(kPlanThreads), 0, st, p.ids, p.M, p.L, p.plan);
@@ -1084,8 +1054,7 @@ hipError_t launch_lora_shrink_dy(const LoraArgs& p, hipStream_t st) {
 hipError_t launch_lora_finalize(const LoraArgs& p, bool scaled, float* T, int64_t ldt, hipStream_t st) {
   const dim3 grid((unsigned)p.slots, 4);
   const uint32_t lds = (uint32_t)(16 * (p.rp + 32) * 4);
-  if (p.type == QMM_F16) launch(lora_finalize_kernel<QMM_F16>, grid, dim3(LT), lds, st, p, scaled ? 1 : 0, T, ldt);
-  else launch(lora_finalize_kernel<QMM_BF16>, grid, dim3(LT), lds, st, p, scaled ? 1 : 0, T, ldt);
+  launch(lora_finalize_kernel, grid, dim3(LT), lds, st, p, scaled ? 1 : 0, T, ldt);
   return hipSuccess;
 }
 

@@ -34,7 +34,7 @@ int splits(int64_t M, int64_t C) {
 }
 
 struct Layout {
-  size_t off = 0, perm = 0, tiles = 0, part = 0, pieces = 0, factor = 0, t = 0, dt = 0, db = 0, da = 0, total = 0;
+  size_t off = 0, perm = 0, tiles = 0, part = 0, pieces = 0, t = 0, dt = 0, db = 0, da = 0, total = 0;
   int chunk = 0;  // rows per chunk of the outer sums
 };
 
@@ -55,11 +55,8 @@ Layout layout(int64_t M, int64_t K, int64_t N, int r, int64_t L, bool grad) {
   const int s = grad ? std::max(splits(M, K), splits(M, N)) : splits(M, K);
   w.part = at;
   at += up256((size_t)s * (size_t)M * rp * 4);
-  // (the longer of the two types' pieces: the query has no type)
   w.pieces = at;
-  at += up256((size_t)M * (size_t)std::max(lora_piece_bytes(QMM_F16, r), lora_piece_bytes(QMM_BF16, r)));
-  w.factor = at;
-  at += up256((size_t)M * 4);
+  at += up256((size_t)M * (size_t)lora_piece_bytes(r));
   if (grad) {
     w.t = at;
     at += up256((size_t)M * rp * 4);
@@ -204,7 +201,6 @@ qmm_status qmm_lora_add(const void* X, int type, int64_t M, int64_t K, int64_t N
   if (e == hipSuccess) e = launch_lora_shrink_x(p, st);
   if (!p.few) {
     p.pieces = (uint8_t*)workspace + l.pieces;
-    p.factor = (float*)((uint8_t*)workspace + l.factor);
     if (e == hipSuccess) e = launch_lora_finalize(p, false, T, r, st);
   }
   if (e == hipSuccess) e = launch_lora_expand(p, st);
@@ -238,10 +234,7 @@ qmm_status qmm_lora_grad(const void* dY, const void* X, int type, int64_t M, int
     p.dY = dY;
     set_split(p, N);
     if (e == hipSuccess) e = launch_lora_shrink_dy(p, st);
-    if (dX) {
-      p.pieces = ws + l.pieces;
-      p.factor = (float*)(ws + l.factor);
-    }
+    if (dX) p.pieces = ws + l.pieces;
     if (e == hipSuccess) e = launch_lora_finalize(p, true, dt, p.rp, st);
   }
   if (dA || dB) {

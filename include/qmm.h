@@ -484,7 +484,9 @@ qmm_status qmm_validate_grouped_mm_grad(const void* dY, const void* X, int type,
  *   dT[m] = s_a * (B_a^T dy_m)           fp32
  *   dX[m] = base[m] + A_a^T dT[m]        base: the projection's own input gradient
  *   dA_a  = sum over its rows m of dT[m] x_m^T;  dB_a = s_a * sum over m of dy_m T[m]^T
- * (zeros for an adapter without rows).  T and dT are not rounded below fp32.
+ * (zeros for an adapter without rows).  T and dT are not rounded below fp32, whatever the range of
+ * a row's ranks; infinities and NaN give what the formulas give (where |T| >= 2^-86), in their own
+ * rows and adapters.
  *
  *   X [M][K], dY [M][N], A [L][r][K], B [L][N][r], all of `type` (QMM_F16 or QMM_BF16).
  *   ids   int32 [M] (device), in any order.   scale fp32 [L] (device) or NULL (1).
