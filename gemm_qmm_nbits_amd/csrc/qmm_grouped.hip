@@ -102,7 +102,8 @@ __global__ __launch_bounds__(WM* WN * 64) void grouped_kernel(GroupedArgs p) {
 
   // work-groups are dealt round-robin over the 8 XCDs: a unit of `jgroup` column tiles of one
   // row tile stays on one XCD, so that its a rows are fetched into one L2
-  const int x = (int)blockIdx.x & 7, q = (int)blockIdx.x >> 3;
+  const uint32_t at = tile_index();
+  const int x = (int)(at & 7u), q = (int)(at >> 3);
   const int unit = (q / p.jgroup) * 8 + x;
   const int groups = (p.jtiles + p.jgroup - 1) / p.jgroup;
   const int slot = unit / groups;
@@ -154,7 +155,7 @@ __global__ __launch_bounds__(WM* WN * 64) void grouped_kernel(GroupedArgs p) {
     for (int g = 0; g < FN; ++g) acc[f][g] = f32x16{};
 
   const int nst = (int)((C + KS - 1) / KS);
-  const int first = ROT && nst > 0 ? (int)((blockIdx.x * 2654435761u) >> 8) % nst : 0;
+  const int first = ROT && nst > 0 ? (int)((at * 2654435761u) >> 8) % nst : 0;
   auto copy = [&](int i, uint8_t* t) {  // the i-th stage this work-group takes
     int s = i;
     if (ROT && i < nst) s = i + first < nst ? i + first : i + first - nst;
@@ -275,7 +276,7 @@ void go_tile(GroupedArgs p, hipStream_t st) {
   p.jtiles = (int)((p.J + BN - 1) / BN);
   p.itiles = OP == GROUPED_DW ? (int)(p.E * ((p.I + BM - 1) / BM)) : (int)((p.R + BM - 1) / BM + std::min(p.E, p.R));
   p.jgroup = unit_tiles(p.itiles, p.jtiles);
-  const dim3 grid((unsigned)unit_slots(p.itiles, p.jtiles, p.jgroup));
+  const dim3 grid = tile_grid(unit_slots(p.itiles, p.jtiles, p.jgroup), WM * WN * 64);
   constexpr bool ROT = OP == GROUPED_MM && BM == 64;
   if (p.vec) launch((grouped_kernel<TY, BM, BN, WM, WN, OP, true, ROT>), grid, dim3(WM * WN * 64), 0, st, p);
   else launch((grouped_kernel<TY, BM, BN, WM, WN, OP, false, ROT>), grid, dim3(WM * WN * 64), 0, st, p);

@@ -240,6 +240,15 @@ static void launch_cast_at(const void* src, int64_t M, int64_t K, int64_t Kp, ui
 
 hipError_t launch_cast_pad_f16(const void* src, int src_type, int64_t M, int64_t K, int64_t Kp,
                                uint16_t* dst, float* row_scale, hipStream_t st) {
+  // a work-group per row: a launch holds less than 2^32 threads
+  constexpr int64_t kRows = 1LL << 23;
+  for (; M > kRows; M -= kRows) {
+    const hipError_t e = launch_cast_pad_f16(src, src_type, kRows, K, Kp, dst, row_scale, st);
+    if (e != hipSuccess) return e;
+    src = (const uint8_t*)src + kRows * K * (src_type == QMM_F32 ? 4 : 2);
+    dst += kRows * Kp;
+    row_scale += kRows;
+  }
   if (M <= 0) return hipSuccess;
   const bool vec = K % 8 == 0 && (uintptr_t)src % 16 == 0;
   if (src_type == QMM_F32) launch_cast_at<QMM_F32>(src, M, K, Kp, dst, row_scale, vec, st);

@@ -224,6 +224,16 @@ inline int64_t unit_slots(int64_t row_tiles, int col_tiles, int per_unit) {
   return (row_tiles * ((col_tiles + per_unit - 1) / per_unit) + 7) / 8 * 8 * per_unit;
 }
 
+// A grid of `groups` work-groups of `threads`: in x alone up to the launch's limit of 2^32 threads there,
+// else in rows of 2^20 (a multiple of the XCDs, so that the dealing goes on); the places past the last
+// group lie past every tile.
+inline dim3 tile_grid(int64_t groups, int threads) {
+  if (groups * threads < (1LL << 32)) return dim3((unsigned)groups);
+  constexpr int64_t row = 1 << 20;
+  return dim3((unsigned)row, (unsigned)((groups + row - 1) / row));
+}
+__device__ __forceinline__ uint32_t tile_index() { return blockIdx.y * gridDim.x + blockIdx.x; }
+
 // Waits until this wave's copies into LDS but the newest N, and all its LDS accesses, are
 // done, then for the other waves of the work-group: after it, every wave's copies older than
 // those are in LDS, and no wave still reads what they had read before.
