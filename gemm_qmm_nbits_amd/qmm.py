@@ -16,6 +16,7 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libqmm.so")
 
 QMM_F32, QMM_F16, QMM_BF16 = 0, 1, 2
+QMM_E_BITS, QMM_E_BLOCK = -3, -4
 QMM_ZP_NONE, QMM_ZP_PACKED, QMM_ZP_F16, QMM_ZP_UNIFORM = 0, 1, 2, 3
 QMOE_FP, QMOE_INT8_ACT = 0, 1
 STATUS = {0: "QMM_OK", -1: "QMM_E_NULL", -2: "QMM_E_DTYPE", -3: "QMM_E_BITS", -4: "QMM_E_BLOCK",
@@ -674,9 +675,14 @@ def qmm_lora_grad(dY, X, A, B, ids, scale=None, T=None, base=None, dX=None, dA=N
 # input gradients of low-bit projections
 # ---------------------------------------------------------------------------
 
-def _dgrad_shapes(dY, W, K, block, bits, out, out_dtype, stream):
+def _dgrad_shapes(name, dY, W, K, block, bits, out, out_dtype, stream):
     """Checks dY [M, N] and the packed weights W [N, nblk, block * bits / 8]."""
     ty = _types()
+    # the format first, as the shapes are computed from it
+    if bits not in (2, 3, 4, 8):
+        raise QmmError(name, QMM_E_BITS)
+    if block not in (16, 32, 64, 128, 256) or (bits == 3 and block == 16):
+        raise QmmError(name, QMM_E_BLOCK)
     if dY.dim() != 2:
         raise ValueError("dY must be [M, N]")
     M, N = dY.shape
@@ -714,7 +720,8 @@ def qmm_nbits_dgrad(dY, W, scales, K, bits, block, zp=None, zp_kind=QMM_ZP_NONE,
     """dX[M, K] = dY[M, N] . dequant(W): the input gradient of qmm_nbits, from the same weight buffers.
 
     f32: dY and the weights enter the products as they are (qmm_nbits_dgrad_f32), not rounded to fp16."""
-    dev, code, M, N, out, out_t = _dgrad_shapes(dY, W, K, block, bits, out, out_dtype, stream)
+    name = "qmm_nbits_dgrad_f32" if f32 else "qmm_nbits_dgrad"
+    dev, code, M, N, out, out_t = _dgrad_shapes(name, dY, W, K, block, bits, out, out_dtype, stream)
     nblk = nblocks(K, block)
     s_p = _sized(scales, "scales", N * nblk, 2, dev)
     z_p = None
@@ -723,7 +730,6 @@ def qmm_nbits_dgrad(dY, W, scales, K, bits, block, zp=None, zp_kind=QMM_ZP_NONE,
     elif zp is not None and zp_kind == QMM_ZP_F16:
         z_p = _sized(zp, "zp", N * nblk, 2, dev)
     keep, ws, wsb = _dgrad_workspace(f32, workspace, code, M, K, N, dY, stream)
-    name = "qmm_nbits_dgrad_f32" if f32 else "qmm_nbits_dgrad"
     st = getattr(lib(), name)(dY.data_ptr(), code, M, K, N, W.data_ptr(), bits, block, s_p, z_p, zp_kind,
                               float(uniform_zp), out.data_ptr(), out_t, ws, wsb, _handle(stream, dev))
     _check(name, st)
@@ -734,11 +740,11 @@ def qmm_codebook4_dgrad(dY, W, absmax, codebook, K, block=64, out=None, out_dtyp
                         f32=False):
     """dX[M, K] = dY[M, N] . (codebook[q] * absmax): the input gradient of qmm_codebook4 (f32: as
     qmm_nbits_dgrad)."""
-    dev, code, M, N, out, out_t = _dgrad_shapes(dY, W, K, block, 4, out, out_dtype, stream)
+    name = "qmm_codebook4_dgrad_f32" if f32 else "qmm_codebook4_dgrad"
+    dev, code, M, N, out, out_t = _dgrad_shapes(name, dY, W, K, block, 4, out, out_dtype, stream)
     a_p = _sized(absmax, "absmax", N * nblocks(K, block), 4, dev)
     c_p = _sized(codebook, "codebook", 16, 4, dev)
     keep, ws, wsb = _dgrad_workspace(f32, workspace, code, M, K, N, dY, stream)
-    name = "qmm_codebook4_dgrad_f32" if f32 else "qmm_codebook4_dgrad"
     st = getattr(lib(), name)(dY.data_ptr(), code, M, K, N, W.data_ptr(), block, a_p, c_p, out.data_ptr(), out_t, ws,
                               wsb, _handle(stream, dev))
     _check(name, st)

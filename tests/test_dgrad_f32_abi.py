@@ -80,3 +80,23 @@ def test_pieces_hold_the_weights(n, top):
     assert np.abs(total / w - 1).max() <= 2.0 ** -38
     for v in p:
         assert v.all() and np.array_equal(np.sign(v), np.sign(w))
+
+
+@pytest.mark.parametrize("f32", [False, True])
+def test_binding_refuses_formats_by_status(f32):
+    """The statuses of qmm_nbits for bits and blocks, before any shape is computed from them."""
+    import torch
+
+    dY, W = torch.zeros(2, 32, dtype=torch.bfloat16), torch.zeros(32, 64, dtype=torch.uint8)
+    s = torch.ones(32 * 16, dtype=torch.float16)
+    for block in (0, -64, 8, 48, 512):
+        with pytest.raises(Q.QmmError) as e:
+            Q.qmm_nbits_dgrad(dY, W, s, 128, 4, block, f32=f32)
+        assert e.value.status == -4
+        with pytest.raises(Q.QmmError) as e:
+            Q.qmm_codebook4_dgrad(dY, W, s.float(), torch.ones(16), 128, block, f32=f32)
+        assert e.value.status == -4
+    for bits, block, status in ((5, 64, -3), (0, 64, -3), (3, 16, -4)):
+        with pytest.raises(Q.QmmError) as e:
+            Q.qmm_nbits_dgrad(dY, W, s, 128, bits, block, f32=f32)
+        assert e.value.status == status
