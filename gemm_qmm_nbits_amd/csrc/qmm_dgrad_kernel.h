@@ -13,6 +13,7 @@ namespace qmm {
 namespace {
 
 constexpr int kStage = kDgradStage;
+static_assert(kStage == kTileStage, "");
 
 // The 16 codes of one thread and stage, with their scale and zero point.
 template <int BITS>
@@ -88,11 +89,11 @@ __global__ __launch_bounds__(WM* WN * 64) void dgrad_kernel(DgradArgs p) {
     __syncthreads();
   }
 
-  TileLoad<BM, NW, kStage, false, true> la;
+  TileLoad<BM, NW, false, true> la;
   la.init(p.dY16 + m0 * p.lda, p.lda, p.M - m0, p.n16, wave, lane);
   const int wm = wave / WN, wn = wave % WN;
-  TileRead<BM, kStage, false> ra;
-  TileRead<BN, kStage, true> rb;
+  TileRead<BM, false> ra;
+  TileRead<BN, true> rb;
   ra.init(wm * FM * 32, lane);
   rb.init(wn * FN * 32, lane);
 
@@ -150,7 +151,7 @@ __global__ __launch_bounds__(WM* WN * 64) void dgrad_kernel(DgradArgs p) {
     }
   };
   // half of the group (8 codes) into the tile: piece kc / 8 + half of row c, swizzled
-  const uint32_t seg_x = BN == 64 ? (uint32_t)((c >> 1) & 1) : (uint32_t)(c & 3);
+  const uint32_t seg_x = (uint32_t)(c & 3);
   auto store_w = [&](const Codes<BITS>& q, uint8_t* tile, int half) {
     uint32_t xw, xw2 = 0;
     if constexpr (BITS == 2) xw = q.w[0] >> (16 * half);

@@ -88,7 +88,7 @@ __device__ __forceinline__ void store_tile(const GroupedArgs& p, const f32x16 (&
 // work-groups that stream rows of one pitch do not ask the same memory channels at once.
 template <int TY, int BM, int BN, int WM, int WN, int OP, bool VEC, bool ROT>
 __global__ __launch_bounds__(WM* WN * 64) void grouped_kernel(GroupedArgs p) {
-  constexpr int NW = WM * WN, KS = 32;
+  constexpr int NW = WM * WN, KS = kTileStage;
   constexpr bool AX = OP == GROUPED_DW;   // a across
   constexpr bool BX = OP != GROUPED_MM;   // b across
   constexpr int FM = BM / WM / 32, FN = BN / WN / 32;
@@ -130,8 +130,8 @@ __global__ __launch_bounds__(WM* WN * 64) void grouped_kernel(GroupedArgs p) {
   const int64_t I = OP == GROUPED_DW ? p.I : o1 - o0;  // rows of this expert's output
   const int64_t C = OP == GROUPED_DW ? o1 - o0 : p.C;
 
-  TileLoad<BM, NW, KS, AX, VEC> la;
-  TileLoad<BN, NW, KS, BX, VEC> lb;
+  TileLoad<BM, NW, AX, VEC> la;
+  TileLoad<BN, NW, BX, VEC> lb;
   const uint16_t* a = (const uint16_t*)p.a;
   const uint16_t* b = (const uint16_t*)p.b;
   if constexpr (OP == GROUPED_DW) {
@@ -143,8 +143,8 @@ __global__ __launch_bounds__(WM* WN * 64) void grouped_kernel(GroupedArgs p) {
     else lb.init(b + e * C * p.J + j0, p.J, p.J - j0, C, wave, lane);
   }
   const int wm = wave / WN, wn = wave % WN;
-  TileRead<BM, KS, AX> ra;
-  TileRead<BN, KS, BX> rb;
+  TileRead<BM, AX> ra;
+  TileRead<BN, BX> rb;
   ra.init(wm * FM * 32, lane);
   rb.init(wn * FN * 32, lane);
 

@@ -1,18 +1,18 @@
-// Tiles of 16-bit operands in LDS for the matrix cores: how a stage of KS contraction values
-// (32 or 64) is copied in and read back as operands of v_mfma_f32_32x32x16.
+// Tiles of 16-bit operands in LDS for the matrix cores: how a stage of 32 contraction values is
+// copied in and read back as operands of v_mfma_f32_32x32x16.
 //
-// An operand tile holds T rows (output rows or columns) by KS contraction values, in one of
+// An operand tile holds T rows (output rows or columns) by 32 contraction values, in one of
 // two forms, by how the operand lies in memory:
-//   along   the contraction runs along memory rows: [T][KS], 2 KS bytes per tile row.  A lane's
-//           operand (8 consecutive contraction values of one row) is one 16-byte read.  64 values
-//           are whole 128-byte lines; 32 values fetch every line twice.
-//   across  the contraction runs down memory columns: [KS][T], 2 T bytes per contraction
+//   along   the contraction runs along memory rows: [T][32], 64 bytes per tile row (half of a
+//           128-byte line, so every line is fetched twice).  A lane's operand (8 consecutive
+//           contraction values of one row) is one 16-byte read.
+//   across  the contraction runs down memory columns: [32][T], 2 T bytes per contraction
 //           value.  A lane's operand is two ds_read_b64_tr_b16, each of which hands a group
 //           of 16 lanes a 4 x 16 block transposed.
 // Either way tiles are filled by direct global->LDS copies of 16 bytes per lane, which write
 // LDS in lane order, so the bank swizzle is applied by choosing which 16 bytes a lane fetches:
-//   along   KS = 32: piece p (of 4) of row r sits at p ^ ((r / 4) % 4); KS = 64: piece p (of 8) at
-//           p ^ ((r / 2) % 8): 16 rows read at one piece cover the 16 bank groups of 256 bytes.
+//   along   piece p (of 4) of row r sits at p ^ ((r / 4) % 4): 16 rows read at one piece cover the
+//           16 bank groups of 256 bytes.
 //   across  the 64-byte segment s of contraction row c sits at s ^ (c % 4) (T = 64, two segments:
 //           s ^ ((c / 2) % 2)): the four rows of a transposed read lie in four bank quarters.
 // Bytes outside the operand (rows past the end, contraction values past the end) read as zero:
@@ -28,6 +28,7 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 
 constexpr uint32_t kPastRange = 0x80000000u;     // an offset past every descriptor's range
 constexpr uint32_t kTileRange = 0x7fffffffu;
+constexpr int kTileStage = 32;                   // contraction values of a stage
 
 typedef __attribute__((address_space(3))) uint8_t lds_u8;
 
@@ -42,8 +43,9 @@ __device__ __forceinline__ f32x16 mfma32(const uint4& a, const uint4& b, f32x16 
 
 // Copies one operand's tiles.  T: tile rows; NW: waves; ACROSS: the form; VEC: 16-byte
 // copies (else element loads through registers).
-template <int T, int NW, int KS, bool ACROSS, bool VEC>
+template <int T, int NW, bool ACROSS, bool VEC>
 struct TileLoad {
+  static constexpr int KS = kTileStage;
   static constexpr int kPer = T * KS * 2 / 1024 / NW;  // copies per wave and stage
   static_assert(kPer >= 1, "every wave copies, so that all wait for the same count");
   const uint8_t* base;  // first row (along) or first contraction row (across)
@@ -72,7 +74,7 @@ struct TileLoad {
         off[q] = piece * 8 < width ? (uint32_t)(c * ld) + (uint32_t)piece * 16u : kPastRange;
       } else {
         const int r = at / (2 * KS), pos = (at % (2 * KS)) / 16;
-        const int piece = pos ^ (KS == 32 ? (r >> 2) & 3 : (r >> 1) & 7);
+        const int piece = pos ^ ((r >> 2) & 3);
         crow[q] = piece * 8;
         off[q] = r < rows ? (uint32_t)(r * ld) + (uint32_t)piece * 16u : kPastRange;
       }
@@ -125,8 +127,9 @@ struct TileLoad {
 
 // Reads operands of one 32-row fragment.  The lane part of the address is fixed; `row` (a
 // multiple of 32) and the 16 contraction values are constants of the code.
-template <int T, int KS, bool ACROSS>
+template <int T, bool ACROSS>
 struct TileRead {
+  static constexpr int KS = kTileStage;
   uint32_t at;     // along: byte of row lane % 32;  across: byte of this lane's block row
   uint32_t sw;     // along: the piece exclusive-or;  across: the segment exclusive-or
 
@@ -138,7 +141,7 @@ struct TileRead {
       at = (uint32_t)(c * 2 * T + ((g & 1) * 16 + 4 * (i & 3)) * 2);
     } else {
       const int r = lane & 31;
-      sw = (uint32_t)(KS == 32 ? (r >> 2) & 3 : (r >> 1) & 7);
+      sw = (uint32_t)((r >> 2) & 3);
       at = (uint32_t)((row0 + r) * 2 * KS);
     }
     seg0 = row0 / 32;
