@@ -12,16 +12,16 @@
 // s + 1 (loaded two stages ago) are dequantized between the two halves of the stage's
 // matrix instructions.
 //
-// 2048 x 5120 x 7680, 4-bit, block 64: 187 us, 861 TFLOP/s (the dense kernel of qmm_grouped.hip at
+// 2048 x 5120 x 7680, 4-bit, block 64: 182 us, 886 TFLOP/s (the dense kernel of qmm_grouped.hip at
 // 8192^3: 1250), matrix units about half busy, the rest waits and dequantization (28% of the vector
-// issue slots), plus 20 us for the cast of dY and 32 for the three splits' sums; with every row
-// tile of a column tile on one XCD, so that dY16 was read anew per column tile, 258 us.  16 rows,
-// codebook, 4096 x 14336: 24 us against 6.6 for its bytes, bound by the codebook's LDS reads and the
-// dequantization's vector instructions (about 40% busy each) between barriers.
+// issue slots), plus 22 us for the cast of dY and 31 for the three splits' sums: 235 the call; with
+// every row tile of a column tile on one XCD, so that dY16 was read anew per column tile, 258 us.
+// Codebook, 2048 x 4096 x 14336: 265 + 31 + 21 = 317.  16 rows, codebook, 4096 x 14336: 23 us (33 the
+// call) against 6.6 for its bytes, bound by the codebook's LDS reads and the dequantization's vector
+// instructions (about 40% busy each) between barriers.
 //
 // When the tiles do not fill the chip the contraction is split; fp32 partial sums are added
-// in split order by a second kernel.  The sums' order depends only on
-// the shape.
+// in split order by a second kernel.  The sums' order depends only on the shape.
 #include "qmm_dgrad_kernel.h"
 
 #include <algorithm>
@@ -31,7 +31,8 @@ namespace qmm {
 namespace {
 
 // out = rs[m] * (((P[0] + P[1]) + ...) + P[S - 1]): four columns per thread, eight splits' loads
-// under way at once.
+// under way at once.  Where M K is no multiple of 4 the partial sums of a split lie unaligned to the
+// next one's and are read one by one: 1 x 1023 x 8192 takes 50 us a call, 1 x 1024 x 8192 16.
 __global__ __launch_bounds__(256) void dgrad_reduce_kernel(const float* P, int S, int64_t M, int64_t K, const float* rs,
                                                            void* out, int out_type) {
   const int64_t total = M * K, quads = (total + 3) / 4;

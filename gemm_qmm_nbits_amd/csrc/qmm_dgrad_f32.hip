@@ -10,9 +10,10 @@
 // the pieces of a weight are tiles of their own in LDS, made from one dequantization (qmm_dgrad_kernel.h).
 //
 // 2048 x 5120 x 7680, 4-bit, packed zero points (2 pieces), us a call, with the relative L2 error of an
-// fp32 dX, against the fp16 form: bf16 dY 312 (4e-7) / 245 (2e-4), fp16 dY 588 / 202; 8-bit (3 pieces)
-// 567 / 236; codebook 2048 x 4096 x 14336 736 / 319.  Bound by the matrix work.  Few rows: 16 x 4096 x
-// 14336, codebook, 48 / 34; 1 x 5120 x 7680 25 / 25.
+// fp32 dX, against the fp16 form: bf16 dY 304 (4e-7) / 235 (2e-4), fp16 dY 588 / 202; 8-bit (3 pieces)
+// 567 / 236; codebook 2048 x 4096 x 14336 736 / 317.  Bound by the matrix work (the first: 282 us in the
+// product, 1140 TFLOP/s of pieces, and 21 for the join).  Few rows: 16 x 4096 x 14336, codebook, 48 / 34
+// (43 in the product); 1 x 5120 x 7680 25 / 25.
 #include "qmm_dgrad_kernel.h"
 
 namespace qmm {

@@ -88,7 +88,9 @@ __device__ __forceinline__ uint4 load8(const uint16_t* row, int64_t i, int64_t n
 // first sweeps count the rows of earlier groups (the group's first position), the second
 // ones scan the group's own rows over the threads and write them in order.  Every group's
 // place depends only on the ids, so one launch does it.  An id outside [0, L) is group L.
-// (8192 rows: 4 us, two reads of the ids and two scans; a loop over single ids took 12.)
+// (8192 rows: 4 us, two reads of the ids and two scans; a loop over single ids took 12.)  Every group reads
+// all ids, so the time grows as M L: a call on 500 rows takes 18 us with 64 adapters loaded, 33 with 1024,
+// 110 with 8192 and 376 with 32768.
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanSweep = kPlanThreads * 8;
 
@@ -384,8 +386,9 @@ __device__ __forceinline__ f32x4 sum_parts(const LoraArgs& p, const float* q) {
 // Rows need no alignment (a vector access may start at any element).  The last group of a
 // width that is no multiple of 64 starts at width - 64 and stores its new columns only.
 //
-// 4096 x 35840, rank 32, fp32 base, bf16 out: 196 us for 881 MB (4.5 TB/s); a kernel that only copies
-// that base to that output takes 150 to 175.  dX of 8192 x 5120, rank 16: 64 us for 252 MB.  (Lanes
+// 4096 x 35840, rank 32, fp32 base, bf16 out: 192 us for 881 MB (4.6 TB/s), fp16 about 15 more; a kernel
+// that only copies that base to that output takes 150 to 175.  dX of 8192 x 5120, rank 16: 66 us for
+// 252 MB.  (Lanes
 // that keep their matrix layout and write 32-byte pieces of 16 rows: 485 us; t summed from the
 // splits in every work-group: 286.)
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));

@@ -116,3 +116,38 @@ def test_a_stream_of_the_tensors_device_is_needed():
 
     with pytest.raises(ValueError):
         Q._handle(Other, 0)
+
+
+@pytest.mark.parametrize("M,K,r", [(40, 96, 300), (12, 8200, 64), (300, 128, 512)])
+@pytest.mark.parametrize("ty", ["float16", "bfloat16"])
+def test_captured_adapters_of_high_rank(M, K, r, ty):
+    """Forms whose shared memory passes 32 KB (its limit is raised per call) captured, the first call of
+    their shape included, and replayed between eager calls."""
+    t = torch()
+    g = t.Generator(device="cuda").manual_seed(M)
+    N, L = 192, 2
+
+    def randn(*shape):
+        return t.randn(*shape, device="cuda", generator=g).to(getattr(t, ty))
+
+    X, dY, A, B = randn(M, K), randn(M, N), randn(L, r, K), randn(L, N, r)
+    ids = t.randint(-1, L, (M,), dtype=t.int32, device="cuda", generator=g)
+    outs = [t.empty_like(dY), t.empty_like(X), t.empty(L, r, K, device="cuda"), t.empty(L, N, r, device="cuda")]
+
+    def step(o):
+        Q.qmm_lora_add(X, A, B, ids, out=o[0])
+        Q.qmm_lora_grad(dY, X, A, B, ids, dX=o[1], dA=o[2], dB=o[3])
+        return o
+
+    t.cuda.synchronize()
+    graph = t.cuda.CUDAGraph()
+    with t.cuda.graph(graph):
+        step(outs)
+    x0 = X.clone()
+    for k in range(3):
+        X.copy_(x0 * (k + 1))
+        graph.replay()
+        t.cuda.synchronize()
+        got = [host_bits(v).copy() for v in outs]
+        for a, b in zip(got, step([t.empty_like(v) for v in outs])):
+            assert np.array_equal(a, host_bits(b)), k
