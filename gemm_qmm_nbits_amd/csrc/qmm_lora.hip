@@ -449,7 +449,8 @@ constexpr int kAp = 72;           // 16-bit elements of a rank's 64 columns ther
 constexpr int kWaveLds = 4608;    // bytes of that piece: 16 rows of sums, or 32 ranks of A
 static_assert(16 * kXp * 4 <= kWaveLds && 32 * kAp * 2 <= kWaveLds, "");
 
-// Pieces of t: truncations to bf16, t = p0 + p1 + p2 exactly (8 bits each), whatever its magnitude.
+// Pieces of t: truncations to bf16, t = p0 + p1 + p2 exactly (8 bits each) but for what lies below
+// bf16's smallest value, 2^-133.
 // Every piece but the first also takes t 2^-40, so that no piece of a value other than 0 is 0 (down to
 // 2^-86) and an infinite weight times the pieces is what it is times t; all pieces of an infinite t are
 // infinite.  With up to 16 ranks a contraction step has places left: they take a fourth piece.

@@ -406,7 +406,8 @@ qmm_status qmm_codebook4_dgrad(const void* dY, int dy_type, int64_t M, int64_t K
 size_t qmm_dgrad_workspace_bytes(int64_t M, int64_t K, int64_t N);
 
 /* The same gradients with dY and the dequantized weights as they are: only the fp32 sums and dX are
- * rounded, as in the forward product with up to 8 rows.  For fp32 dX (relative L2 <= 1e-5), for weights
+ * rounded, as in the forward product with up to 8 rows (what of a value lies below 2^-133 is
+ * dropped).  For fp32 dX (relative L2 <= 1e-5), for weights
  * that fp16 does not hold (below 6e-5 it loses their bits: small absmax or scales) and for gradients
  * of a wide range in one row.  Costs about twice the matrix work for codes of up to 4 bits with
  * integer zero points, three times it otherwise, twice that for fp16 dY and three times for fp32 dY;
@@ -491,8 +492,8 @@ qmm_status qmm_validate_grouped_mm_grad(const void* dY, const void* X, int type,
  *   dX[m] = base[m] + A_a^T dT[m]        base: the projection's own input gradient
  *   dA_a  = sum over its rows m of dT[m] x_m^T;  dB_a = s_a * sum over m of dy_m T[m]^T
  * (zeros for an adapter without rows).  T and dT are not rounded below fp32, whatever the range of
- * a row's ranks; infinities and NaN give what the formulas give (where |T| >= 2^-86), in their own
- * rows and adapters.
+ * a row's ranks (what of a value lies below 2^-133 is dropped); infinities and NaN give what the
+ * formulas give (where |T| >= 2^-86), in their own rows and adapters.
  *
  *   X [M][K], dY [M][N], A [L][r][K], B [L][N][r], all of `type` (QMM_F16 or QMM_BF16).
  *   ids   int32 [M] (device), in any order.   scale fp32 [L] (device) or NULL (1).

@@ -118,6 +118,29 @@ def test_a_stream_of_the_tensors_device_is_needed():
         Q._handle(Other, 0)
 
 
+@pytest.mark.parametrize("name", NAMES[:-1])
+def test_captured_on_a_forked_stream(name):
+    """A call on a given stream that a captured one forked: its memory is the graph's, and replays repeat
+    the call's results."""
+    t = torch()
+    call, _ = entries()[name]
+    want = [host_bits(v).copy() for v in call(None)]
+    side = t.cuda.Stream()
+    t.cuda.synchronize()
+    graph = t.cuda.CUDAGraph()
+    with t.cuda.graph(graph):
+        side.wait_stream(t.cuda.current_stream())
+        outs = list(call(side))
+        t.cuda.current_stream().wait_stream(side)
+    for _ in range(3):
+        for v in outs:
+            v.zero_()
+        graph.replay()
+        t.cuda.synchronize()
+        assert all(np.array_equal(host_bits(v), b) for v, b in zip(outs, want))
+        call(None)
+
+
 @pytest.mark.parametrize("M,K,r", [(40, 96, 300), (12, 8200, 64), (300, 128, 512)])
 @pytest.mark.parametrize("ty", ["float16", "bfloat16"])
 def test_captured_adapters_of_high_rank(M, K, r, ty):
