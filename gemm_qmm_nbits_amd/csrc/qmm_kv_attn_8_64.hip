@@ -1,0 +1,6 @@
+// Attention over the low-bit cache: 8-bit codes, heads of 64 dimensions.
+#include "qmm_kv_attn.h"
+
+namespace qmm {
+hipError_t launch_kv_attn_8_64(const KvAttnArgs& p, hipStream_t st) { return kv::by_group<8, 64>(p, st); }
+}  // namespace qmm

@@ -49,6 +49,11 @@ class qmm_lora_weights(Structure):
     _fields_ = [("A", c_void_p), ("B", c_void_p), ("scale", c_void_p)]
 
 
+class qkv_cache(Structure):
+    _fields_ = [("k", c_void_p), ("v", c_void_p), ("k_params", c_void_p), ("v_params", c_void_p), ("pages", c_int64),
+                ("heads", c_int), ("page", c_int), ("D", c_int), ("bits", c_int), ("group", c_int)]
+
+
 _lib = None
 
 _SIGS = {
@@ -140,6 +145,19 @@ _SIGS = {
     "qmm_validate_lora_grad": (c_int, [c_void_p, c_void_p, c_int, c_int64, c_int64, c_int64, c_int, c_int64,
                                        c_void_p, qmm_lora_weights, c_void_p, c_void_p, c_int, c_void_p, c_int,
                                        c_void_p, c_void_p, c_int, c_void_p, c_size_t]),
+    "qkv_cache_store": (c_int, [c_void_p, c_int64, c_int64, c_void_p, c_int64, c_int64, c_int, c_int64, c_void_p,
+                                POINTER(qkv_cache), c_void_p]),
+    "qkv_cache_load": (c_int, [POINTER(qkv_cache), c_void_p, c_int64, c_void_p, c_void_p, c_int, c_void_p]),
+    "qkv_attention": (c_int, [c_void_p, c_int64, c_int64, c_int, c_int64, c_int, c_int64, c_void_p, c_void_p, c_void_p,
+                              c_int64, c_int64, c_int64, c_float, c_int, c_int64, c_void_p, POINTER(qkv_cache),
+                              c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "qkv_attention_workspace_bytes": (c_size_t, [c_int64, c_int, c_int, c_int, c_int64, c_int64, c_int64]),
+    "qmm_validate_kv_store": (c_int, [c_void_p, c_int64, c_int64, c_void_p, c_int64, c_int64, c_int, c_int64, c_void_p,
+                                      POINTER(qkv_cache)]),
+    "qmm_validate_kv_load": (c_int, [POINTER(qkv_cache), c_void_p, c_int64, c_void_p, c_void_p, c_int]),
+    "qmm_validate_kv_attention": (c_int, [c_void_p, c_int64, c_int64, c_int, c_int64, c_int, c_int64, c_void_p,
+                                          c_void_p, c_void_p, c_int64, c_int64, c_int64, c_float, c_int, c_int64,
+                                          c_void_p, POINTER(qkv_cache), c_void_p, c_void_p, c_void_p, c_size_t]),
     "qmm_hbm_read_probe": (c_int, [c_void_p, c_int64, c_void_p, c_int, c_void_p]),
     "qmm_launch_timing_begin": (c_int, [c_int]),
     "qmm_launch_timing_end": (c_int, [c_void_p, c_int, c_void_p]),
@@ -811,6 +829,163 @@ def qmoe_grouped_mm_grad(dY, X, row_offsets, W, dX=None, dW=None, dbias=None, dx
                                     _handle(stream, dev))
     _check("qmoe_grouped_mm_grad", st)
     return dX, dW, dbias
+
+
+# ---------------------------------------------------------------------------
+# low-bit key/value cache
+# ---------------------------------------------------------------------------
+
+def qkv_cache_new(pages, heads, D, bits=4, group=64, page=64, device=None, stream=None):
+    """An empty cache (every slot reads as zeros): a dict of its pools k, v (codes), k_params, v_params
+    (scales and offsets) and its format bits, group.  `device`: the current one when not given.
+    With a stream, fill and use it there."""
+    if bits not in (4, 8):
+        raise QmmError("qkv_cache_new", QMM_E_BITS)
+    if group not in (32, 64, 128) or group > D:
+        raise QmmError("qkv_cache_new", QMM_E_BLOCK)
+    ty = _types()
+    like = _Place(ty.torch.device("cuda", ty.torch.cuda.current_device()) if device is None
+                  else ty.torch.device(device))
+
+    def pool(row_bytes):
+        return _temporary(pages * heads * page * row_bytes, like, stream, zeroed=True)
+
+    def params():
+        return pool(4 * (D // group)).view(ty.torch.float16).view(pages, heads, page, 2, D // group)
+
+    return dict(k=pool(D * bits // 8).view(pages, heads, page, -1), v=pool(D * bits // 8).view(pages, heads, page, -1),
+                k_params=params(), v_params=params(), bits=bits, group=group)
+
+
+class _Place:
+    def __init__(self, device):
+        self.device = device
+
+
+def _kv_cache(cache):
+    """Checks a cache's tensors: device index, (pages, heads, page, D) and the descriptor."""
+    ty = _types()
+    k, bits, group = cache["k"], cache["bits"], cache["group"]
+    if bits not in (4, 8):
+        raise QmmError("qkv_cache", QMM_E_BITS)
+    if k.dim() != 4:
+        raise ValueError("k must be [pages, heads, page, D * bits / 8]")
+    pages, heads, page, row = k.shape
+    D = row * 8 // bits
+    if group not in (32, 64, 128) or D % group:
+        raise QmmError("qkv_cache", QMM_E_BLOCK)
+    dev = _device_of(k)
+    _expect(k, "k", k.shape, ty.u8, dev)
+    _expect(cache["v"], "v", k.shape, ty.u8, dev)
+    shape = (pages, heads, page, 2, D // group)
+    f16 = ty.only[ty.torch.float16]
+    _expect(cache["k_params"], "k_params", shape, f16, dev)
+    _expect(cache["v_params"], "v_params", shape, f16, dev)
+    c = qkv_cache(k.data_ptr(), cache["v"].data_ptr(), cache["k_params"].data_ptr(), cache["v_params"].data_ptr(),
+                  pages, heads, page, D, bits, group)
+    return ty, dev, heads, page, D, c
+
+
+def _rows_of(t, name, heads, D, codes, dev):
+    """Checks rows [T, heads, D] whose last dimension is dense: element-type code, row and head strides."""
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != D:
+        raise ValueError(f"{name} must be [T, {heads}, {D}], got {tuple(t.shape)}")
+    code = codes.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be one of {list(codes)}, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on the device of the call")
+    row, head, one = t.stride()
+    if one != 1:
+        raise ValueError(f"the last dimension of {name} must be dense")
+    return code, row, head
+
+
+def qkv_cache_store(K, V, slots, cache, stream=None):
+    """Quantizes the keys and values [T, heads, D] of T tokens into the cache's slots (int32 [T], slot = page id *
+    page + place; one outside the pool: not stored; of tokens with one slot the last is stored).
+
+    K and V may be slices of a fused projection's output: any row and head strides, the last dimension dense."""
+    ty, dev, heads, page, D, c = _kv_cache(cache)
+    code, krs, khs = _rows_of(K, "K", heads, D, ty.any, dev)
+    T = K.shape[0]
+    vcode, vrs, vhs = _rows_of(V, "V", heads, D, ty.any, dev)
+    if V.shape[0] != T or vcode != code:
+        raise ValueError("K and V differ in their number of rows or dtype")
+    _expect(slots, "slots", (T,), ty.i32, dev)
+    st = lib().qkv_cache_store(K.data_ptr(), krs, khs, V.data_ptr(), vrs, vhs, code, T, slots.data_ptr(),
+                               ctypes.byref(c), _handle(stream, dev))
+    _check("qkv_cache_store", st)
+
+
+def qkv_cache_load(cache, slots, out_dtype=None, K=None, V=None, need=(True, True), stream=None):
+    """The keys and values [T, heads, D] that the slots hold (zeros for a slot outside the pool), of out_dtype
+    (default fp32); need: whether keys and values are read (None in the place of one that is not)."""
+    ty, dev, heads, page, D, c = _kv_cache(cache)
+    T = slots.shape[0]
+    _expect(slots, "slots", (T,), ty.i32, dev)
+    if out_dtype is None:
+        given = K if K is not None else V
+        out_dtype = ty.torch.float32 if given is None else given.dtype
+    if K is None and need[0]:
+        K = _new((T, heads, D), out_dtype, cache["k"], stream)
+    if V is None and need[1]:
+        V = _new((T, heads, D), out_dtype, cache["k"], stream)
+    k_p, k_t = _optional(K, "K", (T, heads, D), ty.any, dev)
+    v_p, v_t = _optional(V, "V", (T, heads, D), ty.any, dev)
+    if K is not None and V is not None and k_t != v_t:
+        raise TypeError("K and V differ in dtype")
+    st = lib().qkv_cache_load(ctypes.byref(c), slots.data_ptr(), T, k_p, v_p, v_t if K is None else k_t,
+                              _handle(stream, dev))
+    _check("qkv_cache_load", st)
+    return K, V
+
+
+def qkv_attention(Q, cache, table, kv_len, cu_q=None, max_q=None, max_kv=None, scale=None, causal=True, window=0,
+                  sinks=None, out=None, lse=None, need_lse=False, workspace=None, stream=None):
+    """softmax(scale Q K^T) V over the cached tokens of B sequences: out [T, q_heads, D] of Q's dtype, or (out, lse)
+    with need_lse (or lse given): lse fp32 [T, q_heads].
+
+    Q [T, q_heads, D] fp16 or bf16 (any row and head strides); table int32 [B, width]: the pages of each sequence;
+    kv_len int32 [B]: its tokens, those of the queries included.  cu_q int32 [B + 1]: the queries of sequence b are the
+    rows cu_q[b] .. cu_q[b + 1] - 1, its last tokens (None: one query per sequence, T = B).  max_q: the most queries of
+    a sequence (default T), max_kv: the most tokens expected (default: the table's); host numbers, no device value is
+    read.  scale defaults to D ** -0.5; window > 0: the last `window` tokens up to the query's own; sinks fp32
+    [q_heads]: logits that take part in the sum only.  Rows of no sequence are not written."""
+    ty, dev, heads, page, D, c = _kv_cache(cache)
+    if Q.dim() != 3:
+        raise ValueError("Q must be [T, q_heads, D]")
+    T, q_heads = Q.shape[0], Q.shape[1]
+    code, row, head = _rows_of(Q, "Q", q_heads, D, ty.half, dev)
+    if q_heads % heads:
+        raise ValueError(f"{q_heads} query heads do not share {heads} cache heads evenly")
+    if table.dim() != 2:
+        raise ValueError("table must be [B, width]")
+    B, width = table.shape
+    _expect(table, "table", (B, width), ty.i32, dev)
+    _expect(kv_len, "kv_len", (B,), ty.i32, dev)
+    cu_p, _ = _optional(cu_q, "cu_q", (B + 1,), ty.i32, dev)
+    s_p, _ = _optional(sinks, "sinks", (q_heads,), ty.f32, dev)
+    if cu_q is None:
+        if T != B:
+            raise ValueError("without cu_q every sequence has one query: Q must be [B, q_heads, D]")
+        max_q = 1
+    elif max_q is None:
+        max_q = max(T, 1)
+    bound = max_kv or width * page
+    if out is None:
+        out = _new((T, q_heads, D), Q.dtype, Q, stream)
+    _expect(out, "out", (T, q_heads, D), ty.only[Q.dtype], dev)
+    if lse is None and need_lse:
+        lse = _new((T, q_heads), ty.torch.float32, Q, stream)
+    l_p, _ = _optional(lse, "lse", (T, q_heads), ty.f32, dev)
+    keep, ws, wsb = _scratch(workspace, _bytes_of("qkv_attention_workspace_bytes", T, q_heads, heads, D, B, max_q,
+                                                  bound), Q, stream)
+    st = lib().qkv_attention(Q.data_ptr(), row, head, code, T, q_heads, B, cu_p, kv_len.data_ptr(), table.data_ptr(),
+                             width, max_q, bound, D ** -0.5 if scale is None else float(scale), int(bool(causal)),
+                             window, s_p, ctypes.byref(c), out.data_ptr(), l_p, ws, wsb, _handle(stream, dev))
+    _check("qkv_attention", st)
+    return out if lse is None else (out, lse)
 
 
 def hbm_read_probe(buf, sink, groups, stream=None):

@@ -540,6 +540,97 @@ qmm_status qmm_validate_lora_grad(const void* dY, const void* X, int type, int64
                                   int g_type, const void* workspace, size_t workspace_bytes);
 
 /* ---------------------------------------------------------------------------
+ * A key/value cache in 4 or 8 bits, and attention over it.
+ *
+ * The cache is a pool of pages; a slot is page_id * page + place.  A key (or value) of one token
+ * and head is a row of D codes, unsigned `bits`-wide fields, least significant first; `group`
+ * consecutive dimensions share a fp16 scale s and offset o, and code c stands for c * s + o (not
+ * rounded).  Dimension d is the field at position (d % W) * (D / W) + d / W of its row, W = 4 for
+ * keys and 16 for values: the order in which the lanes of a matrix instruction take them.
+ *   k, v                uint8 [pages][heads][page][D * bits / 8], 16-byte aligned
+ *   k_params, v_params  fp16 [pages][heads][page][2][D / group] (scales, then offsets), 16-byte aligned
+ *   bits in {4, 8}, D in {64, 128, 256}, group in {32, 64, 128} and <= D, page a power of two in
+ *   [16, 65536], pages * page < 2^31, 1 <= heads <= 4096.
+ * The descriptor is a HOST struct; its pointers are device pointers.
+ *
+ * qkv_cache_store -- quantizes the keys and values of T tokens into their slots.
+ *   x = the value clamped to +-57344;  o = fp16(min of the group);  s = fp16(fp32(fp32(max - o) /
+ *   (2^bits - 1))), at least 0;  c = the integer nearest to (x - o) / s as a real number, halves to the
+ *   even one, clamped into the codes (0 when s is 0: a group whose steps would lie below 2^-25).
+ *   A group that holds a NaN or an infinity reads back as NaN.
+ *   K, V    [T][heads][D] of `type` (any of the three types), element (t, h, d) at
+ *           t * row_stride + h * head_stride + d (strides in elements, >= 0).  Rows that are 16-byte
+ *           aligned are the fastest.
+ *   slots   int32 [T] (device).  A slot outside the pool: the token is not stored.  Of several tokens
+ *           with one slot the last is stored.
+ *
+ * qkv_cache_load -- the values of T slots: K, V dense [T][heads][D] of `type`, fp32(c * s + o) rounded
+ *   to it; zeros for a slot outside the pool.  K or V may be NULL (not read).
+ *
+ * qkv_attention -- for query i of sequence b (n of them, the last n of its kv_len[b] tokens, so at
+ * position p = kv_len[b] - n + i) and head a, over the tokens t of the sequence that it sees:
+ *     S_t = scale * q . k_t;   out = sum_t e^(S_t) v_t / (sum_t e^(S_t) + e^(sinks[a]));
+ *     lse = log(sum_t e^(S_t) + e^(sinks[a]))
+ *   with head a reading cache head a / (q_heads / heads).  It sees t < kv_len[b] whose page is in the
+ *   pool, with t <= p when causal, and t > p - window when window > 0 (causal only).  A query that sees
+ *   nothing: out = 0, lse = the sink or -inf.  What hidden tokens hold, and what lies behind kv_len,
+ *   reaches no result.
+ *   Q       of `type` (QMM_F16 or QMM_BF16), element (row, a, d) at row * row_stride + a * head_stride
+ *           + d (elements); T rows.  out dense [T][q_heads][D] of `type`; lse fp32 [T][q_heads] or NULL.
+ *   cu_q    int32 [B + 1] (device): the queries of sequence b are the rows cu_q[b] .. cu_q[b + 1] - 1
+ *           (clamped into [0, T], the first max_q of them); rows of no sequence are not written.
+ *           NULL: row b is the one query of sequence b (T = B).
+ *   kv_len  int32 [B] (device), clamped into [0, table_width * page].
+ *   table   int32 [B][table_width] (device): pages of each sequence; one outside the pool is not seen.
+ *   max_q   the greatest number of queries of a sequence (1 when cu_q is NULL); sets the grid.
+ *   max_kv  the greatest kv_len expected: only how the work is split depends on it (0: the table's).
+ *   sinks   fp32 [q_heads] (device) or NULL (none).  window 0: none.
+ *   Codes enter the products as they are and scales are applied in fp32: S and lse carry fp32 sums'
+ *   errors; e^(S_t) s is rounded to fp16 (relative 2^-11, of its largest down to 2^-30) for the
+ *   second product.  Queries are scaled by a power of two per row to fp16: exact down to 2^-31 of the
+ *   row's largest element.  A query with a NaN or an infinity (or elements past 2^100) gives NaN.
+ *   B <= 65535, T <= 2^24, q_heads <= 4096 a multiple of heads with q_heads / heads <= 512.
+ *   workspace: at least qkv_attention_workspace_bytes, 256-byte aligned; calls that share one must not
+ *   overlap.  The sums' order depends on the sizes, max_q, max_kv and the lengths only.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+  uint8_t* k;
+  uint8_t* v;
+  uint16_t* k_params;
+  uint16_t* v_params;
+  int64_t pages;
+  int heads, page, D, bits, group;
+} qkv_cache;
+
+qmm_status qkv_cache_store(const void* K, int64_t k_row_stride, int64_t k_head_stride, const void* V,
+                           int64_t v_row_stride, int64_t v_head_stride, int type, int64_t T,
+                           const int32_t* slots, const qkv_cache* cache, void* stream);
+qmm_status qkv_cache_load(const qkv_cache* cache, const int32_t* slots, int64_t T, void* K, void* V, int type,
+                          void* stream);
+qmm_status qkv_attention(const void* Q, int64_t row_stride, int64_t head_stride, int type, int64_t T,
+                         int q_heads, int64_t B, const int32_t* cu_q, const int32_t* kv_len,
+                         const int32_t* table, int64_t table_width, int64_t max_q, int64_t max_kv,
+                         float scale, int causal, int64_t window, const float* sinks,
+                         const qkv_cache* cache, void* out, float* lse, void* workspace,
+                         size_t workspace_bytes, void* stream);
+size_t qkv_attention_workspace_bytes(int64_t T, int q_heads, int heads, int D, int64_t B, int64_t max_q,
+                                     int64_t max_kv);
+
+/* Host-only checks of the arguments, as qmm_validate_nbits. */
+qmm_status qmm_validate_kv_store(const void* K, int64_t k_row_stride, int64_t k_head_stride, const void* V,
+                                 int64_t v_row_stride, int64_t v_head_stride, int type, int64_t T,
+                                 const int32_t* slots, const qkv_cache* cache);
+qmm_status qmm_validate_kv_load(const qkv_cache* cache, const int32_t* slots, int64_t T, const void* K,
+                                const void* V, int type);
+qmm_status qmm_validate_kv_attention(const void* Q, int64_t row_stride, int64_t head_stride, int type,
+                                     int64_t T, int q_heads, int64_t B, const int32_t* cu_q,
+                                     const int32_t* kv_len, const int32_t* table, int64_t table_width,
+                                     int64_t max_q, int64_t max_kv, float scale, int causal,
+                                     int64_t window, const float* sinks, const qkv_cache* cache,
+                                     const void* out, const float* lse, const void* workspace,
+                                     size_t workspace_bytes);
+
+/* ---------------------------------------------------------------------------
  * Tuning control and introspection.
  * qmm_tuning_mode: 0 = time candidates on the first call of a shape (default),
  *   1 = never time, always use the default tiling, 2 = force candidate
