@@ -44,7 +44,8 @@ struct KvPlan {
   int64_t tiles; // row tiles per sequence and cache head
   int splits;    // parts of the tokens, joined by a second launch when more than one
 };
-KvPlan kv_plan(int q_heads, int heads, int D, int64_t B, int64_t max_q, int64_t max_kv);
+KvPlan kv_plan(int q_heads, int heads, int D, int64_t B, int64_t max_q, int64_t max_kv,
+               int64_t window);
 
 struct KvAttnArgs {
   const uint16_t* q;

@@ -93,8 +93,8 @@ qmm_status check_attention(const void* Q, int64_t rs, int64_t hs, int type, int6
   if (!std::isfinite(scale)) return QMM_E_PARAM;
   if (!cu_q && (T != B || max_q != 1)) return QMM_E_SHAPE;
   if (T == 0 || B == 0) return QMM_OK;
-  const KvPlan k = kv_plan(q_heads, c->heads, c->D, B, max_q, max_kv ? max_kv : width * c->page);
-  if (k.tiles * k.splits * c->heads > kMaxGroups / B || T * q_heads > (1LL << 26)) return QMM_E_SHAPE;
+  const KvPlan k = kv_plan(q_heads, c->heads, c->D, B, max_q, max_kv ? max_kv : width * c->page, window);
+  if (k.tiles * k.splits * c->heads > kMaxGroups / B || (k.splits > 1 && T * q_heads > kMaxGroups)) return QMM_E_SHAPE;
   if (!Q || !kv_len || (!table && width > 0) || !out) return QMM_E_NULL;
   if (!aligned(Q, 2) || !aligned(cu_q, 4) || !aligned(kv_len, 4) || !aligned(table, 4) || !aligned(sinks, 4) ||
       !aligned(out, 8) || !aligned(lse, 4))
@@ -185,9 +185,9 @@ qmm_status qkv_cache_load(const qkv_cache* cache, const int32_t* slots, int64_t 
 }
 
 size_t qkv_attention_workspace_bytes(int64_t T, int q_heads, int heads, int D, int64_t B, int64_t max_q,
-                                     int64_t max_kv) {
-  if (!valid_plan(T, q_heads, heads, B, max_q, max_kv) || T == 0 || B == 0) return 0;
-  return workspace_of(T, q_heads, D, kv_plan(q_heads, heads, D, B, max_q, max_kv));
+                                     int64_t max_kv, int64_t window) {
+  if (!valid_plan(T, q_heads, heads, B, max_q, max_kv) || T == 0 || B == 0 || window < 0) return 0;
+  return workspace_of(T, q_heads, D, kv_plan(q_heads, heads, D, B, max_q, max_kv, window));
 }
 
 qmm_status qkv_attention(const void* Q, int64_t row_stride, int64_t head_stride, int type, int64_t T, int q_heads,
@@ -223,7 +223,7 @@ qmm_status qkv_attention(const void* Q, int64_t row_stride, int64_t head_stride,
   p.page_log2 = log2_of(cache->page);
   p.out = (uint16_t*)out;
   p.lse = lse;
-  p.plan = kv_plan(q_heads, cache->heads, cache->D, B, max_q, max_kv ? max_kv : table_width * cache->page);
+  p.plan = kv_plan(q_heads, cache->heads, cache->D, B, max_q, max_kv ? max_kv : table_width * cache->page, window);
   if (p.plan.splits > 1) {
     const size_t n = (size_t)p.plan.splits * T * q_heads;
     p.part = (float*)workspace;

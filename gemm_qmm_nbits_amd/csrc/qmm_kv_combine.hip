@@ -1,4 +1,6 @@
 // Attention over the low-bit cache: the plan of a call and the join of its parts.
+#include <algorithm>
+
 #include "qmm_device.h"
 #include "qmm_internal.h"
 #include "qmm_kv.h"
@@ -8,15 +10,17 @@ namespace qmm {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kMaxParts = 128;  // two a lane
 
-// One output row (query, head) per D / 4 lanes, the parts in their order.  A part without visible tokens
-// has sum 0 and is skipped: its vector was not written.
+// A work-group per output row (query, head).  Every wave reads the parts' two numbers, two a lane, and
+// keeps their factors in its own piece of LDS; then kThreads / (D / 4) parts at a time are summed, 4
+// dimensions a lane, each thread's parts in order, and the threads' sums in order.  A part without visible
+// tokens has sum 0 and is skipped: its vector was not written.
 __global__ __launch_bounds__(kThreads) void kv_combine_kernel(KvAttnArgs p) {
-  const int per = p.c.D / 4;
-  const int64_t row = (int64_t)blockIdx.x * (kThreads / per) + threadIdx.x / per;
-  const int d = 4 * (threadIdx.x % per);
-  const int64_t n = p.T * p.q_heads;
-  if (row >= n) return;
+  __shared__ float factors[kThreads / 64][kMaxParts];
+  __shared__ f32x4 join[kThreads];
+  const int tid = threadIdx.x, lane = tid & 63, per = p.c.D / 4, lanes = kThreads / per;
+  const int64_t row = blockIdx.x, n = p.T * p.q_heads;
   if (p.cu_q) {  // rows of no sequence, and those past max_q, have no parts
     const int64_t t = row / p.q_heads;
     int64_t lo = 0, hi = p.B;  // the last sequence that begins at or before row t
@@ -30,23 +34,42 @@ __global__ __launch_bounds__(kThreads) void kv_combine_kernel(KvAttnArgs p) {
     if (t < q0 || t >= q1 || t - q0 >= p.max_q) return;
   }
   const int splits = p.plan.splits;
-  float ref = -INFINITY;
-  for (int s = 0; s < splits; ++s) {
-    const float* st = p.stats + 2 * (s * n + row);
-    if (st[1] != 0.0f) ref = fmaxf(ref, st[0]);
-  }
-  float total = 0.0f;
-  f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int s = 0; s < splits; ++s) {
-    const float* st = p.stats + 2 * (s * n + row);
-    const float l = st[1];
-    if (l == 0.0f) continue;
-    const float a = __builtin_amdgcn_exp2f(st[0] - ref);
-    total = fmaf(l, a, total);
-    const f32x4 v = *(const f32x4*)(p.part + (s * n + row) * p.c.D + d);
+  float* factor = factors[tid >> 6];
+  float rs[2], ls[2], ref = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = fmaf(v[i], a, o[i]);
+  for (int k = 0; k < 2; ++k) {
+    const int s = lane + 64 * k;
+    const float* st = p.stats + 2 * ((s < splits ? s : 0) * n + row);
+    rs[k] = st[0];
+    ls[k] = s < splits ? st[1] : 0.0f;
+    if (ls[k] != 0.0f) ref = fmaxf(ref, rs[k]);
   }
+#pragma unroll
+  for (int k = 1; k < 64; k <<= 1) ref = fmaxf(ref, __shfl_xor(ref, k, 64));
+  float total = 0.0f;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const float a = ls[k] != 0.0f ? __builtin_amdgcn_exp2f(rs[k] - ref) : 0.0f;
+    factor[lane + 64 * k] = a;
+    total = ls[k] != 0.0f ? fmaf(ls[k], a, total) : total;
+  }
+#pragma unroll
+  for (int k = 1; k < 64; k <<= 1) total += __shfl_xor(total, k, 64);
+  const int d = 4 * (tid % per);
+  f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+  for (int s = tid / per; s < splits; s += lanes) {
+    const float a = factor[s];
+    if (a != 0.0f) {
+      const f32x4 v = *(const f32x4*)(p.part + (s * n + row) * p.c.D + d);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[i] = fmaf(v[i], a, o[i]);
+    }
+  }
+  join[tid] = o;
+  __syncthreads();
+  if (tid >= per) return;
+  for (int k = 1; k < lanes; ++k) o += join[k * per + tid];
   const bool none = total == 0.0f;
   float lse = none ? -INFINITY : (ref + __builtin_amdgcn_logf(total)) * 0.69314718f;
   if (p.sinks) {
@@ -68,7 +91,7 @@ __global__ __launch_bounds__(kThreads) void kv_combine_kernel(KvAttnArgs p) {
 
 }  // namespace
 
-KvPlan kv_plan(int q_heads, int heads, int D, int64_t B, int64_t max_q, int64_t max_kv) {
+KvPlan kv_plan(int q_heads, int heads, int D, int64_t B, int64_t max_q, int64_t max_kv, int64_t window) {
   KvPlan k{};
   const int64_t rows = max_q * (q_heads / heads);
   const int most = D == 256 ? 2 : 4;
@@ -77,17 +100,17 @@ KvPlan kv_plan(int q_heads, int heads, int D, int64_t B, int64_t max_q, int64_t 
   const int64_t per = k.by_rows ? 64 * most : 16 * k.mt;
   k.tiles = (rows + per - 1) / per;
   const int64_t groups = k.tiles * heads * B;
-  int64_t splits = groups >= 768 ? 1 : (768 + groups - 1) / groups;
-  const int64_t parts = (max_kv + 255) / 256;
-  if (splits > parts) splits = parts;
-  if (splits > 128) splits = 128;
+  // tokens that a row tile sees at most
+  if (window > 0 && window < max_kv) max_kv = std::min(max_kv, window + std::min(max_q, (per - 1) / (q_heads / heads) + 2));
+  auto over = [](int64_t n, int64_t d) { return (n + d - 1) / d; };
+  int64_t splits = std::max(std::min(over(512, groups), over(max_kv, 256)), std::min(over(3072, groups), over(max_kv, 2048)));
+  if (splits > kMaxParts) splits = kMaxParts;
   k.splits = splits < 1 ? 1 : (int)splits;
   return k;
 }
 
 hipError_t launch_kv_combine(const KvAttnArgs& p, hipStream_t st) {
-  const int64_t per = kThreads / (p.c.D / 4);
-  launch(kv_combine_kernel, dim3((unsigned)((p.T * p.q_heads + per - 1) / per)), dim3(kThreads), 0, st, p);
+  launch(kv_combine_kernel, dim3((unsigned)(p.T * p.q_heads)), dim3(kThreads), 0, st, p);
   return hipGetLastError();
 }
 

@@ -151,7 +151,7 @@ _SIGS = {
     "qkv_attention": (c_int, [c_void_p, c_int64, c_int64, c_int, c_int64, c_int, c_int64, c_void_p, c_void_p, c_void_p,
                               c_int64, c_int64, c_int64, c_float, c_int, c_int64, c_void_p, POINTER(qkv_cache),
                               c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
-    "qkv_attention_workspace_bytes": (c_size_t, [c_int64, c_int, c_int, c_int, c_int64, c_int64, c_int64]),
+    "qkv_attention_workspace_bytes": (c_size_t, [c_int64, c_int, c_int, c_int, c_int64, c_int64, c_int64, c_int64]),
     "qmm_validate_kv_store": (c_int, [c_void_p, c_int64, c_int64, c_void_p, c_int64, c_int64, c_int, c_int64, c_void_p,
                                       POINTER(qkv_cache)]),
     "qmm_validate_kv_load": (c_int, [POINTER(qkv_cache), c_void_p, c_int64, c_void_p, c_void_p, c_int]),
@@ -980,7 +980,7 @@ def qkv_attention(Q, cache, table, kv_len, cu_q=None, max_q=None, max_kv=None, s
         lse = _new((T, q_heads), ty.torch.float32, Q, stream)
     l_p, _ = _optional(lse, "lse", (T, q_heads), ty.f32, dev)
     keep, ws, wsb = _scratch(workspace, _bytes_of("qkv_attention_workspace_bytes", T, q_heads, heads, D, B, max_q,
-                                                  bound), Q, stream)
+                                                  bound, window), Q, stream)
     st = lib().qkv_attention(Q.data_ptr(), row, head, code, T, q_heads, B, cu_p, kv_len.data_ptr(), table.data_ptr(),
                              width, max_q, bound, D ** -0.5 if scale is None else float(scale), int(bool(causal)),
                              window, s_p, ctypes.byref(c), out.data_ptr(), l_p, ws, wsb, _handle(stream, dev))

@@ -614,7 +614,7 @@ qmm_status qkv_attention(const void* Q, int64_t row_stride, int64_t head_stride,
                          const qkv_cache* cache, void* out, float* lse, void* workspace,
                          size_t workspace_bytes, void* stream);
 size_t qkv_attention_workspace_bytes(int64_t T, int q_heads, int heads, int D, int64_t B, int64_t max_q,
-                                     int64_t max_kv);
+                                     int64_t max_kv, int64_t window);
 
 /* Host-only checks of the arguments, as qmm_validate_nbits. */
 qmm_status qmm_validate_kv_store(const void* K, int64_t k_row_stride, int64_t k_head_stride, const void* V,

@@ -360,7 +360,7 @@ def test_repeats_streams_and_graph():
     slots = t.zeros(3, dtype=t.int32, device="cuda")
     out = t.empty(3, 8, 128, dtype=t.bfloat16, device="cuda")
     lse = t.empty(3, 8, device="cuda")
-    ws = t.empty(Q.lib().qkv_attention_workspace_bytes(3, 8, 2, 128, 3, 1, 512), dtype=t.uint8, device="cuda")
+    ws = t.empty(Q.lib().qkv_attention_workspace_bytes(3, 8, 2, 128, 3, 1, 512, 0), dtype=t.uint8, device="cuda")
     assert ws.numel() > 0
 
     def place():

@@ -105,7 +105,7 @@ def test_attention_refusals():
 
 
 def test_attention_workspace():
-    need = Q.lib().qkv_attention_workspace_bytes(5, 32, 8, 128, 5, 1, 30000)
+    need = Q.lib().qkv_attention_workspace_bytes(5, 32, 8, 128, 5, 1, 30000, 0)
     assert need > 0
     assert attn(max_kv=30000) == -7 and attn(max_kv=30000, ws=FAKE, wsb=need - 1) == -7
     assert attn(max_kv=30000, ws=FAKE, wsb=need) == 0
@@ -116,6 +116,15 @@ def test_attention_workspace():
     rows = 5 * 32
     assert any(need == -(-s * rows * 128 * 4 // 256) * 256 + s * rows * 8 for s in range(2, 200))
     # one part: nothing to join
-    assert Q.lib().qkv_attention_workspace_bytes(5, 32, 8, 128, 5, 1, 100) == 0
-    assert Q.lib().qkv_attention_workspace_bytes(0, 32, 8, 128, 0, 1, 30000) == 0
-    assert Q.lib().qkv_attention_workspace_bytes(5, 33, 8, 128, 5, 1, 30000) == 0
+    assert Q.lib().qkv_attention_workspace_bytes(5, 32, 8, 128, 5, 1, 100, 0) == 0
+    assert Q.lib().qkv_attention_workspace_bytes(0, 32, 8, 128, 0, 1, 30000, 0) == 0
+    assert Q.lib().qkv_attention_workspace_bytes(5, 33, 8, 128, 5, 1, 30000, 0) == 0
+
+
+def test_a_window_needs_no_more_parts_than_its_tokens():
+    q = Q.lib().qkv_attention_workspace_bytes
+    assert q(5, 32, 8, 128, 5, 1, 30000, 128) == 0
+    assert q(5, 32, 8, 128, 5, 1, 30000, 29000) <= q(5, 32, 8, 128, 5, 1, 30000, 0)
+    assert q(5, 32, 8, 128, 5, 1, 30000, 1 << 40) == q(5, 32, 8, 128, 5, 1, 30000, 0)
+    assert q(5, 32, 8, 128, 5, 1, 30000, -1) == 0
+    assert attn(max_kv=30000, window=128) == 0 and attn(max_kv=30000, window=29000) == -7
