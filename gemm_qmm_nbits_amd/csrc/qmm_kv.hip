@@ -5,6 +5,8 @@
 // codes in the cache (every 4th dimension for keys, every 16th for values) is reached by exchanging index
 // bits between the field number inside a lane's word and the lane number, a few lane exchanges of packed
 // words instead of one byte store per element.
+#include <algorithm>
+
 #include "qmm_device.h"
 #include "qmm_internal.h"
 #include "qmm_kv.h"
@@ -15,6 +17,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kBitmapWords = 64;
+constexpr int kAhead = 16;  // slots that a lane reads at once
 
 // A lane's 8 codes: 32 or 64 bits.
 template <int BITS>
@@ -116,69 +119,170 @@ __device__ __forceinline__ int word_of(int a) {
   else return ((a & 1) << 2) | (a >> 1);                                                  // (a0 e2 e1)
 }
 
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+// A lane's 8 elements as they lie in memory, and as fp32.
 template <int T>
-__device__ __forceinline__ void load8(const void* base, int64_t i, int vec, float* x) {
-  if constexpr (T == QMM_F32) {
-    const float* p = (const float*)base + i;
+struct Raw {
+  u32x4 v[T == QMM_F32 ? 2 : 1];
+  __device__ __forceinline__ void load(const void* base, int64_t i, int vec) {
+    constexpr int N = T == QMM_F32 ? 2 : 1;
+    const uint8_t* p = (const uint8_t*)base + i * (T == QMM_F32 ? 4 : 2);
     if (vec) {
-      const f32x4 u = *(const f32x4*)p, v = *(const f32x4*)(p + 4);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x[e] = u[e], x[4 + e] = v[e];
+      for (int k = 0; k < N; ++k) v[k] = *(const u32x4*)(p + 16 * k);
+    } else if constexpr (T == QMM_F32) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e / 4][e % 4] = ((const uint32_t*)p)[e];
     } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = p[e];
+      for (int e = 0; e < 4; ++e)
+        v[0][e] = (uint32_t)((const uint16_t*)p)[2 * e] | (uint32_t)((const uint16_t*)p)[2 * e + 1] << 16;
     }
-  } else {
-    const uint16_t* p = (const uint16_t*)base + i;
-    uint16_t h[8];
-    if (vec) {
-      *(uint4*)h = *(const uint4*)p;
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) h[e] = p[e];
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = T == QMM_F16 ? f16_to_f32(h[e]) : bf16_to_f32(h[e]);
   }
+  __device__ __forceinline__ float at(int e) const {
+    if constexpr (T == QMM_F32) return __uint_as_float(v[e / 4][e % 4]);
+    const uint16_t h = (uint16_t)(v[0][e / 2] >> (16 * (e & 1)));
+    return T == QMM_F16 ? f16_to_f32(h) : bf16_to_f32(h);
+  }
+};
+
+// The nearest integer to (x - o) / s of the real numbers, halves to the even one, where y, the quotient in
+// fp32, lies next to a half (n = rint(y)): x against o + s (n +- 1/2), which fp64 holds exactly (o and s are
+// multiples of 2^-24, the sum is below 2^18).
+__device__ __forceinline__ float code_next_to_half(float x, float o, float s, float y, float n) {
+  const float lo = y - n > 0.0f ? n : n - 1.0f;
+  const double half = (double)o + (double)s * ((double)lo + 0.5);
+  const double d = (double)x;
+  return d > half ? lo + 1.0f : d < half ? lo : 2.0f * rintf(0.5f * lo) == lo ? lo : lo + 1.0f;
 }
 
-// The nearest integer to (x - o) / s of the real numbers, halves to the even one, unless it lies outside
-// the codes.  y, the quotient in fp32, is off by less than 2^8 * 3 * 2^-24 (three roundings), so only
-// quotients within 2^-13 of a half are decided anew: x against o + s (n + 1/2), which fp64 holds exactly
-// (o and s are multiples of 2^-24, the sum is below 2^18).  y's part past a half is exact.
-__device__ __forceinline__ float code_of(float x, float o, float s, float inv) {
-  const float y = __fmul_rn(__fsub_rn(x, o), inv);
-  float n = rintf(y);
-  const float f = y - n;
-  if (__builtin_expect(fabsf(f) > 0.5f - 0x1p-13f, 0)) {
-    const float lo = f > 0.0f ? n : n - 1.0f;
-    const double half = (double)o + (double)s * ((double)lo + 0.5);
-    const double d = (double)x;
-    n = d > half ? lo + 1.0f : d < half ? lo : 2.0f * rintf(0.5f * lo) == lo ? lo : lo + 1.0f;
-  }
-  return n;
+// Minimum (or maximum) over the lanes of a group of 4, 8 or 16.
+template <bool MAX>
+__device__ __forceinline__ float group_extreme(float v, int lanes) {
+  auto with = [&](float u) { v = MAX ? fmaxf(v, u) : fminf(v, u); };
+  with(dpp_f<kDppXor1>(v));
+  with(dpp_f<kDppXor2>(v));
+  if (lanes > 4) with(dpp_f<kDppHalfMirror>(v));
+  if (lanes > 8) with(dpp_f<kDppMirror>(v));
+  return v;
 }
 
-template <int BITS, int D, int T>
-__global__ __launch_bounds__(kThreads) void kv_store_kernel(KvStoreArgs p) {
+// Quantizes a lane's 8 elements of a row and writes its word and its group's parameters (at < 0: takes part
+// in the exchanges only).
+template <int BITS, int D, int T, bool KEY>
+__device__ __forceinline__ void quantize8(const Raw<T>& raw, const qkv_cache& c, int64_t row, int lane) {
   typedef typename Word<BITS>::type W;
-  constexpr int LR = D / 8;              // lanes of a row
-  constexpr int RP = kThreads / LR;      // rows at a time
   constexpr float kTop = (float)((1 << BITS) - 1);
+  const int a = lane % (D / 8), G = D / c.group, lg = c.group / 8;  // lanes of a group
+  float x[8], finite = 0.0f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    x[e] = raw.at(e);
+    finite = fmaf(x[e], 0.0f, finite);  // NaN once an element is not finite
+  }
+  float lo = x[0], hi = x[0];
+#pragma unroll
+  for (int e = 1; e < 8; ++e) {
+    lo = fminf(lo, x[e]);
+    hi = fmaxf(hi, x[e]);
+  }
+  lo = group_extreme<false>(lo, lg);
+  hi = group_extreme<true>(hi, lg);
+  const float bad = group_extreme<true>(finite == 0.0f ? 0.0f : 1.0f, lg);
+  if (__builtin_expect(__builtin_amdgcn_ballot_w64(fmaxf(-lo, hi) > kKvLimit) != 0, 0)) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = fminf(fmaxf(x[e], -kKvLimit), kKvLimit);
+    lo = fminf(fmaxf(lo, -kKvLimit), kKvLimit);
+    hi = fminf(fmaxf(hi, -kKvLimit), kKvLimit);
+  }
+  uint16_t ob = f32_to_f16(lo);
+  const float o = f16_to_f32(ob);
+  uint16_t sb = f32_to_f16(materialize(__fdiv_rn(fmaxf(__fsub_rn(hi, o), 0.0f), kTop)));
+  float s = f16_to_f32(sb);
+  if (bad != 0.0f) {
+    ob = 0x7e00;
+    sb = 0;
+    s = 0.0f;
+  }
+  // The quotient in fp32, y, is off by less than 2^BITS * 4 * 2^-24 (two roundings and the reciprocal's,
+  // of one unit in the last place): where it lies within twice that of a half (y's distance from an integer
+  // is exact) the codes are decided anew.
+  constexpr float kNear = 0.5f - (BITS == 8 ? 0x1p-13f : 0x1p-17f);
+  const bool some = s > 0.0f;
+  const float inv = some ? __builtin_amdgcn_rcpf(s) : 0.0f;
+  float n[8], from = 0.0f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float y = __fmul_rn(__fsub_rn(x[e], o), inv);
+    n[e] = rintf(y);
+    from = fmaxf(from, fabsf(y - n[e]));
+  }
+  if (__builtin_amdgcn_ballot_w64(some && from > kNear) != 0) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float y = __fmul_rn(__fsub_rn(x[e], o), inv);
+      if (some && fabsf(y - n[e]) > kNear) n[e] = code_next_to_half(x[e], o, s, y, n[e]);
+    }
+  }
+  W w = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float c = some ? fminf(fmaxf(n[e], 0.0f), kTop) : 0.0f;
+    w |= (W)(uint32_t)c << (BITS * e);
+  }
+  w = to_order<BITS, D, KEY>(w, lane);
+  if (row < 0) return;
+  ((W*)((KEY ? c.k : c.v) + row * (D * BITS / 8)))[word_of<D, KEY>(a)] = w;
+  if (a % lg == 0) {
+    uint16_t* q = (KEY ? c.k_params : c.v_params) + row * (2 * G) + a / lg;
+    q[0] = sb;
+    q[G] = ob;
+  }
+}
+
+// A work-group stores p.tokens tokens (all heads), kItems rows per lane group at a time.  Of tokens with one
+// slot the last is stored: a token that a later one repeats is dropped.  The later slots are looked up in a
+// bitmap of the work-group's own (their low 11 bits) first, while the first rows are on their way.
+template <int BITS, int D, int T, int kItems>
+__global__ __launch_bounds__(kThreads) void kv_store_kernel(KvStoreArgs p) {
+  constexpr int RP = kThreads / (D / 8);  // rows at a time
   __shared__ int32_t slot_of[64];
   __shared__ uint32_t bitmap[kBitmapWords];
-  const int tid = threadIdx.x, a = tid % LR;
+  const int tid = threadIdx.x, a = tid % (D / 8);
   const int64_t t0 = (int64_t)blockIdx.x * p.tokens;
   const int nt = (int)min((int64_t)p.tokens, p.T - t0);
-  const int64_t nslots = p.c.pages * p.c.page;
+  const uint32_t nslots = (uint32_t)(p.c.pages * p.c.page);
+  const int H = p.c.heads, items = nt * H;
 
-  // Of tokens with one slot the last is stored: a token of this work-group that a later one repeats is
-  // dropped.  The later slots are looked up in a bitmap of the own ones (their low 11 bits) first.
+  Raw<T> raw[kItems][2];
+  int token[kItems], head[kItems];
+  auto fetch = [&](int it0) {
+#pragma unroll
+    for (int k = 0; k < kItems; ++k) {
+      const int it = it0 + k * RP + tid / (D / 8);
+      token[k] = it < items ? it / H : -1;
+      head[k] = it - token[k] * H;
+      if (it < items)
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv)
+          raw[k][kv].load(p.x[kv], (t0 + token[k]) * p.row_stride[kv] + head[k] * p.head_stride[kv] + 8 * a, p.vec);
+    }
+  };
+  // slots first: loads return in order, and the rows take longer
+  int32_t later[kAhead];
+  auto read_later = [&](int64_t t) {
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) later[k] = t + k * kThreads < p.T ? p.slots[t + k * kThreads] : -1;
+  };
+  const int32_t own = tid < nt ? p.slots[t0 + tid] : -1;
+  read_later(t0 + 1 + tid);
+#pragma unroll
+  for (int k = 0; k < kItems; ++k) raw[k][0] = raw[k][1] = Raw<T>{};
+  fetch(0);
+
   if (tid < kBitmapWords) bitmap[tid] = 0;
-  if (tid < nt) {
-    const int32_t s = p.slots[t0 + tid];
-    slot_of[tid] = (uint32_t)s < (uint64_t)nslots ? s : -1;
-  }
+  if (tid < nt) slot_of[tid] = (uint32_t)own < nslots ? own : -1;
   __syncthreads();
   if (tid < nt && slot_of[tid] >= 0) {
     const uint32_t s = slot_of[tid];
@@ -186,11 +290,13 @@ __global__ __launch_bounds__(kThreads) void kv_store_kernel(KvStoreArgs p) {
   }
   __syncthreads();
   uint64_t lost = 0;  // of this thread's finds: bit i = token i is repeated
-  for (int64_t t = t0 + 1 + tid; t < p.T; t += kThreads) {
-    const int32_t s = p.slots[t];
-    if (s >= 0 && ((bitmap[((uint32_t)s >> 5) & (kBitmapWords - 1)] >> (s & 31)) & 1))
-      for (int i = 0; i < nt && t0 + i < t; ++i)
-        if (slot_of[i] == s) lost |= 1ull << i;
+  for (int64_t t = t0 + 1 + tid; t < p.T; t += kAhead * kThreads) {
+    if (t > t0 + kThreads) read_later(t);
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+      if (later[k] >= 0 && ((bitmap[((uint32_t)later[k] >> 5) & (kBitmapWords - 1)] >> (later[k] & 31)) & 1))
+        for (int i = 0; i < nt && t0 + i < t + k * kThreads; ++i)
+          if (slot_of[i] == later[k]) lost |= 1ull << i;
   }
   __syncthreads();  // every lookup is done before a slot is struck out
   while (lost) {
@@ -200,140 +306,107 @@ __global__ __launch_bounds__(kThreads) void kv_store_kernel(KvStoreArgs p) {
   }
   __syncthreads();
 
-  const int H = p.c.heads, G = D / p.c.group, lg = p.c.group / 8;  // lanes of a group
-  const int items = nt * H;
-  for (int it0 = 0; it0 < items; it0 += RP) {
-    const int it = it0 + tid / LR;
-    const int i = it / H, h = it - i * H;
-    const int32_t slot = it < items ? slot_of[i] : -1;
-    const int64_t page = slot < 0 ? 0 : slot / p.c.page;
-    const int64_t row = (page * H + h) * p.c.page + (slot < 0 ? 0 : slot % p.c.page);
-    float x[2][8];
+  const int page_log2 = __builtin_ctz(p.c.page);
+  for (int it0 = 0; it0 < items; it0 += kItems * RP) {
+    if (it0 > 0) fetch(it0);
 #pragma unroll
-    for (int kv = 0; kv < 2; ++kv) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[kv][e] = 0.0f;
-      if (slot >= 0)
-        load8<T>(p.x[kv], (t0 + i) * p.row_stride[kv] + h * p.head_stride[kv] + 8 * a, p.vec, x[kv]);
-    }
-#pragma unroll
-    for (int kv = 0; kv < 2; ++kv) {
-      float lo = kKvLimit, hi = -kKvLimit, bad = 0.0f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        if (!(fabsf(x[kv][e]) < INFINITY)) bad = 1.0f;
-        x[kv][e] = fminf(fmaxf(x[kv][e], -kKvLimit), kKvLimit);
-        lo = fminf(lo, x[kv][e]);
-        hi = fmaxf(hi, x[kv][e]);
-      }
-      for (int m = 1; m < lg; m <<= 1) {
-        lo = fminf(lo, __shfl_xor(lo, m, 64));
-        hi = fmaxf(hi, __shfl_xor(hi, m, 64));
-        bad = fmaxf(bad, __shfl_xor(bad, m, 64));
-      }
-      uint16_t ob = f32_to_f16(lo);
-      const float o = f16_to_f32(ob);
-      uint16_t sb = f32_to_f16(materialize(__fdiv_rn(fmaxf(__fsub_rn(hi, o), 0.0f), kTop)));
-      float s = f16_to_f32(sb);
-      if (bad != 0.0f) {
-        ob = 0x7e00;
-        sb = 0;
-        s = 0.0f;
-      }
-      const float inv = s > 0.0f ? __fdiv_rn(1.0f, s) : 0.0f;
-      W w = 0;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        float n = 0.0f;
-        if (s > 0.0f) n = fminf(fmaxf(code_of(x[kv][e], o, s, inv), 0.0f), kTop);
-        w |= (W)(uint32_t)n << (BITS * e);
-      }
-      // (every lane takes part in the exchanges)
-      w = kv == 0 ? to_order<BITS, D, true>(w, tid) : to_order<BITS, D, false>(w, tid);
-      if (slot >= 0) {
-        const int n = kv == 0 ? word_of<D, true>(a) : word_of<D, false>(a);
-        ((W*)((kv == 0 ? p.c.k : p.c.v) + row * (D * BITS / 8)))[n] = w;
-        if (a % lg == 0) {
-          uint16_t* q = (kv == 0 ? p.c.k_params : p.c.v_params) + row * (2 * G) + a / lg;
-          q[0] = sb;
-          q[G] = ob;
-        }
-      }
+    for (int k = 0; k < kItems; ++k) {
+      const int32_t slot = token[k] < 0 ? -1 : slot_of[token[k]];
+      const int64_t row = slot < 0 ? -1
+                                   : (((int64_t)(slot >> page_log2) * H + head[k]) << page_log2) + (slot & (p.c.page - 1));
+      quantize8<BITS, D, T, true>(raw[k][0], p.c, row, tid);
+      quantize8<BITS, D, T, false>(raw[k][1], p.c, row, tid);
     }
   }
 }
+
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 template <int T>
 __device__ __forceinline__ void store8(void* base, int64_t i, int vec, const float* x) {
-  if constexpr (T == QMM_F32) {
-    float* q = (float*)base + i;
-    if (vec) {
-      *(f32x4*)q = f32x4{x[0], x[1], x[2], x[3]};
-      *(f32x4*)(q + 4) = f32x4{x[4], x[5], x[6], x[7]};
-    } else {
+  constexpr int N = T == QMM_F32 ? 2 : 1;
+  u32x4 v[N];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) q[e] = x[e];
+  for (int e = 0; e < 8; ++e) {
+    if constexpr (T == QMM_F32) v[e / 4][e % 4] = __float_as_uint(x[e]);
+    else if (e % 2 == 0) {
+      const f32x2 y = {materialize(x[e]), materialize(x[e + 1])};
+      v[0][e / 2] = T == QMM_F16 ? __builtin_bit_cast(uint32_t, __builtin_convertvector(y, f16x2))
+                                 : __builtin_bit_cast(uint32_t, __builtin_convertvector(y, bf16x2));
     }
+  }
+  uint8_t* q = (uint8_t*)base + i * (T == QMM_F32 ? 4 : 2);
+  if (vec) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) *(u32x4*)(q + 16 * k) = v[k];
   } else {
-    uint16_t* q = (uint16_t*)base + i;
-    uint16_t r[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) r[e] = T == QMM_F16 ? f32_to_f16(materialize(x[e])) : f32_to_bf16(x[e]);
-    if (vec) {
-      *(uint4*)q = *(const uint4*)r;
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) q[e] = r[e];
+    for (int e = 0; e < 8; ++e) {
+      if constexpr (T == QMM_F32) ((uint32_t*)q)[e] = v[e / 4][e % 4];
+      else ((uint16_t*)q)[e] = (uint16_t)(v[0][e / 2] >> (16 * (e & 1)));
     }
   }
 }
 
-template <int BITS, int D, int T>
+// One head of N rows of tokens per lane group and work-group: neighbouring tokens' rows of one head are
+// neighbours in the cache.
+template <int BITS, int D, int T, int N>
 __global__ __launch_bounds__(kThreads) void kv_load_kernel(KvLoadArgs p) {
   typedef typename Word<BITS>::type W;
   constexpr int LR = D / 8, RP = kThreads / LR;
-  const int tid = threadIdx.x, a = tid % LR;
+  const int tid = threadIdx.x, a = tid % LR, h = blockIdx.x % p.c.heads;
   const int H = p.c.heads, G = D / p.c.group, lg = p.c.group / 8;
-  const int64_t it = (int64_t)blockIdx.x * RP + tid / LR;
-  const int64_t t = it / H;
-  const int h = (int)(it - t * H);
-  const bool in = t < p.T;
-  const int32_t slot = in ? p.slots[t] : -1;
-  const bool has = (uint32_t)slot < (uint64_t)(p.c.pages * p.c.page);
-  const int64_t page = has ? slot / p.c.page : 0;
-  const int64_t row = (page * H + h) * p.c.page + (has ? slot % p.c.page : 0);
-  W w[2];
-  float s[2], o[2];
+  const int64_t t0 = (int64_t)(blockIdx.x / p.c.heads) * (RP * N) + tid / LR;
+  const uint32_t nslots = (uint32_t)(p.c.pages * p.c.page);
+  const int page_log2 = __builtin_ctz(p.c.page);
+  int32_t slot[N];
 #pragma unroll
-  for (int kv = 0; kv < 2; ++kv) {
-    w[kv] = 0;
-    s[kv] = o[kv] = 0.0f;
-    if (has && p.y[kv]) {
-      const int n = kv == 0 ? word_of<D, true>(a) : word_of<D, false>(a);
-      w[kv] = ((const W*)((kv == 0 ? p.c.k : p.c.v) + row * (D * BITS / 8)))[n];
-      const uint16_t* q = (kv == 0 ? p.c.k_params : p.c.v_params) + row * (2 * G) + a / lg;
-      s[kv] = f16_to_f32(q[0]);
-      o[kv] = f16_to_f32(q[G]);
+  for (int k = 0; k < N; ++k) slot[k] = t0 + k * RP < p.T ? p.slots[t0 + k * RP] : -1;
+  W w[N][2];
+  uint16_t s[N][2], o[N][2];
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    const bool has = (uint32_t)slot[k] < nslots;
+    const int32_t at = has ? slot[k] : 0;
+    const int64_t row = (((int64_t)(at >> page_log2) * H + h) << page_log2) + (at & (p.c.page - 1));
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv) {
+      w[k][kv] = 0;
+      s[k][kv] = o[k][kv] = 0;
+      if (has && p.y[kv]) {
+        const int n = kv == 0 ? word_of<D, true>(a) : word_of<D, false>(a);
+        w[k][kv] = ((const W*)((kv == 0 ? p.c.k : p.c.v) + row * (D * BITS / 8)))[n];
+        const uint16_t* q = (kv == 0 ? p.c.k_params : p.c.v_params) + row * (2 * G) + a / lg;
+        s[k][kv] = q[0];
+        o[k][kv] = q[G];
+      }
     }
   }
 #pragma unroll
-  for (int kv = 0; kv < 2; ++kv) {
-    const W u = kv == 0 ? from_order<BITS, D, true>(w[kv], tid) : from_order<BITS, D, false>(w[kv], tid);
-    float x[8];
+  for (int k = 0; k < N; ++k)
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      x[e] = fmaf((float)(uint32_t)((u >> (BITS * e)) & ((1u << BITS) - 1)), s[kv], o[kv]);
-    if (in && p.y[kv]) store8<T>(p.y[kv], (t * H + h) * D + 8 * a, p.vec, x);
-  }
+    for (int kv = 0; kv < 2; ++kv) {
+      const W u = kv == 0 ? from_order<BITS, D, true>(w[k][kv], tid) : from_order<BITS, D, false>(w[k][kv], tid);
+      const float sf = f16_to_f32(s[k][kv]), of = f16_to_f32(o[k][kv]);
+      float x[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = fmaf((float)(uint32_t)((u >> (BITS * e)) & ((1u << BITS) - 1)), sf, of);
+      const int64_t t = t0 + k * RP;
+      if (t < p.T && p.y[kv]) store8<T>(p.y[kv], (t * H + h) * D + 8 * a, p.vec, x);
+    }
 }
 
 template <int BITS, int D, int T, bool STORE, typename Args>
 hipError_t go(const Args& p, hipStream_t st) {
   if constexpr (STORE) {
-    launch(kv_store_kernel<BITS, D, T>, dim3((unsigned)((p.T + p.tokens - 1) / p.tokens)), dim3(kThreads), 0, st, p);
+    const dim3 groups((unsigned)((p.T + p.tokens - 1) / p.tokens));
+    if (p.tokens * p.c.heads <= kThreads / (D / 8)) launch(kv_store_kernel<BITS, D, T, 1>, groups, dim3(kThreads), 0, st, p);
+    else launch(kv_store_kernel<BITS, D, T, 2>, groups, dim3(kThreads), 0, st, p);
   } else {
     constexpr int RP = kThreads / (D / 8);
-    launch(kv_load_kernel<BITS, D, T>, dim3((unsigned)((p.T * p.c.heads + RP - 1) / RP)), dim3(kThreads), 0, st, p);
+    auto groups = [&](int n) { return dim3((unsigned)((p.T + n * RP - 1) / (n * RP) * p.c.heads)); };
+    if (p.T * p.c.heads >= 1024 * RP * 4) launch(kv_load_kernel<BITS, D, T, 4>, groups(4), dim3(kThreads), 0, st, p);
+    else launch(kv_load_kernel<BITS, D, T, 1>, groups(1), dim3(kThreads), 0, st, p);
   }
   return hipGetLastError();
 }
@@ -360,10 +433,12 @@ hipError_t by_size(const Args& p, hipStream_t st) {
 }  // namespace
 
 hipError_t launch_kv_store(KvStoreArgs p, hipStream_t st) {
-  // tokens per work-group: one for small batches (latency), more for long ones (every work-group
-  // reads all later slots)
-  p.tokens = 1;
-  while (p.tokens < 64 && p.T > 512ll * p.tokens) p.tokens *= 2;
+  // tokens per work-group: about two rounds of rows, so that small batches fill the chip; more for long
+  // batches, whose work-groups each read all later slots (16384 tokens and more: 1024 work-groups)
+  const int rows = 2 * kThreads / (p.c.D / 8);
+  int64_t n = std::max<int64_t>(rows / p.c.heads, (p.T + 1023) / 1024);
+  while (n > 1 && (p.T + n - 1) / n < 256) n = (n + 1) / 2;
+  p.tokens = (int)std::min<int64_t>(std::max<int64_t>(n, 1), 64);
   return by_size<true>(p, st);
 }
 
