@@ -37,6 +37,9 @@ struct KvLoadArgs {
 };
 hipError_t launch_kv_load(KvLoadArgs p, hipStream_t st);
 
+// Row tiles per wave of the kernel for many rows.
+constexpr int kPromptTiles = 2;
+
 // How an attention call is laid out: a function of the sizes only.
 struct KvPlan {
   int mt;        // tiles of 16 rows per wave (a row = one query of one head of a cache head)

@@ -97,13 +97,15 @@ KvPlan kv_plan(int q_heads, int heads, int D, int64_t B, int64_t max_q, int64_t 
   const int most = D == 256 ? 2 : 4;
   k.mt = rows <= 16 ? 1 : rows <= 32 || most == 2 ? 2 : 4;
   k.by_rows = rows > 16 * most;
-  const int64_t per = k.by_rows ? 64 * most : 16 * k.mt;
+  const int64_t per = k.by_rows ? 64 * kPromptTiles : 16 * k.mt;
   k.tiles = (rows + per - 1) / per;
   const int64_t groups = k.tiles * heads * B;
   // tokens that a row tile sees at most
   if (window > 0 && window < max_kv) max_kv = std::min(max_kv, window + std::min(max_q, (per - 1) / (q_heads / heads) + 2));
   auto over = [](int64_t n, int64_t d) { return (n + d - 1) / d; };
-  int64_t splits = std::max(std::min(over(512, groups), over(max_kv, 256)), std::min(over(3072, groups), over(max_kv, 2048)));
+  int64_t splits = k.by_rows ? std::min(groups < 256 ? over(256, groups) : 1, over(max_kv, 512))
+                             : std::max(std::min(over(512, groups), over(max_kv, 256)),
+                                        std::min(over(3072, groups), over(max_kv, 2048)));
   if (splits > kMaxParts) splits = kMaxParts;
   k.splits = splits < 1 ? 1 : (int)splits;
   return k;

@@ -1,0 +1,165 @@
+// Attention over the low-bit cache for many rows: the waves of a work-group take rows of their own and walk
+// the tokens together.
+//
+// Masking the codes out of their words costs as many vector instructions as all else for one row tile, so
+// the work-group does it once per tile of 32 tokens: each wave makes a quarter of the operands of both
+// products, in their register layout, and leaves them in LDS, where reading one is a conflict-free 16 bytes
+// per lane.  Two buffers: while the waves work on one tile the words of the next are on their way to
+// registers, and are written to the other buffer at the end; one barrier per tile.
+#pragma once
+
+#include "qmm_kv_rows.h"
+
+namespace qmm {
+namespace kv {
+
+// What a thread makes of a tile.  Keys: wave w the chunks (w & 1) NC / 2 .. of half w >> 1, whose codes are
+// neighbours in a lane's part of a row.  Values: the lane whose operand elements belong to token quarter
+// j = w and dimension x, NV / 4 of the row tiles n (by lane >> 4).
+template <int BITS, int D, int G>
+struct Share {
+  static constexpr int NC = D / 32, NV = D / 16, kRow = D * BITS / 8;
+  static constexpr int kKeyWords = NC / 2 * BITS / 4;        // of a lane
+  static constexpr int kValueBits = NV / 4 * BITS;           // of a lane and token: 4, 8, 16 or 32
+  static constexpr int kParamWords = 2 * 32 * G / kThreads;  // of a thread (0: half of the threads or fewer, one)
+  uint32_t k[kKeyWords], v[8], p[kParamWords < 1 ? 1 : kParamWords];
+
+  // rows: cache rows of the first tokens of the two halves
+  __device__ __forceinline__ void load(const qkv_cache& c, const int64_t* rows, int wave, int lane) {
+    const int x = lane & 15, j = lane >> 4;
+    const int64_t kr = rows[wave >> 1];
+    load_words<kKeyWords>(c.k + kr * kRow + (x * kRow + j * (kRow / 4) + (wave & 1) * (kRow / 8)), k);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const uint8_t* at = c.v + rows[e >> 2] * kRow;
+      const int off = (4 * wave + (e & 3)) * kRow + x * (kRow / 16) + (j * kValueBits) / 8;
+      if constexpr (kValueBits <= 8) v[e] = at[off];
+      else if constexpr (kValueBits == 16) v[e] = *(const uint16_t*)(at + off);
+      else v[e] = *(const uint32_t*)(at + off);
+    }
+#pragma unroll
+    for (int i = 0; i < (kParamWords < 1 ? 1 : kParamWords); ++i) {
+      const int w = (wave * 64 + lane) + kThreads * i;  // word of keys' then values' parameters
+      if (kParamWords >= 1 || w < 2 * 32 * G) {
+        const int in = w % (32 * G);  // word of the tile's 32 tokens
+        const int64_t at = in < 16 * G ? rows[0] * G + in : rows[1] * G + (in - 16 * G);
+        p[i] = ((const uint32_t*)(w < 32 * G ? c.k_params : c.v_params))[at];
+      }
+    }
+  }
+
+  // frags: 2 NC key operands, then NV value operands, 1 KiB each; params: keys', then values'
+  __device__ __forceinline__ void store(uint8_t* frags, uint32_t* params, int wave, int lane) const {
+    const int x = lane & 15, q = lane >> 4;
+#pragma unroll
+    for (int i = 0; i < NC / 2; ++i)
+      *(f16x8*)(frags + ((wave >> 1) * NC + (wave & 1) * (NC / 2) + i) * 1024 + lane * 16) = key_operand<BITS>(k, i);
+    constexpr int kPer = NV / 4;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      u32x4 r;
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const uint32_t a = v[2 * t], b = v[2 * t + 1];
+        if constexpr (kValueBits == 4) {  // one code in the byte's half q & 1
+          r[t] = (a | b << 16) & ((q & 1) ? 0x00f000f0u : 0x000f000fu);
+        } else if constexpr (BITS == 4) {  // codes in pairs: the odd ones times 16
+          const uint32_t m = i < 2 ? a | b << 16 : (a >> 8) | (b >> 8) << 16;
+          r[t] = m & ((i & 1) ? 0x00f000f0u : 0x000f000fu);
+        } else {
+          constexpr uint32_t sel[4] = {0x0c040c00u, 0x0c050c01u, 0x0c060c02u, 0x0c070c03u};
+          r[t] = __builtin_amdgcn_perm(b, a, sel[i]);
+        }
+      }
+      *(u32x4*)(frags + (2 * NC + q * kPer + i) * 1024 + (16 * wave + x) * 16) = r;
+    }
+#pragma unroll
+    for (int i = 0; i < (kParamWords < 1 ? 1 : kParamWords); ++i) {
+      const int w = (wave * 64 + lane) + kThreads * i;
+      if (kParamWords >= 1 || w < 2 * 32 * G) params[w] = p[i];
+    }
+  }
+};
+
+template <int G, int NC>
+struct FragKeys {
+  const uint8_t *frags, *off;  // this lane's 16 bytes of the first operand; offsets of its token x
+  __device__ __forceinline__ f16x8 operand(int hh, int c) const { return *(const f16x8*)(frags + (hh * NC + c) * 1024); }
+  __device__ __forceinline__ f16x8 offsets(int hh) const {
+    uint32_t o[4] = {0, 0, 0, 0};
+    if constexpr (G == 1) o[0] = *(const uint16_t*)(off + 64 * hh);
+    else load_words<G / 2>(off + 64 * G * hh, o);
+    return __builtin_bit_cast(f16x8, u32x4{o[0], o[1], o[2], o[3]});
+  }
+};
+
+struct FragValues {
+  const uint8_t* frags;
+  __device__ __forceinline__ void read() {}
+  __device__ __forceinline__ f16x8 operand(int n) const { return *(const f16x8*)(frags + n * 1024); }
+};
+
+template <int BITS, int D, int G, bool FINE>
+__global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void kv_prompt_kernel(KvAttnArgs p) {
+  constexpr int NC = D / 32, NV = D / 16, MT = kPromptTiles, kRows = 16 * MT;
+  constexpr int kFrags = (2 * NC + NV) * 1024, kParams = 2 * 32 * 4 * G;
+  __shared__ __attribute__((aligned(1024))) uint8_t buf[2][kFrags + kParams];
+
+  const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int lane = threadIdx.x & 63, x = lane & 15, j = lane >> 4;
+  Place at;
+  if (!at.find(p, 4 * kRows)) return;
+  Span all, own;  // of the work-group's rows and of this wave's
+  all.set(p, at, at.row0, min(at.row0 + 4 * kRows, at.rows));
+  const int row0 = at.row0 + wave * kRows;
+  const bool idle = row0 >= at.rows;  // makes operands for the others
+  own.set(p, at, idle ? at.row0 : row0, min(row0 + kRows, at.rows));
+  if (idle) own.begin = own.end = 0;
+  const int begin = all.begin & ~31, ntiles = (all.end - begin + 31) >> 5;
+  const int per = (ntiles + p.plan.splits - 1) / p.plan.splits;
+  const int t0 = begin + 32 * min(per * at.split, ntiles), t1 = begin + 32 * min(per * at.split + per, ntiles);
+
+  Queries<BITS, D, G, MT> q;
+  q.read(p, at, row0, x, j);
+
+  Pages pages;
+  Share<BITS, D, G> share;
+  int64_t rows[2];
+  int ok = 0, next_ok = 0;
+  if (t0 < t1) {
+    pages.read(p, at, t0, 32, lane);
+    ok = pages.rows(p, at, 0, t0, rows);
+    share.load(p.c, rows, wave, lane);
+  }
+  q.prepare(p, j);
+  Sums<BITS, D, G, MT> a;
+  a.clear();
+  if (t0 < t1) share.store(buf[0], (uint32_t*)(buf[0] + kFrags), wave, lane);
+  int at_buf = 0;
+  for (int t = t0, s = 1; t < t1; t += 32, ++s) {
+    __syncthreads();  // this tile is written, and the other buffer read
+    const bool more = t + 32 < t1;
+    if (more) {
+      if ((s & 31) == 0) pages.read(p, at, t + 32, 32, lane);
+      next_ok = pages.rows(p, at, s, t + 32, rows);
+      share.load(p.c, rows, wave, lane);
+    }
+    const uint8_t* read = buf[at_buf];
+    if (t < own.end && t + 32 > own.begin) {
+      const FragKeys<G, NC> keys{read + lane * 16, read + kFrags + x * 4 * G + 2 * G};
+      FragValues values{read + 2 * NC * 1024 + lane * 16};
+      const uint8_t* params = read + kFrags + j * 16 * G;
+      tile_step<FINE>(q, a, t, ok, own.whole(t), j, keys, values, params, params + kParams / 2);
+    }
+    at_buf ^= 1;
+    if (more) share.store(buf[at_buf], (uint32_t*)(buf[at_buf] + kFrags), wave, lane);
+    ok = next_ok;
+  }
+  a.close();
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+    if (!idle) a.write(p, at, m, q.out_row[m], j);
+}
+
+}  // namespace kv
+}  // namespace qmm
