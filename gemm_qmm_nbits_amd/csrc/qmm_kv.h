@@ -44,8 +44,12 @@ constexpr int kPromptTiles = 2;
 struct KvPlan {
   int mt;        // tiles of 16 rows per wave (a row = one query of one head of a cache head)
   int by_rows;   // the four waves of a work-group take other rows (else other tokens)
-  int64_t tiles; // row tiles per sequence and cache head
-  int splits;    // parts of the tokens, joined by a second launch when more than one
+  int64_t tiles;  // work-groups' row tiles per sequence and cache head
+  int rows;       // rows of such a tile that exist at most
+  // Groups (row tile, sequence, cache head) below `whole` are one work-group each; the tokens of the others
+  // are split into `splits` parts that a second launch joins.
+  int64_t groups, whole;
+  int splits;
 };
 KvPlan kv_plan(int q_heads, int heads, int D, int64_t B, int64_t max_q, int64_t max_kv,
                int64_t window);
@@ -70,8 +74,8 @@ struct KvAttnArgs {
   int page_log2;
   uint16_t* out;
   float* lse;
-  float* part;   // [splits][T][q_heads][D] sums, not yet divided
-  float* stats;  // [splits][T][q_heads][2]: reference exponent, sum
+  float* part;   // [groups - whole][rows][splits][D] sums, not yet divided
+  float* stats;  // [groups - whole][rows][splits][2]: reference exponent, sum
   KvPlan plan;
 };
 hipError_t launch_kv_attention(const KvAttnArgs& p, hipStream_t st);

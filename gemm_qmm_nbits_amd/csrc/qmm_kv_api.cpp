@@ -70,14 +70,13 @@ qmm_status check_load(const qkv_cache* c, const int32_t* slots, int64_t T, const
 bool valid_plan(int64_t T, int q_heads, int heads, int64_t B, int64_t max_q, int64_t max_kv) {
   return T >= 0 && T <= kMaxTokens && heads >= 1 && heads <= 4096 && q_heads >= heads && q_heads <= 4096 &&
          q_heads % heads == 0 && q_heads / heads <= 512 && B >= 0 && B <= 65535 && max_q >= 1 &&
-         max_q <= kMaxTokens && max_kv >= 0 && max_kv < (1LL << 31);
+         max_q <= kMaxTokens && max_q * (q_heads / heads) < (1LL << 31) && max_kv >= 0 && max_kv < (1LL << 31);
 }
 
-size_t workspace_of(int64_t T, int q_heads, int D, const KvPlan& k) {
-  if (k.splits <= 1) return 0;
-  const size_t n = (size_t)k.splits * T * q_heads;
-  return round256(n * D * 4) + n * 8;
-}
+// parts' rows of a plan
+size_t part_rows(const KvPlan& k) { return (size_t)(k.groups - k.whole) * k.rows * k.splits; }
+
+size_t workspace_of(int D, const KvPlan& k) { return round256(part_rows(k) * D * 4) + part_rows(k) * 8; }
 
 qmm_status check_attention(const void* Q, int64_t rs, int64_t hs, int type, int64_t T, int q_heads, int64_t B,
                            const int32_t* cu_q, const int32_t* kv_len, const int32_t* table, int64_t width,
@@ -94,12 +93,12 @@ qmm_status check_attention(const void* Q, int64_t rs, int64_t hs, int type, int6
   if (!cu_q && (T != B || max_q != 1)) return QMM_E_SHAPE;
   if (T == 0 || B == 0) return QMM_OK;
   const KvPlan k = kv_plan(q_heads, c->heads, c->D, B, max_q, max_kv ? max_kv : width * c->page, window);
-  if (k.tiles * k.splits * c->heads > kMaxGroups / B || (k.splits > 1 && T * q_heads > kMaxGroups)) return QMM_E_SHAPE;
+  if (k.groups * k.splits > kMaxGroups || (k.groups - k.whole) * k.rows > kMaxGroups) return QMM_E_SHAPE;
   if (!Q || !kv_len || (!table && width > 0) || !out) return QMM_E_NULL;
   if (!aligned(Q, 2) || !aligned(cu_q, 4) || !aligned(kv_len, 4) || !aligned(table, 4) || !aligned(sinks, 4) ||
       !aligned(out, 8) || !aligned(lse, 4))
     return QMM_E_ALIGN;
-  const size_t need = workspace_of(T, q_heads, c->D, k);
+  const size_t need = workspace_of(c->D, k);
   if (need) {
     if (!ws || ws_bytes < need) return QMM_E_WORKSPACE;
     if (!aligned(ws, 256)) return QMM_E_ALIGN;
@@ -187,7 +186,7 @@ qmm_status qkv_cache_load(const qkv_cache* cache, const int32_t* slots, int64_t 
 size_t qkv_attention_workspace_bytes(int64_t T, int q_heads, int heads, int D, int64_t B, int64_t max_q,
                                      int64_t max_kv, int64_t window) {
   if (!valid_plan(T, q_heads, heads, B, max_q, max_kv) || T == 0 || B == 0 || window < 0) return 0;
-  return workspace_of(T, q_heads, D, kv_plan(q_heads, heads, D, B, max_q, max_kv, window));
+  return workspace_of(D, kv_plan(q_heads, heads, D, B, max_q, max_kv, window));
 }
 
 qmm_status qkv_attention(const void* Q, int64_t row_stride, int64_t head_stride, int type, int64_t T, int q_heads,
@@ -224,13 +223,11 @@ qmm_status qkv_attention(const void* Q, int64_t row_stride, int64_t head_stride,
   p.out = (uint16_t*)out;
   p.lse = lse;
   p.plan = kv_plan(q_heads, cache->heads, cache->D, B, max_q, max_kv ? max_kv : table_width * cache->page, window);
-  if (p.plan.splits > 1) {
-    const size_t n = (size_t)p.plan.splits * T * q_heads;
-    p.part = (float*)workspace;
-    p.stats = (float*)((char*)workspace + round256(n * cache->D * 4));
-  }
+  const size_t parts = part_rows(p.plan);
+  p.part = (float*)workspace;
+  p.stats = (float*)((char*)workspace + round256(parts * cache->D * 4));
   hipError_t e = launch_kv_attention(p, (hipStream_t)stream);
-  if (e == hipSuccess && p.plan.splits > 1) e = launch_kv_combine(p, (hipStream_t)stream);
+  if (e == hipSuccess && parts > 0) e = launch_kv_combine(p, (hipStream_t)stream);
   if (e != hipSuccess) return (qmm_status)e;
   return (qmm_status)hipGetLastError();
 }

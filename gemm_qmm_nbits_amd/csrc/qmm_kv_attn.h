@@ -9,8 +9,8 @@ namespace kv {
 
 template <typename F>
 hipError_t go(F kernel, const KvAttnArgs& p, hipStream_t st) {
-  const int64_t groups = p.plan.splits * p.c.heads * p.B * p.plan.tiles;
-  launch(kernel, dim3((unsigned)groups), dim3(kThreads), 0, st, p);
+  const int64_t n = p.plan.whole + (p.plan.groups - p.plan.whole) * p.plan.splits;
+  launch(kernel, dim3((unsigned)n), dim3(kThreads), 0, st, p);
   return hipGetLastError();
 }
 

@@ -2,8 +2,7 @@
 #include <algorithm>
 
 #include "qmm_device.h"
-#include "qmm_internal.h"
-#include "qmm_kv.h"
+#include "qmm_kv_rows.h"
 
 namespace qmm {
 
@@ -12,65 +11,10 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kMaxParts = 128;  // two a lane
 
-// A work-group per output row (query, head).  Every wave reads the parts' two numbers, two a lane, and
-// keeps their factors in its own piece of LDS; then kThreads / (D / 4) parts at a time are summed, 4
-// dimensions a lane, each thread's parts in order, and the threads' sums in order.  A part without visible
-// tokens has sum 0 and is skipped: its vector was not written.
-__global__ __launch_bounds__(kThreads) void kv_combine_kernel(KvAttnArgs p) {
-  __shared__ float factors[kThreads / 64][kMaxParts];
-  __shared__ f32x4 join[kThreads];
-  const int tid = threadIdx.x, lane = tid & 63, per = p.c.D / 4, lanes = kThreads / per;
-  const int64_t row = blockIdx.x, n = p.T * p.q_heads;
-  if (p.cu_q) {  // rows of no sequence, and those past max_q, have no parts
-    const int64_t t = row / p.q_heads;
-    int64_t lo = 0, hi = p.B;  // the last sequence that begins at or before row t
-    while (hi - lo > 1) {
-      const int64_t mid = (lo + hi) >> 1;
-      if (p.cu_q[mid] <= t) lo = mid;
-      else hi = mid;
-    }
-    const int64_t q0 = min(max((int64_t)p.cu_q[lo], (int64_t)0), p.T);
-    const int64_t q1 = min(max((int64_t)p.cu_q[lo + 1], q0), p.T);
-    if (t < q0 || t >= q1 || t - q0 >= p.max_q) return;
-  }
-  const int splits = p.plan.splits;
-  float* factor = factors[tid >> 6];
-  float rs[2], ls[2], ref = -INFINITY;
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const int s = lane + 64 * k;
-    const float* st = p.stats + 2 * ((s < splits ? s : 0) * n + row);
-    rs[k] = st[0];
-    ls[k] = s < splits ? st[1] : 0.0f;
-    if (ls[k] != 0.0f) ref = fmaxf(ref, rs[k]);
-  }
-#pragma unroll
-  for (int k = 1; k < 64; k <<= 1) ref = fmaxf(ref, __shfl_xor(ref, k, 64));
-  float total = 0.0f;
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const float a = ls[k] != 0.0f ? __builtin_amdgcn_exp2f(rs[k] - ref) : 0.0f;
-    factor[lane + 64 * k] = a;
-    total = ls[k] != 0.0f ? fmaf(ls[k], a, total) : total;
-  }
-#pragma unroll
-  for (int k = 1; k < 64; k <<= 1) total += __shfl_xor(total, k, 64);
-  const int d = 4 * (tid % per);
-  f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 4
-  for (int s = tid / per; s < splits; s += lanes) {
-    const float a = factor[s];
-    if (a != 0.0f) {
-      const f32x4 v = *(const f32x4*)(p.part + (s * n + row) * p.c.D + d);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) o[i] = fmaf(v[i], a, o[i]);
-    }
-  }
-  join[tid] = o;
-  __syncthreads();
-  if (tid >= per) return;
-  for (int k = 1; k < lanes; ++k) o += join[k * per + tid];
-  const bool none = total == 0.0f;
+// The result of a row from its parts' sums, 4 dimensions d .. d + 3 a lane: `ref` is the greatest of their
+// reference exponents (-inf without any).
+__device__ __forceinline__ void finish(const KvAttnArgs& p, int64_t row, int d, f32x4 o, float total, float ref) {
+  const bool none = ref == -INFINITY;
   float lse = none ? -INFINITY : (ref + __builtin_amdgcn_logf(total)) * 0.69314718f;
   if (p.sinks) {
     const float sink = p.sinks[row % p.q_heads];
@@ -89,7 +33,101 @@ __global__ __launch_bounds__(kThreads) void kv_combine_kernel(KvAttnArgs p) {
   *(uint2*)(p.out + row * p.c.D + d) = *(const uint2*)r;
 }
 
+// Row `index` of those whose tokens were split: its row of the parts and of the output; false if it does not
+// exist.
+__device__ __forceinline__ bool find_row(const KvAttnArgs& p, int per_group, uint32_t index, int64_t* from,
+                                         int64_t* row) {
+  const uint32_t group = index / (uint32_t)p.plan.rows, local = index % (uint32_t)p.plan.rows;
+  kv::Place at;
+  if ((int64_t)group >= p.plan.groups - p.plan.whole) return false;
+  if (!at.find(p, per_group, (uint32_t)p.plan.whole + group) || at.row0 + (int)local >= at.rows) return false;
+  const uint32_t i = (at.row0 + local) / (uint32_t)at.R;
+  *row = (at.q0 + i) * p.q_heads + at.h * at.R + (at.row0 + local - i * at.R);
+  *from = at.part + local;
+  return true;
+}
+
+// Few parts: D / 4 lanes per row, each of which sums its 4 dimensions over the parts in order.  A part without
+// visible tokens has sum 0 and is skipped: its vector was not written.
+constexpr int kFewParts = 8;
+__global__ __launch_bounds__(kThreads) void kv_combine_few_kernel(KvAttnArgs p, int per_group) {
+  const int per = p.c.D / 4, d = 4 * (threadIdx.x % per);
+  int64_t from, row;
+  if (!find_row(p, per_group, blockIdx.x * (kThreads / per) + threadIdx.x / per, &from, &row)) return;
+  const int splits = p.plan.splits;
+  float rs[kFewParts], ls[kFewParts], ref = -INFINITY, total = 0.0f;
+  f32x4 v[kFewParts], o = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int s = 0; s < kFewParts; ++s) {
+    const int64_t at = from * splits + (s < splits ? s : 0);
+    rs[s] = p.stats[2 * at];
+    ls[s] = s < splits ? p.stats[2 * at + 1] : 0.0f;
+    v[s] = *(const f32x4*)(p.part + at * p.c.D + d);
+    if (ls[s] != 0.0f) ref = fmaxf(ref, rs[s]);
+  }
+#pragma unroll
+  for (int s = 0; s < kFewParts; ++s)
+    if (ls[s] != 0.0f) {
+      const float a = __builtin_amdgcn_exp2f(rs[s] - ref);
+      total = fmaf(ls[s], a, total);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[i] = fmaf(v[s][i], a, o[i]);
+    }
+  finish(p, row, d, o, total, ref);
+}
+
+// A work-group per row.  Every wave reads the parts' two numbers, two a lane, and keeps their factors in its
+// own piece of LDS; then kThreads / (D / 4) parts at a time are summed, 4 dimensions a lane, each thread's
+// parts in order, and the threads' sums in order.
+__global__ __launch_bounds__(kThreads) void kv_combine_kernel(KvAttnArgs p, int per_group) {
+  __shared__ float factors[kThreads / 64][kMaxParts];
+  __shared__ f32x4 join[kThreads];
+  const int tid = threadIdx.x, lane = tid & 63, per = p.c.D / 4, lanes = kThreads / per;
+  int64_t from, row;  // of the parts, of the output
+  if (!find_row(p, per_group, blockIdx.x, &from, &row)) return;
+  const int splits = p.plan.splits;
+  float* factor = factors[tid >> 6];
+  float rs[2], ls[2], ref = -INFINITY;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int s = lane + 64 * k;
+    const float* st = p.stats + 2 * (from * splits + (s < splits ? s : 0));
+    rs[k] = st[0];
+    ls[k] = s < splits ? st[1] : 0.0f;
+    if (ls[k] != 0.0f) ref = fmaxf(ref, rs[k]);
+  }
+#pragma unroll
+  for (int k = 1; k < 64; k <<= 1) ref = fmaxf(ref, __shfl_xor(ref, k, 64));
+  float total = 0.0f;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const float a = ls[k] != 0.0f ? __builtin_amdgcn_exp2f(rs[k] - ref) : -1.0f;
+    factor[lane + 64 * k] = a;  // -1: nothing to add
+    total = ls[k] != 0.0f ? fmaf(ls[k], a, total) : total;
+  }
+#pragma unroll
+  for (int k = 1; k < 64; k <<= 1) total += __shfl_xor(total, k, 64);
+  const int d = 4 * (tid % per);
+  f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 8
+  for (int s = tid / per; s < splits; s += lanes) {
+    const f32x4 v = *(const f32x4*)(p.part + (from * splits + s) * p.c.D + d);
+    const float a = factor[s];
+    if (!(a < 0.0f))
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[i] = fmaf(v[i], a, o[i]);
+  }
+  join[tid] = o;
+  __syncthreads();
+  if (tid >= per) return;
+  for (int k = 1; k < lanes; ++k) o += join[k * per + tid];
+  finish(p, row, d, o, total, ref);
+}
+
 }  // namespace
+
+// rows of a work-group
+static int64_t rows_of(const KvPlan& k) { return k.by_rows ? 64 * kPromptTiles : 16 * k.mt; }
 
 KvPlan kv_plan(int q_heads, int heads, int D, int64_t B, int64_t max_q, int64_t max_kv, int64_t window) {
   KvPlan k{};
@@ -97,22 +135,38 @@ KvPlan kv_plan(int q_heads, int heads, int D, int64_t B, int64_t max_q, int64_t 
   const int most = D == 256 ? 2 : 4;
   k.mt = rows <= 16 ? 1 : rows <= 32 || most == 2 ? 2 : 4;
   k.by_rows = rows > 16 * most;
-  const int64_t per = k.by_rows ? 64 * kPromptTiles : 16 * k.mt;
+  const int64_t per = rows_of(k);
   k.tiles = (rows + per - 1) / per;
-  const int64_t groups = k.tiles * heads * B;
+  k.rows = (int)std::min(rows, per);
+  k.groups = k.tiles * heads * B;
   // tokens that a row tile sees at most
   if (window > 0 && window < max_kv) max_kv = std::min(max_kv, window + std::min(max_q, (per - 1) / (q_heads / heads) + 2));
   auto over = [](int64_t n, int64_t d) { return (n + d - 1) / d; };
-  int64_t splits = k.by_rows ? std::min(groups < 256 ? over(256, groups) : 1, over(max_kv, 512))
-                             : std::max(std::min(over(512, groups), over(max_kv, 256)),
-                                        std::min(over(3072, groups), over(max_kv, 2048)));
-  if (splits > kMaxParts) splits = kMaxParts;
-  k.splits = splits < 1 ? 1 : (int)splits;
+  int64_t splits;
+  if (k.by_rows) {
+    // whole rounds of work-groups, two to a compute unit (D = 256: one); what is left over would take a
+    // round of its own and is split as far as that round has room
+    const int64_t room = D == 256 ? 256 : 512;
+    k.whole = k.groups / room * room;
+    const int64_t left = k.groups - k.whole;
+    // (not where the last row tiles see few tokens anyway: a prompt from its first token on)
+    splits = left > 0 && (k.whole == 0 || max_kv >= 2 * max_q) ? std::min(room / left, over(max_kv, 512)) : 1;
+  } else {
+    // two work-groups to a compute unit, with 256 tokens at least, or more where there is more work
+    splits = std::max(std::min(over(512, k.groups), over(max_kv, 256)), std::min(over(3072, k.groups), over(max_kv, 2048)));
+  }
+  k.splits = (int)std::min<int64_t>(std::max<int64_t>(splits, 1), kMaxParts);
+  if (k.splits == 1) k.whole = k.groups;
   return k;
 }
 
 hipError_t launch_kv_combine(const KvAttnArgs& p, hipStream_t st) {
-  launch(kv_combine_kernel, dim3((unsigned)(p.T * p.q_heads)), dim3(kThreads), 0, st, p);
+  const int64_t rows = (p.plan.groups - p.plan.whole) * p.plan.rows;
+  const int per = (int)rows_of(p.plan), each = kThreads / (p.c.D / 4);
+  if (p.plan.splits <= kFewParts)
+    launch(kv_combine_few_kernel, dim3((unsigned)((rows + each - 1) / each)), dim3(kThreads), 0, st, p, per);
+  else
+    launch(kv_combine_kernel, dim3((unsigned)rows), dim3(kThreads), 0, st, p, per);
   return hipGetLastError();
 }
 

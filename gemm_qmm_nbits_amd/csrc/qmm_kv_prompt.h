@@ -100,7 +100,7 @@ struct FragValues {
 };
 
 template <int BITS, int D, int G, bool FINE>
-__global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void kv_prompt_kernel(KvAttnArgs p) {
+__global__ __launch_bounds__(kThreads, D == 256 ? 1 : D == 64 ? 3 : 2) void kv_prompt_kernel(KvAttnArgs p) {
   constexpr int NC = D / 32, NV = D / 16, MT = kPromptTiles, kRows = 16 * MT;
   constexpr int kFrags = (2 * NC + NV) * 1024, kParams = 2 * 32 * 4 * G;
   __shared__ __attribute__((aligned(1024))) uint8_t buf[2][kFrags + kParams];
@@ -116,7 +116,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void kv_prompt_kernel(K
   own.set(p, at, idle ? at.row0 : row0, min(row0 + kRows, at.rows));
   if (idle) own.begin = own.end = 0;
   const int begin = all.begin & ~31, ntiles = (all.end - begin + 31) >> 5;
-  const int per = (ntiles + p.plan.splits - 1) / p.plan.splits;
+  const int per = (ntiles + at.splits - 1) / at.splits;
   const int t0 = begin + 32 * min(per * at.split, ntiles), t1 = begin + 32 * min(per * at.split + per, ntiles);
 
   Queries<BITS, D, G, MT> q;
@@ -158,7 +158,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void kv_prompt_kernel(K
   a.close();
 #pragma unroll
   for (int m = 0; m < MT; ++m)
-    if (!idle) a.write(p, at, m, q.out_row[m], j);
+    if (!idle) a.write(p, at, m, wave * kRows + 16 * m + x, q.out_row[m], j);
 }
 
 }  // namespace kv

@@ -134,16 +134,28 @@ __device__ __forceinline__ float exponent_above(u16x2 m) {
 // A work-group's place in the call: a part of the tokens, a sequence, a cache head and its row tiles (rows
 // are queries times the heads that share the cache head, heads fastest).
 struct Place {
-  int split, h;
+  int split, splits, h;
+  int64_t part;       // row of the parts' buffers that belongs to row0
   int64_t b, q0, nq;  // first query row, queries
   int R, rows, row0;  // heads per cache head, rows of the sequence, first row of the work-group
   int len;
 
-  // False if there is nothing to do.  `per`: rows of a work-group.
+  // The work-group's; false if there is nothing to do.  `per`: rows of a work-group.
   __device__ __forceinline__ bool find(const KvAttnArgs& p, int per) {
     uint32_t id = blockIdx.x;
-    split = id % (uint32_t)p.plan.splits;
-    id /= (uint32_t)p.plan.splits;
+    const uint32_t whole = (uint32_t)p.plan.whole;
+    split = 0;
+    splits = 1;
+    if (id >= whole) {
+      splits = p.plan.splits;
+      split = (id - whole) % (uint32_t)splits;
+      id = whole + (id - whole) / (uint32_t)splits;
+    }
+    return find(p, per, id);
+  }
+  // That of group `id`.
+  __device__ __forceinline__ bool find(const KvAttnArgs& p, int per, uint32_t id) {
+    part = ((int64_t)id - p.plan.whole) * p.plan.rows;
     h = id % (uint32_t)p.c.heads;
     id /= (uint32_t)p.c.heads;
     b = id % (uint32_t)p.B;
@@ -323,10 +335,12 @@ struct Sums {
   }
 
   // The rows of row tile m: the result, or the part's sums and statistics.
-  __device__ __forceinline__ void write(const KvAttnArgs& p, const Place& at, int m, int64_t out_row, int j) const {
+  // `row`: of the work-group.
+  __device__ __forceinline__ void write(const KvAttnArgs& p, const Place& at, int m, int row, int64_t out_row,
+                                        int j) const {
     if (out_row < 0) return;
-    if (p.plan.splits > 1) {
-      const int64_t to = at.split * p.T * p.q_heads + out_row;
+    if (at.splits > 1) {
+      const int64_t to = (at.part + row) * at.splits + at.split;
       if (j == 0) {
         p.stats[2 * to] = ref[m];
         p.stats[2 * to + 1] = l[m];

@@ -146,7 +146,7 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(BITS, D, MT)) void kv_toke
   span.set(p, at, at.row0, min(at.row0 + kRows, at.rows));
   // this work-group's part of the tokens, in tiles of 32, of which each wave takes every fourth
   const int begin = span.begin & ~31, ntiles = (span.end - begin + 31) >> 5;
-  const int per = max((ntiles + p.plan.splits - 1) / p.plan.splits, 8);
+  const int per = max((ntiles + at.splits - 1) / at.splits, 8);
   const int tile0 = min(per * at.split, ntiles) + wave, tile1 = min(per * at.split + per, ntiles);
   const int steps = tile1 > tile0 ? (tile1 - tile0 + 3) / 4 : 0;
   const int t0 = begin + 32 * tile0;
@@ -234,7 +234,7 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(BITS, D, MT)) void kv_toke
   }
   if (wave != 0) return;
 #pragma unroll
-  for (int m = 0; m < MT; ++m) a.write(p, at, m, q.out_row[m], j);
+  for (int m = 0; m < MT; ++m) a.write(p, at, m, 16 * m + x, q.out_row[m], j);
 }
 
 }  // namespace kv

@@ -112,7 +112,7 @@ def test_attention_workspace():
     assert attn(max_kv=30000, ws=FAKE + 128, wsb=need) == -6
     # max_kv 0 takes the table's width
     assert attn(max_kv=0, width=1875) == -7 and attn(max_kv=0, width=1875, ws=FAKE, wsb=need) == 0
-    # the sums and their two numbers for some number of parts
+    # the sums and their two numbers of every row, for some number of parts
     rows = 5 * 32
     assert any(need == -(-s * rows * 128 * 4 // 256) * 256 + s * rows * 8 for s in range(2, 200))
     # one part: nothing to join
