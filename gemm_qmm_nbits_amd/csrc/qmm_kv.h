@@ -57,6 +57,7 @@ KvPlan kv_plan(int q_heads, int heads, int D, int64_t B, int64_t max_q, int64_t 
 struct KvAttnArgs {
   const uint16_t* q;
   int64_t row_stride, head_stride;
+  int vec;  // rows allow 16-byte loads
   int type;
   int64_t T;
   int q_heads, ratio;  // ratio = q_heads / heads

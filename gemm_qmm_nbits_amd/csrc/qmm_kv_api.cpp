@@ -204,6 +204,7 @@ qmm_status qkv_attention(const void* Q, int64_t row_stride, int64_t head_stride,
   p.q = (const uint16_t*)Q;
   p.row_stride = row_stride;
   p.head_stride = head_stride;
+  p.vec = aligned(Q, 16) && row_stride % 8 == 0 && head_stride % 8 == 0;
   p.type = type;
   p.T = T;
   p.q_heads = q_heads;

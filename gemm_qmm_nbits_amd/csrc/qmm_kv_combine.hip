@@ -76,13 +76,14 @@ __global__ __launch_bounds__(kThreads) void kv_combine_few_kernel(KvAttnArgs p, 
   finish(p, row, d, o, total, ref);
 }
 
-// A work-group per row.  Every wave reads the parts' two numbers, two a lane, and keeps their factors in its
-// own piece of LDS; then kThreads / (D / 4) parts at a time are summed, 4 dimensions a lane, each thread's
-// parts in order, and the threads' sums in order.
-__global__ __launch_bounds__(kThreads) void kv_combine_kernel(KvAttnArgs p, int per_group) {
-  __shared__ float factors[kThreads / 64][kMaxParts];
-  __shared__ f32x4 join[kThreads];
-  const int tid = threadIdx.x, lane = tid & 63, per = p.c.D / 4, lanes = kThreads / per;
+// Many parts: a work-group per row.  Every wave reads the parts' two numbers, two a lane, and keeps their
+// factors in its own piece of LDS; then kWide / (D / 4) parts at a time are summed, 4 dimensions a lane, each
+// thread's parts in order, and the threads' sums in order.
+template <int kWide>
+__global__ __launch_bounds__(kWide) void kv_combine_kernel(KvAttnArgs p, int per_group) {
+  __shared__ float factors[kWide / 64][kMaxParts];
+  __shared__ f32x4 join[kWide];
+  const int tid = threadIdx.x, lane = tid & 63, per = p.c.D / 4, lanes = kWide / per;
   int64_t from, row;  // of the parts, of the output
   if (!find_row(p, per_group, blockIdx.x, &from, &row)) return;
   const int splits = p.plan.splits;
@@ -109,7 +110,7 @@ __global__ __launch_bounds__(kThreads) void kv_combine_kernel(KvAttnArgs p, int 
   for (int k = 1; k < 64; k <<= 1) total += __shfl_xor(total, k, 64);
   const int d = 4 * (tid % per);
   f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 8
+#pragma unroll 4
   for (int s = tid / per; s < splits; s += lanes) {
     const f32x4 v = *(const f32x4*)(p.part + (from * splits + s) * p.c.D + d);
     const float a = factor[s];
@@ -120,6 +121,7 @@ __global__ __launch_bounds__(kThreads) void kv_combine_kernel(KvAttnArgs p, int 
   join[tid] = o;
   __syncthreads();
   if (tid >= per) return;
+#pragma unroll 8
   for (int k = 1; k < lanes; ++k) o += join[k * per + tid];
   finish(p, row, d, o, total, ref);
 }
@@ -143,17 +145,18 @@ KvPlan kv_plan(int q_heads, int heads, int D, int64_t B, int64_t max_q, int64_t 
   if (window > 0 && window < max_kv) max_kv = std::min(max_kv, window + std::min(max_q, (per - 1) / (q_heads / heads) + 2));
   auto over = [](int64_t n, int64_t d) { return (n + d - 1) / d; };
   int64_t splits;
+  const int64_t room = D == 256 ? 256 : 512;  // work-groups at once: two to a compute unit, or one
   if (k.by_rows) {
-    // whole rounds of work-groups, two to a compute unit (D = 256: one); what is left over would take a
+    // whole rounds of work-groups; what is left over would take a
     // round of its own and is split as far as that round has room
-    const int64_t room = D == 256 ? 256 : 512;
     k.whole = k.groups / room * room;
     const int64_t left = k.groups - k.whole;
     // (not where the last row tiles see few tokens anyway: a prompt from its first token on)
     splits = left > 0 && (k.whole == 0 || max_kv >= 2 * max_q) ? std::min(room / left, over(max_kv, 512)) : 1;
   } else {
-    // two work-groups to a compute unit, with 256 tokens at least, or more where there is more work
-    splits = std::max(std::min(over(512, k.groups), over(max_kv, 256)), std::min(over(3072, k.groups), over(max_kv, 2048)));
+    // one round of work-groups, with 256 tokens at least, or more where there is more work
+    splits = std::max(std::min(std::max<int64_t>(room / k.groups, 1), over(max_kv, 256)),
+                      std::min(over(3072, k.groups), over(max_kv, 2048)));
   }
   k.splits = (int)std::min<int64_t>(std::max<int64_t>(splits, 1), kMaxParts);
   if (k.splits == 1) k.whole = k.groups;
@@ -165,8 +168,10 @@ hipError_t launch_kv_combine(const KvAttnArgs& p, hipStream_t st) {
   const int per = (int)rows_of(p.plan), each = kThreads / (p.c.D / 4);
   if (p.plan.splits <= kFewParts)
     launch(kv_combine_few_kernel, dim3((unsigned)((rows + each - 1) / each)), dim3(kThreads), 0, st, p, per);
+  else if (rows < 512)  // the chip is not full: 40 rows of 128 parts, 6 us instead of 12
+    launch(kv_combine_kernel<1024>, dim3((unsigned)rows), dim3(1024), 0, st, p, per);
   else
-    launch(kv_combine_kernel, dim3((unsigned)rows), dim3(kThreads), 0, st, p, per);
+    launch(kv_combine_kernel<256>, dim3((unsigned)rows), dim3(256), 0, st, p, per);
   return hipGetLastError();
 }
 

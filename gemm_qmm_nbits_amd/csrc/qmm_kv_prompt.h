@@ -119,9 +119,9 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : D == 64 ? 3 : 2) void kv_p
   const int per = (ntiles + at.splits - 1) / at.splits;
   const int t0 = begin + 32 * min(per * at.split, ntiles), t1 = begin + 32 * min(per * at.split + per, ntiles);
 
-  Queries<BITS, D, G, MT> q;
-  q.read(p, at, row0, x, j);
-
+  QueryPieces<BITS, D, 1, 64> pieces[MT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) pieces[m].read(p, at, row0 + 16 * m, lane);
   Pages pages;
   Share<BITS, D, G> share;
   int64_t rows[2];
@@ -131,7 +131,18 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : D == 64 ? 3 : 2) void kv_p
     ok = pages.rows(p, at, 0, t0, rows);
     share.load(p.c, rows, wave, lane);
   }
-  q.prepare(p, j);
+  Queries<BITS, D, G, MT> q;
+  q.place(p, at, row0, x);
+  uint8_t* mine = buf[0] + wave * query_bytes<D>;  // a wave's queries pass through its own part
+  static_assert(sizeof(buf) >= 4 * query_bytes<D>);
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    pieces[m].template write<G>(p, mine, lane);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    q.take(m, mine, lane);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  }
+  __syncthreads();  // the buffers are free
   Sums<BITS, D, G, MT> a;
   a.clear();
   if (t0 < t1) share.store(buf[0], (uint32_t*)(buf[0] + kFrags), wave, lane);

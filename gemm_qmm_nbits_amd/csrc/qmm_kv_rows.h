@@ -215,6 +215,108 @@ struct Pages {
   }
 };
 
+// ---- queries ------------------------------------------------------------------------------------------
+// Rows of queries become operands by way of LDS: lanes read 8 consecutive dimensions each, a row's lanes find
+// its largest magnitude and group sums among themselves, and scatter the elements to where the lanes that
+// hold the operands read 16 bytes at once.  (Element loads by the lanes that need them, every wave for
+// itself, took 18 us in a call of 512 work-groups with 32 rows each.)
+
+template <int BITS>
+__device__ __forceinline__ constexpr int slot_of_field(int e) {
+  const int r = e & 3;
+  return BITS == 4 ? (e < 4 ? 2 * e : 2 * (e - 4) + 1) : (e & 4) + ((r >> 1) | ((r & 1) << 1));
+}
+
+// Sum or maximum over aligned groups of 4, 8, 16 or 32 lanes.
+template <bool MAX>
+__device__ __forceinline__ float over_lanes(float v, int lanes) {
+  auto with = [&](float u) { v = MAX ? fmaxf(v, u) : v + u; };
+  with(dpp_f<kDppXor1>(v));
+  with(dpp_f<kDppXor2>(v));
+  if (lanes > 4) with(dpp_f<kDppHalfMirror>(v));
+  if (lanes > 8) with(dpp_f<kDppMirror>(v));
+  if (lanes > 16) with(__shfl_xor(v, 16, 64));
+  return v;
+}
+
+// Operands of a row tile in LDS.
+template <int D>
+constexpr int query_bytes = (D / 32 + 1) * 1024 + 64;
+
+// `N` pieces of 8 dimensions of a thread, out of the rows of `TILES` row tiles that `THREADS` threads share.
+template <int BITS, int D, int TILES, int THREADS>
+struct QueryPieces {
+  static constexpr int LR = D / 8, kPieces = TILES * 16 * LR, N = kPieces < THREADS ? 1 : kPieces / THREADS;
+  static_assert(kPieces % 64 == 0 && (kPieces < THREADS || kPieces % THREADS == 0));  // whole waves
+  u32x4 v[N];
+
+  __device__ __forceinline__ void read(const KvAttnArgs& p, const Place& at, int row0, int thread) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const int piece = k * THREADS + thread, row = row0 + piece / LR, a = piece % LR;
+      if (kPieces < THREADS && piece >= kPieces) break;
+      // (a row past the last takes the first one's query; its results go nowhere)
+      const uint32_t r = row < at.rows ? row : 0, i = r / (uint32_t)at.R;
+      const uint16_t* q = p.q + (at.q0 + i) * p.row_stride + (at.h * at.R + (r - i * at.R)) * p.head_stride + 8 * a;
+      if (p.vec) {
+        v[k] = *(const u32x4*)q;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[k][e] = (uint32_t)q[2 * e] | (uint32_t)q[2 * e + 1] << 16;
+      }
+    }
+  }
+
+  // to: query_bytes<D> for each row tile
+  template <int G>
+  __device__ __forceinline__ void write(const KvAttnArgs& p, uint8_t* to, int thread) const {
+    constexpr int lg = LR / G;  // lanes of a group
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const int piece = k * THREADS + thread, row = piece / LR, a = piece % LR, x = row & 15;
+      if (kPieces < THREADS && piece >= kPieces) break;
+      uint8_t* tile = to + (row >> 4) * query_bytes<D>;
+      float f[8], top = 0.0f, finite = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint16_t u = (uint16_t)(v[k][e / 2] >> (16 * (e & 1)));
+        f[e] = p.type == QMM_F16 ? f16_to_f32(u) : bf16_to_f32(u);
+        top = fmaxf(top, fabsf(f[e]));
+        finite = fmaf(f[e], 0.0f, finite);  // NaN once an element is not finite
+      }
+      top = over_lanes<true>(finite == 0.0f ? top : INFINITY, LR);
+      // largest magnitude to [2^7, 2^8): a group's sum stays below 2^15
+      const int be = (int)(__float_as_uint(top) >> 23);
+      const int ex = min(max(134 - max(be, 1), -96), 100);
+      const float up = __uint_as_float((uint32_t)(ex + 127) << 23);
+      float sum = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float y = f[e] * up;
+        sum += (float)(_Float16)y;
+        const int field = 2 * (a & 3) + e / 4, j = e % 4;
+        // (slots of odd and even fields differ only by lane: the factor of odd 4-bit fields is the lane's)
+        const float z = BITS == 4 && (field & 1) ? y * 0.0625f : y;
+        *(_Float16*)(tile + (a >> 2) * 1024 + (j * 16 + x) * 16 + 2 * slot_of_field<BITS>(field)) = (_Float16)z;
+      }
+      sum = over_lanes<false>(sum, lg);
+      uint8_t* sq = tile + (D / 32) * 1024 + x * 16;
+      if (a % lg == 0) {
+        const _Float16 s0 = (_Float16)sum;
+        const float r1 = sum - (float)s0;
+        const _Float16 s1 = (_Float16)r1;
+        _Float16* to_g = (_Float16*)sq + a / lg;
+        to_g[0] = s0;
+        to_g[128] = s1;
+        to_g[256] = (_Float16)(r1 - (float)s1);
+      }
+      if (a == 0)
+        ((float*)(tile + (D / 32 + 1) * 1024))[x] =
+            top < 0x1p100f ? p.scale * __uint_as_float((uint32_t)(127 - ex) << 23) : __builtin_nanf("");
+    }
+  }
+};
+
 // The queries of a wave's MT row tiles: operands, group sums, factors of the scores, what each row sees.
 template <int BITS, int D, int G, int MT>
 struct Queries {
@@ -223,77 +325,33 @@ struct Queries {
   float f24[MT], f1[MT];
   int see_lo[MT], see_hi[MT];
   int64_t out_row[MT];  // row of Q times q_heads plus head; -1: no row
-  uint16_t raw[MT][NC][8];
 
-  __device__ __forceinline__ void read(const KvAttnArgs& p, const Place& at, int row0, int x, int j) {
+  __device__ __forceinline__ void place(const KvAttnArgs& p, const Place& at, int row0, int x) {
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
       const int row = row0 + 16 * m + x;
       const bool has = row < at.rows;
-      // (a row past the last takes the first one's query; its results go nowhere)
       const uint32_t i = (uint32_t)(has ? row : 0) / (uint32_t)at.R;
       const int head = at.h * at.R + (int)((has ? row : 0) - i * at.R);
       out_row[m] = has ? (at.q0 + i) * p.q_heads + head : -1;
       const int64_t pos = at.len - at.nq + i;
       see_hi[m] = has ? (int)(p.causal ? max(pos + 1, (int64_t)0) : at.len) : 0;
       see_lo[m] = p.window > 0 ? (int)max(pos - p.window + 1, (int64_t)0) : 0;
-      const uint16_t* q = p.q + (at.q0 + i) * p.row_stride + head * p.head_stride + j;
-#pragma unroll
-      for (int c = 0; c < NC; ++c)
-#pragma unroll
-        for (int s = 0; s < 8; ++s) raw[m][c][s] = q[32 * c + 4 * key_field<BITS>(s)];
     }
   }
 
-  __device__ __forceinline__ void prepare(const KvAttnArgs& p, int j) {
+  // from: what QueryPieces wrote of row tile m
+  __device__ __forceinline__ void take(int m, const uint8_t* from, int lane) {
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      float v[NC][8], top = 0.0f;
+    for (int c = 0; c < NC; ++c) qb[m][c] = *(const f16x8*)(from + c * 1024 + lane * 16);
+    u32x4 s = *(const u32x4*)(from + NC * 1024 + lane * 16);
+    if (lane >= 48) s = u32x4{0, 0, 0, 0};
+    if constexpr (G == 1) s[0] &= 0xffffu;
 #pragma unroll
-      for (int c = 0; c < NC; ++c)
-#pragma unroll
-        for (int s = 0; s < 8; ++s) {
-          const uint16_t u = raw[m][c][s];
-          v[c][s] = p.type == QMM_F16 ? f16_to_f32(u) : bf16_to_f32(u);
-          const float a = fabsf(v[c][s]);
-          top = a <= top ? top : a;  // keeps a NaN
-        }
-#pragma unroll
-      for (int k = 16; k <= 32; k <<= 1) {
-        const float a = __shfl_xor(top, k, 64);
-        top = a <= top || top != top ? top : a;
-      }
-      // largest magnitude to [2^7, 2^8): a group's sum stays below 2^15
-      const int be = (int)(__float_as_uint(top) >> 23);
-      const int ex = min(max(134 - max(be, 1), -96), 100);
-      const float up = __uint_as_float((uint32_t)(ex + 127) << 23);
-      f1[m] = top < 0x1p100f ? p.scale * __uint_as_float((uint32_t)(127 - ex) << 23) : __builtin_nanf("");
-      f24[m] = f1[m] * 0x1p24f;
-      float sums[G];
-#pragma unroll
-      for (int g = 0; g < G; ++g) sums[g] = 0.0f;
-#pragma unroll
-      for (int c = 0; c < NC; ++c)
-#pragma unroll
-        for (int s = 0; s < 8; ++s) {
-          const float a = v[c][s] * up;
-          sums[c * G / NC] += (float)(_Float16)a;
-          qb[m][c][s] = (_Float16)(BITS == 4 && (key_field<BITS>(s) & 1) ? a * 0.0625f : a);
-        }
-#pragma unroll
-      for (int g = 0; g < 8; ++g) {
-        _Float16 piece = (_Float16)0.0f;
-        if (g < G) {
-          const float s = sum_over_j(sums[g < G ? g : 0]);
-          const _Float16 a = (_Float16)s;
-          const float r1 = s - (float)a;
-          const _Float16 bb = (_Float16)r1;
-          const _Float16 cc = (_Float16)(r1 - (float)bb);
-          piece = j == 0 ? a : j == 1 ? bb : j == 2 ? cc : (_Float16)0.0f;
-        }
-        sq[m][g] = piece;
-      }
-    }
+    for (int w = (G + 1) / 2; w < 4; ++w) s[w] = 0;
+    sq[m] = __builtin_bit_cast(f16x8, s);
+    f1[m] = ((const float*)(from + (NC + 1) * 1024))[lane & 15];
+    f24[m] = f1[m] * 0x1p24f;
   }
 };
 

@@ -134,8 +134,9 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(BITS, D, MT)) void kv_toke
   typedef Format<BITS, D, G> F;
   constexpr int NV = D / 16, kRows = 16 * MT, kBuf = 4 * F::kTile;
   static_assert(kBuf >= 2 * NV * 1024, "the join uses the first buffer");
+  constexpr int kQueries = MT * query_bytes<D>;  // these pass through the second buffer
   // objects of their own, so that the compiler does not make a read of one wait for the copies into the other
-  __shared__ __attribute__((aligned(1024))) uint8_t ring0[kBuf], ring1[kBuf];
+  __shared__ __attribute__((aligned(1024))) uint8_t ring0[kBuf], ring1[kBuf > kQueries ? kBuf : kQueries];
   __shared__ float refs[4][kRows], ls[4][kRows];
 
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
@@ -151,8 +152,8 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(BITS, D, MT)) void kv_toke
   const int steps = tile1 > tile0 ? (tile1 - tile0 + 3) / 4 : 0;
   const int t0 = begin + 32 * tile0;
 
-  Queries<BITS, D, G, MT> q;
-  q.read(p, at, at.row0, x, j);
+  QueryPieces<BITS, D, MT, kThreads> pieces;
+  pieces.read(p, at, at.row0, threadIdx.x);
 
   Pages pages;
   // the copies of step s's tile; whether its halves have a page
@@ -170,7 +171,13 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(BITS, D, MT)) void kv_toke
     return ok;
   };
   int ok0 = fetch(0, ring0), ok1 = 0;
-  q.prepare(p, j);
+  Queries<BITS, D, G, MT> q;
+  q.place(p, at, at.row0, x);
+  pieces.template write<G>(p, ring1, threadIdx.x);
+  __syncthreads();
+#pragma unroll
+  for (int m = 0; m < MT; ++m) q.take(m, ring1 + m * query_bytes<D>, lane);
+  __syncthreads();  // the buffer is free
   Sums<BITS, D, G, MT> a;
   a.clear();
 
