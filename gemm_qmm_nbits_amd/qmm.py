@@ -862,27 +862,36 @@ class _Place:
         self.device = device
 
 
+def _dense(t, dtype, shape, dev):
+    """Whether t is a dense tensor of that dtype and shape on device index `dev` (what _expect explains if not)."""
+    return t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous()
+
+
 def _kv_cache(cache):
-    """Checks a cache's tensors: device index, (pages, heads, page, D) and the descriptor."""
+    """Checks a cache's tensors: types, device index, heads, page, D and the descriptor."""
     ty = _types()
-    k, bits, group = cache["k"], cache["bits"], cache["group"]
-    if bits not in (4, 8):
+    torch = ty.torch
+    k, v, kp, vp, bits, group = (cache["k"], cache["v"], cache["k_params"], cache["v_params"], cache["bits"],
+                                 cache["group"])
+    if bits != 4 and bits != 8:
         raise QmmError("qkv_cache", QMM_E_BITS)
-    if k.dim() != 4:
+    shape = k.shape
+    if len(shape) != 4:
         raise ValueError("k must be [pages, heads, page, D * bits / 8]")
-    pages, heads, page, row = k.shape
+    pages, heads, page, row = shape
     D = row * 8 // bits
     if group not in (32, 64, 128) or D % group:
         raise QmmError("qkv_cache", QMM_E_BLOCK)
     dev = _device_of(k)
-    _expect(k, "k", k.shape, ty.u8, dev)
-    _expect(cache["v"], "v", k.shape, ty.u8, dev)
-    shape = (pages, heads, page, 2, D // group)
-    f16 = ty.only[ty.torch.float16]
-    _expect(cache["k_params"], "k_params", shape, f16, dev)
-    _expect(cache["v_params"], "v_params", shape, f16, dev)
-    c = qkv_cache(k.data_ptr(), cache["v"].data_ptr(), cache["k_params"].data_ptr(), cache["v_params"].data_ptr(),
-                  pages, heads, page, D, bits, group)
+    params = (pages, heads, page, 2, D // group)
+    u8, f16 = torch.uint8, torch.float16
+    if not (_dense(k, u8, shape, dev) and _dense(v, u8, shape, dev) and _dense(kp, f16, params, dev)
+            and _dense(vp, f16, params, dev)):
+        _expect(k, "k", shape, ty.u8, dev)
+        _expect(v, "v", shape, ty.u8, dev)
+        _expect(kp, "k_params", params, ty.only[f16], dev)
+        _expect(vp, "v_params", params, ty.only[f16], dev)
+    c = qkv_cache(k.data_ptr(), v.data_ptr(), kp.data_ptr(), vp.data_ptr(), pages, heads, page, D, bits, group)
     return ty, dev, heads, page, D, c
 
 
@@ -928,9 +937,9 @@ def qkv_cache_load(cache, slots, out_dtype=None, K=None, V=None, need=(True, Tru
         given = K if K is not None else V
         out_dtype = ty.torch.float32 if given is None else given.dtype
     if K is None and need[0]:
-        K = _new((T, heads, D), out_dtype, cache["k"], stream)
+        K = _new((T, heads, D), out_dtype, slots, stream)
     if V is None and need[1]:
-        V = _new((T, heads, D), out_dtype, cache["k"], stream)
+        V = _new((T, heads, D), out_dtype, slots, stream)
     k_p, k_t = _optional(K, "K", (T, heads, D), ty.any, dev)
     v_p, v_t = _optional(V, "V", (T, heads, D), ty.any, dev)
     if K is not None and V is not None and k_t != v_t:
@@ -955,32 +964,45 @@ def qkv_attention(Q, cache, table, kv_len, cu_q=None, max_q=None, max_kv=None, s
     ty, dev, heads, page, D, c = _kv_cache(cache)
     if Q.dim() != 3:
         raise ValueError("Q must be [T, q_heads, D]")
-    T, q_heads = Q.shape[0], Q.shape[1]
+    T, q_heads, _ = Q.shape
     code, row, head = _rows_of(Q, "Q", q_heads, D, ty.half, dev)
     if q_heads % heads:
         raise ValueError(f"{q_heads} query heads do not share {heads} cache heads evenly")
     if table.dim() != 2:
         raise ValueError("table must be [B, width]")
     B, width = table.shape
-    _expect(table, "table", (B, width), ty.i32, dev)
-    _expect(kv_len, "kv_len", (B,), ty.i32, dev)
-    cu_p, _ = _optional(cu_q, "cu_q", (B + 1,), ty.i32, dev)
-    s_p, _ = _optional(sinks, "sinks", (q_heads,), ty.f32, dev)
+    i32 = ty.torch.int32
+    if not (_dense(table, i32, (B, width), dev) and _dense(kv_len, i32, (B,), dev)):
+        _expect(table, "table", (B, width), ty.i32, dev)
+        _expect(kv_len, "kv_len", (B,), ty.i32, dev)
+    cu_p = s_p = l_p = None
+    if sinks is not None:
+        _expect(sinks, "sinks", (q_heads,), ty.f32, dev)
+        s_p = sinks.data_ptr()
     if cu_q is None:
         if T != B:
             raise ValueError("without cu_q every sequence has one query: Q must be [B, q_heads, D]")
         max_q = 1
-    elif max_q is None:
-        max_q = max(T, 1)
+    else:
+        _expect(cu_q, "cu_q", (B + 1,), ty.i32, dev)
+        cu_p = cu_q.data_ptr()
+        if max_q is None:
+            max_q = max(T, 1)
     bound = max_kv or width * page
     if out is None:
         out = _new((T, q_heads, D), Q.dtype, Q, stream)
-    _expect(out, "out", (T, q_heads, D), ty.only[Q.dtype], dev)
-    if lse is None and need_lse:
+    else:
+        _expect(out, "out", (T, q_heads, D), ty.only[Q.dtype], dev)
+    if lse is not None:
+        _expect(lse, "lse", (T, q_heads), ty.f32, dev)
+        l_p = lse.data_ptr()
+    elif need_lse:
         lse = _new((T, q_heads), ty.torch.float32, Q, stream)
-    l_p, _ = _optional(lse, "lse", (T, q_heads), ty.f32, dev)
-    keep, ws, wsb = _scratch(workspace, _bytes_of("qkv_attention_workspace_bytes", T, q_heads, heads, D, B, max_q,
-                                                  bound, window), Q, stream)
+        l_p = lse.data_ptr()
+    need = _bytes_of("qkv_attention_workspace_bytes", T, q_heads, heads, D, B, max_q, bound, window)
+    ws, wsb = None, 0
+    if need > 1 or workspace is not None:
+        keep, ws, wsb = _scratch(workspace, need, Q, stream)
     st = lib().qkv_attention(Q.data_ptr(), row, head, code, T, q_heads, B, cu_p, kv_len.data_ptr(), table.data_ptr(),
                              width, max_q, bound, D ** -0.5 if scale is None else float(scale), int(bool(causal)),
                              window, s_p, ctypes.byref(c), out.data_ptr(), l_p, ws, wsb, _handle(stream, dev))
