@@ -42,8 +42,8 @@ constexpr int kPromptTiles = 2;
 
 // How an attention call is laid out: a function of the sizes only.
 struct KvPlan {
-  int mt;        // tiles of 16 rows per wave (a row = one query of one head of a cache head)
-  int by_rows;   // the four waves of a work-group take other rows (else other tokens)
+  int by_rows;    // the four waves of a work-group take other rows (else other tokens)
+  int mt;         // tiles of 16 rows per wave if not (a row = one query of one head of a cache head)
   int64_t tiles;  // work-groups' row tiles per sequence and cache head
   int rows;       // rows of such a tile that exist at most
   // Groups (row tile, sequence, cache head) below `whole` are one work-group each; the tokens of the others

@@ -16,11 +16,9 @@ hipError_t go(F kernel, const KvAttnArgs& p, hipStream_t st) {
 
 template <int BITS, int D, int G, bool FINE>
 hipError_t by_plan(const KvAttnArgs& p, hipStream_t st) {
-  constexpr int kMost = D == 256 ? 2 : 4;
   if (p.plan.by_rows) return go(kv_prompt_kernel<BITS, D, G, FINE>, p, st);
   if (p.plan.mt == 1) return go(kv_tokens_kernel<BITS, D, G, 1, FINE>, p, st);
-  if (p.plan.mt == 2) return go(kv_tokens_kernel<BITS, D, G, 2, FINE>, p, st);
-  return go(kv_tokens_kernel<BITS, D, G, kMost, FINE>, p, st);
+  return go(kv_tokens_kernel<BITS, D, G, 2, FINE>, p, st);
 }
 
 template <int BITS, int D, int G>

@@ -134,9 +134,12 @@ static int64_t rows_of(const KvPlan& k) { return k.by_rows ? 64 * kPromptTiles :
 KvPlan kv_plan(int q_heads, int heads, int D, int64_t B, int64_t max_q, int64_t max_kv, int64_t window) {
   KvPlan k{};
   const int64_t rows = max_q * (q_heads / heads);
-  const int most = D == 256 ? 2 : 4;
-  k.mt = rows <= 16 ? 1 : rows <= 32 || most == 2 ? 2 : 4;
-  k.by_rows = rows > 16 * most;
+  // The kernel for many rows does the least work per row and token, the one for few rows has its answer
+  // sooner: 4 waves share a row tile's tokens, and there are four times as many work-groups.  The first where
+  // there is work enough (32 heads on 8, 128 dimensions, one sequence: 512 of 512 tokens 33 against 21 us, 1024 of
+  // 1024 37 and 45, 512 of 8192 139 and 182).
+  k.by_rows = rows > 64 && rows * heads * B >= (1ll << 26) / std::max<int64_t>(max_kv, 1);
+  k.mt = rows <= 16 ? 1 : 2;
   const int64_t per = rows_of(k);
   k.tiles = (rows + per - 1) / per;
   k.rows = (int)std::min(rows, per);
