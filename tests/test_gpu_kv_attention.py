@@ -108,13 +108,39 @@ def test_single_tokens(bits, D, group, ty):
     check(p, "single")
 
 
-# queries per sequence such that every number of row tiles per wave is taken, with four heads per cache head:
-# up to 16 rows, 32, 64, and waves on rows of their own past that (128 at D = 256: past 32)
+# Past 64 rows of one cache head, calls that expect much work take another kernel: with MUCH tokens expected
+# these small ones do too.
+MUCH = 1 << 30
+KERNELS = pytest.mark.parametrize("kv", [None, MUCH], ids=["few", "many"])
+
+
+# queries per sequence, with four heads per cache head: up to 16 rows, 32, two row tiles and many
 @pytest.mark.parametrize("bits,D,group", FORMATS)
 @pytest.mark.parametrize("news", [[4, 3, 1], [8, 5, 2], [16, 9, 13], [70, 33, 1]])
 def test_several_tokens(bits, D, group, news):
     p = Problem([90, 41, 13], news, heads=4, kv=1, D=D, bits=bits, group=group, seed=sum(news) + D)
     check(p, "several")
+
+
+@pytest.mark.parametrize("bits,D,group", FORMATS)
+@pytest.mark.parametrize("ty", ["f16", "bf16"])
+def test_many_rows(bits, D, group, ty):
+    """Row tiles of 128 with rows missing, in parts that join."""
+    p = Problem([90, 41, 13], [70, 33, 1], heads=4, kv=1, D=D, bits=bits, group=group, seed=D + group, ty=ty)
+    check(p, "many", max_kv=MUCH)
+
+
+@pytest.mark.parametrize("D,page", [(64, 16), (128, 64)])
+def test_many_rows_in_one_part(D, page):
+    """Work-groups enough that none is split: the results are written directly."""
+    p = Problem([150, 100, 70, 333], [70, 65, 70, 1], heads=72, kv=72, D=D, group=64, page=page, seed=D)
+    check(p, "one part", max_kv=MUCH)
+
+
+def test_many_work_groups_and_some_left_over():
+    """More than one round of work-groups, of which the rest is split."""
+    p = Problem([140, 130, 129, 131, 70], [130, 66, 129, 66, 67], heads=60, kv=60, D=64, group=64, seed=3)
+    check(p, "left over", max_kv=MUCH)
 
 
 @pytest.mark.parametrize("heads,kv", [(1, 1), (3, 3), (5, 1), (10, 2), (40, 10), (16, 1), (17, 1), (64, 8), (72, 1)])
@@ -126,36 +152,40 @@ def test_head_layouts(heads, kv, new):
 
 @pytest.mark.parametrize("page", [16, 32, 64, 128, 512])
 @pytest.mark.parametrize("new", [1, 40])
-def test_pages(page, new):
+@KERNELS
+def test_pages(page, new, kv):
     """Pages that end inside a tile and tables with more pages than tokens."""
     p = Problem([16, 200, 531, 49], [new if n >= new else n for n in (16, 200, 531, 49)], page=page, seed=page)
-    check(p, "pages")
+    check(p, "pages", max_kv=kv)
 
 
 @pytest.mark.parametrize("window", [1, 2, 16, 31, 32, 33, 100, 10 ** 6, 2 ** 40])
 @pytest.mark.parametrize("new", [1, 5, 90])
-def test_windows(window, new):
+@KERNELS
+def test_windows(window, new, kv):
     t = torch()
     p = Problem([300, 95, 4], [new, new, min(new, 4)], seed=new)
-    check(p, "window", window=window)
-    check(p, "window, sinks", window=window, sinks=t.linspace(-3, 3, p.heads, device="cuda"))
+    check(p, "window", window=window, max_kv=kv)
+    check(p, "window, sinks", window=window, sinks=t.linspace(-3, 3, p.heads, device="cuda"), max_kv=kv)
 
 
 @pytest.mark.parametrize("new", [1, 20, 100])
-def test_not_causal(new):
+@KERNELS
+def test_not_causal(new, kv):
     p = Problem([130, 101, 300], [new] * 3, seed=new)
-    check(p, "all tokens", causal=False)
+    check(p, "all tokens", causal=False, max_kv=kv)
 
 
 @pytest.mark.parametrize("news", [[5, 5, 5], [30, 40, 9]])
-def test_queries_that_see_nothing(news):
+@KERNELS
+def test_queries_that_see_nothing(news, kv):
     """More queries than tokens: the first ones stand before the sequence."""
     t = torch()
     p = Problem([3, 0, 1], news, seed=2)
-    out, lse = check(p, "nothing")
+    out, lse = check(p, "nothing", max_kv=kv)
     assert not bool(out[news[0]:news[0] + news[1]].any())
     sinks = t.randn(p.heads, device="cuda")
-    out, lse = check(p, "nothing, sinks", sinks=sinks)
+    out, lse = check(p, "nothing, sinks", sinks=sinks, max_kv=kv)
     assert bool((lse[news[0]] == sinks).all())
 
 
@@ -168,12 +198,14 @@ def test_sinks(sink):
     check(p, "sinks, parts", sinks=sinks, max_kv=100000)
     p = Problem([200, 77], [50, 77], seed=6)
     check(p, "sinks, many rows", sinks=sinks)
+    check(p, "sinks, many rows, parts", sinks=sinks, max_kv=MUCH)
 
 
 @pytest.mark.parametrize("scale", [0.0, -0.3, 1.0, 1e-3])
 def test_scales(scale):
     check(Problem([130, 64], [1, 1], seed=7), "scale", scale=scale)
     check(Problem([130, 64], [33, 20], seed=7), "scale", scale=scale)
+    check(Problem([130, 64], [33, 20], seed=7), "scale", scale=scale, max_kv=MUCH)
 
 
 @pytest.mark.parametrize("max_kv", [1, 300, 2000, 20000, 10 ** 9])
@@ -193,35 +225,38 @@ def test_long():
 
 @pytest.mark.parametrize("std,v_std", [(30.0, 1.0), (1e-3, 1e-3), (5.0, 100.0), (1.0, 3e-4)])
 @pytest.mark.parametrize("new", [1, 70])
-def test_ranges(std, v_std, new):
+@KERNELS
+def test_ranges(std, v_std, new, kv):
     """Peaked and flat softmax, large and small values (scales down to fp16's subnormals)."""
-    check(Problem([300, 90], [new, new], q_std=std, v_std=v_std, seed=11), "ranges")
+    check(Problem([300, 90], [new, new], q_std=std, v_std=v_std, seed=11), "ranges", max_kv=kv)
 
 
-def test_value_scales_that_grow():
+@pytest.mark.parametrize("new", [1, 90])
+@KERNELS
+def test_value_scales_that_grow(new, kv):
     """Later tokens with scales a million times the first ones', in one group of several: the reference exponent
     follows, whatever the scores do."""
     t = torch()
-    p = Problem([400], [1], D=128, group=32, seed=12, page=16)
+    p = Problem([400], [new], D=128, group=32, seed=12, page=16)
     pages = p.table_h[0]
     for i, pg in enumerate(pages):
         p.cache["v_params"][int(pg), :, :, :, 1] *= float(2.0 ** (i % 13 - 6))
-    check(p, "growing")
+    check(p, "growing", max_kv=kv)
     for i, pg in enumerate(pages):
         p.cache["k_params"][int(pg)] *= float(2.0 ** ((i % 5) - 2))
-    check(p, "growing scores")
+    check(p, "growing scores", max_kv=kv)
     t.cuda.synchronize()
 
 
 @pytest.mark.parametrize("new", [1, 6, 70])
-def test_hidden_tokens_do_not_leak(new):
+@KERNELS
+def test_hidden_tokens_do_not_leak(new, kv):
     """NaN in tokens behind the sequence, before the window, after a query's position, on pages that are not in the
     table, and any bits there: the results of rows that do not see them keep every bit."""
     t = torch()
     p = Problem([100, 77], [new, new], page=16, seed=13)
     window = 30
-    clean = [host_bits(x).copy() for x in p.call(window=window)]
-    last = dev(np.array([15], np.int32))
+    clean = [host_bits(x).copy() for x in p.call(window=window, max_kv=kv)]
     # all slots of no sequence, and those behind each sequence's end
     used = np.zeros((p.cache["k"].shape[0], 16), bool)
     for b, n in enumerate(p.lens):
@@ -231,7 +266,7 @@ def test_hidden_tokens_do_not_leak(new):
     for w in ("k", "v"):
         p.cache[w].permute(0, 2, 1, 3)[hide] = 255
         p.cache[w + "_params"].permute(0, 2, 1, 3, 4)[hide] = float("nan")
-    got = [host_bits(x) for x in p.call(window=window)]
+    got = [host_bits(x) for x in p.call(window=window, max_kv=kv)]
     assert all(np.array_equal(a, b) for a, b in zip(got, clean))
     # a token in the middle: rows whose window misses it, and rows before it, keep their bits
     tok = p.lens[0] - max(1, new // 2)
@@ -239,7 +274,7 @@ def test_hidden_tokens_do_not_leak(new):
     for w in ("k", "v"):
         p.cache[w + "_params"][pg, :, tok % 16, 1] = float("nan")
         p.cache[w + "_params"][pg, :, tok % 16, 0] = float("inf")
-    out, lse = p.call(window=window)
+    out, lse = p.call(window=window, max_kv=kv)
     first = p.lens[0] - new
     for i in range(p.T):
         sees = i < new and tok <= first + i and tok > first + i - window
@@ -252,11 +287,10 @@ def test_hidden_tokens_do_not_leak(new):
         p.cache[w + "_params"][pg, :, tok % 16] = 1.0
     p.cache["v_params"][pg, :, tok % 16, 1, 1] = float("nan")
     p.cache["v_params"][pg, :, tok % 16, 0, 1] = 0.0
-    out, lse = p.call(window=window)
+    out, lse = p.call(window=window, max_kv=kv)
     i = tok - first
     assert bool(t.isnan(out[i, :, 32:]).all()) and not bool(t.isnan(out[i, :, :32]).any())
     assert not bool(t.isnan(lse[i]).any())
-    del last
 
 
 def test_pages_outside_the_pool():
@@ -269,6 +303,7 @@ def test_pages_outside_the_pool():
         p.table.copy_(dev(p.table_h))
         check(p, "pages outside")
         check(p, "pages outside", causal=False)
+        check(p, "pages outside", max_kv=MUCH)
     t.cuda.synchronize()
 
 
@@ -285,12 +320,14 @@ def test_lengths_outside_the_table():
     assert bool(t.isneginf(lse[1]).all())
 
 
-def test_rows_of_no_sequence():
+@pytest.mark.parametrize("many", [False, True])
+def test_rows_of_no_sequence(many):
     """Rows before the first sequence, behind the last and past max_q are left as they were; offsets outside [0, T]
     are clamped."""
     t = torch()
-    for max_kv in (None, 50000):
-        p = Problem([50, 90, 20], [4, 6, 2], seed=16, extra=5)
+    for max_kv in (None, 50000, MUCH):
+        # (many: 32 heads of one cache head, 192 rows and more)
+        p = Problem([50, 90, 20], [4, 6, 2], heads=32 if many else 8, kv=1 if many else 2, seed=16, extra=5)
         cu = np.array([2, 6, 12, 14], np.int32)
         p.cu_h = cu
         p.cu.copy_(dev(cu))
@@ -307,30 +344,32 @@ def test_rows_of_no_sequence():
 
 
 @pytest.mark.parametrize("ty", ["f16", "bf16"])
-def test_strided_queries(ty):
+@KERNELS
+def test_strided_queries(ty, kv):
     """Queries as a slice of a fused projection, at any element offset, heads first, and shared rows."""
     t = torch()
-    p = Problem([60, 45], [5, 9], ty=ty, seed=17)
-    want = [host_bits(x).copy() for x in p.call()]
+    p = Problem([60, 45], [5, 30], ty=ty, seed=17)
+    want = [host_bits(x).copy() for x in p.call(max_kv=kv)]
     wide = t.zeros(p.T, p.heads + 3, p.D + 1, dtype=tt(ty), device="cuda")
     base = p.Q
     for view in (wide[:, 1:p.heads + 1, 1:], wide[:, 3:, :p.D],
                  t.zeros(p.heads, p.T, p.D, dtype=tt(ty), device="cuda").transpose(0, 1)):
         view.copy_(base)
         p.Q = view
-        got = [host_bits(x) for x in p.call()]
+        got = [host_bits(x) for x in p.call(max_kv=kv)]
         assert all(np.array_equal(a, b) for a, b in zip(got, want))
     p.Q = base[:1].expand(p.T, p.heads, p.D)
-    check(p, "shared rows")
+    check(p, "shared rows", max_kv=kv)
 
 
-def test_queries_not_finite():
+@KERNELS
+def test_queries_not_finite(kv):
     t = torch()
     for new in (1, 40):
         p = Problem([60, 45], [new, new], seed=18)
-        clean = host_bits(p.call()[0]).copy()
+        clean = host_bits(p.call(max_kv=kv)[0]).copy()
         p.Q[0, 1, 5], p.Q[0, 2, 0], p.Q[new, 3, 63] = float("nan"), float("inf"), -float("inf")
-        out, lse = p.call()
+        out, lse = p.call(max_kv=kv)
         bad = [(0, 1), (0, 2), (new, 3)]
         for r, a in bad:
             assert bool(t.isnan(out[r, a]).all()) and bool(t.isnan(lse[r, a]))
@@ -343,11 +382,11 @@ def test_queries_not_finite():
 def test_queries_of_a_wide_range():
     """bf16 rows of 1e30 and of 1e-30 (scores scaled back), with elements 2^-20 of the largest: all are kept."""
     t = torch()
-    for s in (2.0 ** 90, 2.0 ** -100):
-        p = Problem([60, 45], [1, 1], seed=19)
+    for s, new in ((2.0 ** 90, 1), (2.0 ** -100, 1), (2.0 ** 90, 40)):
+        p = Problem([60, 45], [new, new], seed=19)
         p.Q[:, :, ::2] *= 2.0 ** -20
         p.Q *= s
-        check(p, "range", scale=0.1 / s)
+        check(p, "range", scale=0.1 / s, max_kv=MUCH)
     t.cuda.synchronize()
 
 
@@ -406,6 +445,47 @@ def test_repeats_streams_and_graph():
         want = [host_bits(x) for x in step()]
         for a, b in zip(got, want + want):
             assert np.array_equal(a, b), k
+
+
+@pytest.mark.parametrize("kv", [400, MUCH])
+def test_prompt_chunk_in_a_graph(kv):
+    """Storing a chunk of a prompt and attention over it, captured; offsets, lengths and inputs change between
+    replays, with eager calls and other allocations between them."""
+    t = torch()
+    p = Problem([200, 150], [90, 60], heads=8, kv=2, D=128, group=64, page=32, seed=23)
+    new = t.randn(2, 150, 2, 128, device="cuda", dtype=t.bfloat16)
+    slots = t.zeros(150, dtype=t.int32, device="cuda")
+    out, lse = t.empty(150, 8, 128, dtype=t.bfloat16, device="cuda"), t.empty(150, 8, device="cuda")
+
+    def place(cu, lens):
+        at = []
+        for b in range(2):
+            n = cu[b + 1] - cu[b]
+            at += [p.table_h[b, i // 32] * 32 + i % 32 for i in range(lens[b] - n, lens[b])]
+        slots.copy_(dev(np.array(at, np.int32)))
+
+    def step(o=out, e=lse):
+        Q.qkv_cache_store(new[0], new[1], slots, p.cache)
+        return Q.qkv_attention(p.Q, p.cache, p.table, p.kv_len, cu_q=p.cu, max_q=100, max_kv=kv, out=o, lse=e)
+
+    place(p.cu_h, p.lens)
+    ref = [host_bits(x).copy() for x in step()]
+    assert all(np.array_equal(host_bits(a), b) for a, b in zip(step(), ref))
+    g = t.cuda.CUDAGraph()
+    with t.cuda.graph(g):
+        step()
+    for k, (cu, lens) in enumerate((([0, 90, 150], [200, 150]), ([0, 60, 150], [60, 160]), ([0, 100, 150], [101, 50]),
+                                    ([0, 90, 150], [200, 150]))):
+        p.cu.copy_(dev(np.array(cu, np.int32)))
+        p.kv_len.copy_(dev(np.array(lens, np.int32)))
+        place(cu, lens)
+        new.copy_(t.randn(2, 150, 2, 128, device="cuda"))
+        g.replay()
+        t.cuda.synchronize()
+        got = [host_bits(x).copy() for x in (out, lse)]
+        p.cu_h, p.lens, p.news = np.array(cu), lens, [cu[1], cu[2] - cu[1]]
+        for a, b in zip(got, check(p, "graph", max_q=100, max_kv=kv)):
+            assert np.array_equal(a, host_bits(b)), k
 
 
 def test_batch_gives_the_rows_of_single_calls():
