@@ -6,6 +6,13 @@
 // products, in their register layout, and leaves them in LDS, where reading one is a conflict-free 16 bytes
 // per lane.  Two buffers: while the waves work on one tile the words of the next are on their way to
 // registers, and are written to the other buffer at the end; one barrier per tile.
+//
+// With groups of 32 and bf16 results the value operands are values, fp16(c s + o) with one rounding (relative
+// 2^-11; the scale and the offset are multiples of 2^-24, so small values are exact), and the weights p alone
+// are rounded to fp16: the second product then needs neither scales nor offsets per row.  2048 queries at 8192
+// tokens, 4 bits: 40 heads of 128 dimensions on 10 682 -> 551 us, 64 of 64 on 8 664 -> 586, 16 of 256 on 8
+// 1003 -> 837; with groups of 64 or 128 between 8 % more and 6 % less.  For fp16 results it would cost a bit:
+// codes.
 #pragma once
 
 #include "qmm_kv_rows.h"
@@ -16,7 +23,7 @@ namespace kv {
 // What a thread makes of a tile.  Keys: wave w the chunks (w & 1) NC / 2 .. of half w >> 1, whose codes are
 // neighbours in a lane's part of a row.  Values: the lane whose operand elements belong to token quarter
 // j = w and dimension x, NV / 4 of the row tiles n (by lane >> 4).
-template <int BITS, int D, int G>
+template <int BITS, int D, int G, bool VALUES>
 struct Share {
   static constexpr int NC = D / 32, NV = D / 16, kRow = D * BITS / 8;
   static constexpr int kKeyWords = NC / 2 * BITS / 4;        // of a lane
@@ -37,6 +44,9 @@ struct Share {
       else if constexpr (kValueBits == 16) v[e] = *(const uint16_t*)(at + off);
       else v[e] = *(const uint32_t*)(at + off);
     }
+  }
+
+  __device__ __forceinline__ void load_params(const qkv_cache& c, const int64_t* rows, int wave, int lane) {
 #pragma unroll
     for (int i = 0; i < (kParamWords < 1 ? 1 : kParamWords); ++i) {
       const int w = (wave * 64 + lane) + kThreads * i;  // word of keys' then values' parameters
@@ -48,35 +58,88 @@ struct Share {
     }
   }
 
-  // frags: 2 NC key operands, then NV value operands, 1 KiB each; params: keys', then values'
-  __device__ __forceinline__ void store(uint8_t* frags, uint32_t* params, int wave, int lane) const {
+  // Codes i of tokens 2 t and 2 t + 1 as the halves of a word; `odd_times_16`: those of odd i of 4 bits so.
+  __device__ __forceinline__ uint32_t codes(int t, int i, int q, bool odd_times_16) const {
+    const uint32_t a = v[2 * t], b = v[2 * t + 1];
+    if constexpr (BITS == 8) {
+      constexpr uint32_t sel[4] = {0x0c040c00u, 0x0c050c01u, 0x0c060c02u, 0x0c070c03u};
+      return __builtin_amdgcn_perm(b, a, sel[i]);
+    } else {
+      const uint32_t m = i < 2 ? a | b << 16 : (a >> 8) | (b >> 8) << 16;
+      const bool odd = kValueBits == 4 ? q & 1 : i & 1;  // (4 bits: one code, in the byte's half q & 1)
+      if (odd_times_16) return m & (odd ? 0x00f000f0u : 0x000f000fu);
+      return (odd ? m >> 4 : m) & 0x000f000fu;
+    }
+  }
+
+  __device__ __forceinline__ void store_params(uint32_t* params, int wave, int lane) const {
+#pragma unroll
+    for (int i = 0; i < (kParamWords < 1 ? 1 : kParamWords); ++i) {
+      const int w = (wave * 64 + lane) + kThreads * i;
+      if (kParamWords >= 1 || w < 2 * 32 * G) params[w] = p[i];
+    }
+  }
+
+  // frags: 2 NC key operands, then NV value operands, 1 KiB each.  VALUES: params: the tile's, in LDS; bad: set
+  // where one of values is not finite
+  __device__ __forceinline__ void store(uint8_t* frags, const uint32_t* params, int* bad, int wave, int lane) const {
     const int x = lane & 15, q = lane >> 4;
 #pragma unroll
     for (int i = 0; i < NC / 2; ++i)
       *(f16x8*)(frags + ((wave >> 1) * NC + (wave & 1) * (NC / 2) + i) * 1024 + lane * 16) = key_operand<BITS>(k, i);
     constexpr int kPer = NV / 4;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      u32x4 r;
+    u32x4* to = (u32x4*)(frags + (2 * NC + q * kPer) * 1024 + (16 * wave + x) * 16);
+    if constexpr (VALUES) {
+      u32x4 r[kPer];
+      f16x2 z = {0, 0}, scale[4][G == 8 ? 2 : 1], off[4][G == 8 ? 2 : 1];
+      // words of a token: G = 1 scale and offset; G = 2 scales, offsets; else one of the scales, one of the offsets
+      const uint32_t* at = params + 32 * G + 4 * wave * G + (G == 4 ? q >> 1 : G == 8 ? q : 0);
+      const uint32_t own = (G == 2 ? q >= 2 : q & 1) ? 0x07060302u : 0x05040100u;
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
-        const uint32_t a = v[2 * t], b = v[2 * t + 1];
-        if constexpr (kValueBits == 4) {  // one code in the byte's half q & 1
-          r[t] = (a | b << 16) & ((q & 1) ? 0x00f000f0u : 0x000f000fu);
-        } else if constexpr (BITS == 4) {  // codes in pairs: the odd ones times 16
-          const uint32_t m = i < 2 ? a | b << 16 : (a >> 8) | (b >> 8) << 16;
-          r[t] = m & ((i & 1) ? 0x00f000f0u : 0x000f000fu);
-        } else {
-          constexpr uint32_t sel[4] = {0x0c040c00u, 0x0c050c01u, 0x0c060c02u, 0x0c070c03u};
-          r[t] = __builtin_amdgcn_perm(b, a, sel[i]);
+        const uint32_t* a = at + (16 * (t >> 1) + 2 * (t & 1)) * G;
+        const uint32_t s0 = a[0], s1 = a[G], o0 = G > 1 ? a[G / 2] : s0, o1 = G > 1 ? a[G + G / 2] : s1;
+        auto halves = [&](uint32_t x, uint32_t y, uint32_t sel) {
+          return __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(y, x, sel));
+        };
+        scale[t][0] = halves(s0, s1, G == 1 || G == 8 ? 0x05040100u : own);
+        off[t][0] = halves(o0, o1, G == 1 ? 0x07060302u : G == 8 ? 0x05040100u : own);
+        if constexpr (G == 8) {
+          scale[t][1] = halves(s0, s1, 0x07060302u);
+          off[t][1] = halves(o0, o1, 0x07060302u);
         }
       }
-      *(u32x4*)(frags + (2 * NC + q * kPer + i) * 1024 + (16 * wave + x) * 16) = r;
-    }
+      const f16x2 none = {0, 0}, base = {1024, 1024};
 #pragma unroll
-    for (int i = 0; i < (kParamWords < 1 ? 1 : kParamWords); ++i) {
-      const int w = (wave * 64 + lane) + kThreads * i;
-      if (kParamWords >= 1 || w < 2 * 32 * G) params[w] = p[i];
+      for (int i = 0; i < kPer; ++i)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          // 0x6400 + c is the fp16 number 1024 + c
+          const f16x2 c = __builtin_bit_cast(f16x2, codes(t, i, q, false) | 0x64006400u) - base;
+          const f16x2 y = __builtin_elementwise_fma(c, scale[t][G == 8 ? i >> 1 : 0], off[t][G == 8 ? i >> 1 : 0]);
+          z = __builtin_elementwise_fma(y, none, z);
+          r[i][t] = __builtin_bit_cast(uint32_t, y);
+        }
+      if (__builtin_expect(__builtin_amdgcn_ballot_w64(z[0] != z[0] || z[1] != z[1]) != 0, 0)) {
+        *bad = 1;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+#pragma unroll
+          for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+              if (((r[i][t] >> (16 * half)) & 0x7c00u) == 0x7c00u) r[i][t] &= ~(0xffffu << (16 * half));
+      }
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) to[i * 64] = r[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        u32x4 r;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) r[t] = codes(t, i, q, true);
+        to[i * 64] = r;
+      }
     }
   }
 };
@@ -93,8 +156,12 @@ struct FragKeys {
   }
 };
 
+template <bool VALUES>
 struct FragValues {
+  static constexpr bool kValues = VALUES;
   const uint8_t* frags;
+  const int* flag;
+  __device__ __forceinline__ bool bad() const { return __builtin_amdgcn_readfirstlane(*flag) != 0; }
   __device__ __forceinline__ void read() {}
   __device__ __forceinline__ f16x8 operand(int n) const { return *(const f16x8*)(frags + n * 1024); }
 };
@@ -103,7 +170,11 @@ template <int BITS, int D, int G, bool FINE>
 __global__ __launch_bounds__(kThreads, D == 256 ? 1 : D == 64 ? 3 : 2) void kv_prompt_kernel(KvAttnArgs p) {
   constexpr int NC = D / 32, NV = D / 16, MT = kPromptTiles, kRows = 16 * MT;
   constexpr int kFrags = (2 * NC + NV) * 1024, kParams = 2 * 32 * 4 * G;
-  __shared__ __attribute__((aligned(1024))) uint8_t buf[2][kFrags + kParams];
+  constexpr bool kValues = !FINE && G == NC;
+  constexpr int kAhead = kValues ? 2 : 1, kRing = kAhead + 1;  // tiles that parameters come ahead (codes: one)
+  __shared__ __attribute__((aligned(1024))) uint8_t buf[2][kFrags];
+  __shared__ __attribute__((aligned(16))) uint32_t params[kRing][kParams / 4];  // of tile s: s % kRing
+  __shared__ int bad[3];  // of tile s: bad[s % 3], cleared two tiles ahead
 
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int lane = threadIdx.x & 63, x = lane & 15, j = lane >> 4;
@@ -123,13 +194,19 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : D == 64 ? 3 : 2) void kv_p
 #pragma unroll
   for (int m = 0; m < MT; ++m) pieces[m].read(p, at, row0 + 16 * m, lane);
   Pages pages;
-  Share<BITS, D, G> share;
+  Share<BITS, D, G, kValues> share;
   int64_t rows[2];
-  int ok = 0, next_ok = 0;
+  int ok = 0, next_ok = 0, ahead_ok = 0;
   if (t0 < t1) {
     pages.read(p, at, t0, 32, lane);
     ok = pages.rows(p, at, 0, t0, rows);
+    share.load_params(p.c, rows, wave, lane);
     share.load(p.c, rows, wave, lane);
+    share.store_params(params[0], wave, lane);
+    if (kValues && t0 + 32 < t1) {
+      next_ok = pages.rows(p, at, 1, t0 + 32, rows);
+      share.load_params(p.c, rows, wave, lane);
+    }
   }
   Queries<BITS, D, G, MT> q;
   q.place(p, at, row0, x);
@@ -142,31 +219,40 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : D == 64 ? 3 : 2) void kv_p
     q.take(m, mine, lane);
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   }
+  if (threadIdx.x < 3) bad[threadIdx.x] = 0;
   __syncthreads();  // the buffers are free
   Sums<BITS, D, G, MT> a;
   a.clear();
-  if (t0 < t1) share.store(buf[0], (uint32_t*)(buf[0] + kFrags), wave, lane);
+  if (t0 < t1) share.store(buf[0], params[0], bad, wave, lane);
+  if (kValues && t0 + 32 < t1) share.store_params(params[1], wave, lane);
   int at_buf = 0;
   for (int t = t0, s = 1; t < t1; t += 32, ++s) {
     __syncthreads();  // this tile is written, and the other buffer read
-    const bool more = t + 32 < t1;
-    if (more) {
-      if ((s & 31) == 0) pages.read(p, at, t + 32, 32, lane);
-      next_ok = pages.rows(p, at, s, t + 32, rows);
-      share.load(p.c, rows, wave, lane);
+    const bool more = t + 32 < t1, ahead = t + 32 * kAhead < t1;
+    const int now = (s - 1) % kRing, next = s % kRing, then = (s + kAhead - 1) % kRing;
+    if (kValues && threadIdx.x == 0) bad[then] = 0;
+    if (kValues && more) share.load(p.c, rows, wave, lane);
+    if (ahead) {
+      const int sa = s + kAhead - 1, ta = t + 32 * kAhead;
+      if ((sa & 31) == 0) pages.read(p, at, ta, 32, lane);
+      ahead_ok = pages.rows(p, at, sa, ta, rows);
+      if constexpr (!kValues) share.load(p.c, rows, wave, lane);
+      share.load_params(p.c, rows, wave, lane);
     }
     const uint8_t* read = buf[at_buf];
     if (t < own.end && t + 32 > own.begin) {
-      const FragKeys<G, NC> keys{read + lane * 16, read + kFrags + x * 4 * G + 2 * G};
-      FragValues values{read + 2 * NC * 1024 + lane * 16};
-      const uint8_t* params = read + kFrags + j * 16 * G;
-      tile_step<FINE>(q, a, t, ok, own.whole(t), j, keys, values, params, params + kParams / 2);
+      const FragKeys<G, NC> keys{read + lane * 16, (const uint8_t*)params[now] + x * 4 * G + 2 * G};
+      FragValues<kValues> values{read + 2 * NC * 1024 + lane * 16, bad + now};
+      const uint8_t* pj = (const uint8_t*)params[now] + j * 16 * G;
+      tile_step<FINE>(q, a, t, ok, own.whole(t), j, keys, values, pj, pj + kParams / 2);
     }
     at_buf ^= 1;
-    if (more) share.store(buf[at_buf], (uint32_t*)(buf[at_buf] + kFrags), wave, lane);
-    ok = next_ok;
+    if (more) share.store(buf[at_buf], params[next], bad + next, wave, lane);
+    if (ahead) share.store_params(params[then], wave, lane);
+    ok = kValues ? next_ok : ahead_ok;
+    next_ok = ahead_ok;
   }
-  a.close();
+  a.template close<kValues>();
 #pragma unroll
   for (int m = 0; m < MT; ++m)
     if (!idle) a.write(p, at, m, wave * kRows + 16 * m + x, q.out_row[m], j);

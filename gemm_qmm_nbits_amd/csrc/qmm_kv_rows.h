@@ -362,8 +362,10 @@ struct Sums {
   static constexpr int NV = D / 16;  // tiles of the second product's rows
   f32x4 O[MT][NV];
   float Oo[MT][G], ref[MT], limit[MT], l[MT];
+  uint32_t nan;  // products of values: bit G m + g where a row sees a value of group g that is not finite
 
   __device__ __forceinline__ void clear() {
+    nan = 0;
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
       ref[m] = 0.0f;
@@ -376,19 +378,27 @@ struct Sums {
     }
   }
 
-  // After the last tile: the offsets' part joins the sums, in the values' own units.
+  // After the last tile: the offsets' part joins the sums, in the values' own units.  VALUES: the products took
+  // values, not codes.
+  template <bool VALUES>
   __device__ __forceinline__ void close() {
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
       if (limit[m] != 15.0f) ref[m] = kLowest;
       l[m] = sum_over_j(l[m]);
 #pragma unroll
-      for (int g = 0; g < G; ++g) Oo[m][g] = sum_over_j(Oo[m][g]);
+      for (int g = 0; g < G; ++g) {
+        if constexpr (VALUES) Oo[m][g] = (nan >> (G * m + g)) & 1 ? __builtin_nanf("") : 0.0f;
+        Oo[m][g] = sum_over_j(Oo[m][g]);
+      }
 #pragma unroll
       for (int n = 0; n < NV; ++n)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          O[m][n][i] = fmaf(O[m][n][i], BITS == 4 && (n & 1) ? 0x1p20f : 0x1p24f, Oo[m][n * G / NV]);
+          if constexpr (VALUES)
+            O[m][n][i] += Oo[m][n * G / NV];
+          else
+            O[m][n][i] = fmaf(O[m][n][i], BITS == 4 && (n & 1) ? 0x1p20f : 0x1p24f, Oo[m][n * G / NV]);
     }
   }
 
@@ -435,7 +445,9 @@ struct Sums {
 
 // One tile of 32 tokens from t on.  keys.operand(hh, c), keys.offsets(hh): operands of the first product;
 // values.read(), values.operand(n): of the second; kp, vp: parameters of token 4 j in LDS.  ok: whether each
-// half has a page (bits 0, 1).  FINE: p s as two fp16 values.
+// half has a page (bits 0, 1).  FINE: p s as two fp16 values.  Values::kValues: the second product takes values
+// fp16(c s + o) with p alone as weights; values.bad() tells whether a parameter of the tile is not finite (its
+// values are 0 then).
 template <bool FINE, int BITS, int D, int G, int MT, typename Keys, typename Values>
 __device__ __forceinline__ void tile_step(const Queries<BITS, D, G, MT>& q, Sums<BITS, D, G, MT>& a, int t, int ok,
                                           bool whole, int j, const Keys& keys, Values& values, const uint8_t* kp,
@@ -472,12 +484,41 @@ __device__ __forceinline__ void tile_step(const Queries<BITS, D, G, MT>& q, Sums
     }
   }
 
+  constexpr bool kValues = Values::kValues;
+  auto sees = [&](int m, int e) {
+    const int tok = t + 16 * (e >> 2) + 4 * j + (e & 3);
+    return tok >= q.see_lo[m] && tok < q.see_hi[m] && ((ok >> (e >> 2)) & 1);
+  };
   Params<G> vs[2];
-  vs[0].load(vp);
-  vs[1].load(vp + 64 * G);
   float ve[MT];
   bool fixed = false;  // offsets are read, and their values that are not finite taken out
-  {
+  if constexpr (kValues) {
+    static_assert(MT <= 2);  // the bits of Sums::nan
+#pragma unroll
+    for (int m = 0; m < MT; ++m) ve[m] = 0.0f;
+    if (!(whole && ok == 3)) {
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) S[m][e >> 2][e & 3] = sees(m, e) ? S[m][e >> 2][e & 3] : -INFINITY;
+    }
+    if (__builtin_expect(values.bad(), 0)) {
+#pragma unroll 1
+      for (int e = 0; e < 8; ++e) {
+        uint32_t seen = 0;
+#pragma unroll
+        for (int m = 0; m < MT; ++m) seen |= sees(m, e) ? ((1u << G) - 1) << (G * m) : 0;
+        const uint16_t* at = (const uint16_t*)(vp + 64 * G * (e >> 2)) + 2 * G * (e & 3);
+#pragma unroll 1
+        for (int g = 0; g < G; ++g)
+          // (not finite, or beyond fp16 at the largest code)
+          if (!(fabsf(fmaf(half_of(at[g], 0), (1 << BITS) - 1, half_of(at[G + g], 0))) < 65520.0f))
+            a.nan |= seen & (((1u << G) + 1) << g);
+      }
+    }
+  } else {
+    vs[0].load(vp);
+    vs[1].load(vp + 64 * G);
     u16x2 mx = {0, 0};
 #pragma unroll
     for (int e = 0; e < 8; ++e)
@@ -486,7 +527,7 @@ __device__ __forceinline__ void tile_step(const Queries<BITS, D, G, MT>& q, Sums
 #pragma unroll
     for (int m = 0; m < MT; ++m) ve[m] = exponent_above(mx);
   }
-  if (!(whole && ok == 3)) {
+  if (!kValues && !(whole && ok == 3)) {
     uint32_t vis[MT];
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
@@ -494,8 +535,7 @@ __device__ __forceinline__ void tile_step(const Queries<BITS, D, G, MT>& q, Sums
       u16x2 mx = {0, 0};
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const int tok = t + 16 * (e >> 2) + 4 * j + (e & 3);
-        const bool see = tok >= q.see_lo[m] && tok < q.see_hi[m] && ((ok >> (e >> 2)) & 1);
+        const bool see = sees(m, e);
         vis[m] |= see ? 1u << e : 0u;
         S[m][e >> 2][e & 3] = see ? S[m][e >> 2][e & 3] : -INFINITY;
 #pragma unroll
@@ -562,8 +602,10 @@ __device__ __forceinline__ void tile_step(const Queries<BITS, D, G, MT>& q, Sums
       for (int n = 0; n < NV; ++n)
 #pragma unroll
         for (int i = 0; i < 4; ++i) a.O[m][n][i] *= al;
+      if constexpr (!kValues) {
 #pragma unroll
-      for (int g = 0; g < G; ++g) a.Oo[m][g] *= al;
+        for (int g = 0; g < G; ++g) a.Oo[m][g] *= al;
+      }
     }
   }
 
@@ -576,6 +618,15 @@ __device__ __forceinline__ void tile_step(const Queries<BITS, D, G, MT>& q, Sums
       pr[m][e] = __builtin_amdgcn_exp2f(S[m][e >> 2][e & 3]);
       a.l[m] += pr[m][e];
     }
+    if constexpr (kValues) {
+#pragma unroll
+      for (int e = 0; e < 8; e += 2) {
+        const f16x2 w = __builtin_convertvector((f32x2{pr[m][e], pr[m][e + 1]}), f16x2);
+        pb[m][0][e] = w[0];
+        pb[m][0][e + 1] = w[1];
+      }
+      continue;
+    }
 #pragma unroll
     for (int g = 0; g < G; ++g)
 #pragma unroll
@@ -585,22 +636,24 @@ __device__ __forceinline__ void tile_step(const Queries<BITS, D, G, MT>& q, Sums
         if constexpr (FINE) pl[m][g][e] = (_Float16)fmaf(pr[m][e], sc, -(float)pb[m][g][e]);
       }
   }
-  if (G > 2 && !fixed) {
-    vs[0].load_offsets();
-    vs[1].load_offsets();
+  if constexpr (!kValues) {
+    if (G > 2 && !fixed) {
+      vs[0].load_offsets();
+      vs[1].load_offsets();
+    }
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int g = 0; g < G; ++g)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) a.Oo[m][g] = fmaf(pr[m][e], vs[e >> 2].offset(e & 3, g), a.Oo[m][g]);
   }
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int g = 0; g < G; ++g)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) a.Oo[m][g] = fmaf(pr[m][e], vs[e >> 2].offset(e & 3, g), a.Oo[m][g]);
   values.read();
   // (two n at a time: a product and the next into the same sums lie apart)
 #pragma unroll
   for (int n = 0; n < NV; n += 2) {
     const f16x8 v0 = values.operand(n), v1 = values.operand(n + 1);
-    const int g = n * G / NV;
+    const int g = kValues ? 0 : n * G / NV;
 #pragma unroll
     for (int m = 0; m < MT; ++m) a.O[m][n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, pb[m][g], a.O[m][n], 0, 0, 0);
 #pragma unroll

@@ -109,6 +109,7 @@ struct TileKeys {
 template <int BITS, int D, int G>
 struct TileValues {
   typedef Format<BITS, D, G> F;
+  static constexpr bool kValues = false;
   uint32_t w[8][F::kValueWords];
   const uint8_t* at;
   __device__ __forceinline__ void read() {
@@ -202,7 +203,7 @@ __global__ __launch_bounds__(kThreads, waves_per_simd(BITS, D, MT)) void kv_toke
     step(s + 1, ring1, ok1, ring0, ok0);
   }
 
-  a.close();
+  a.template close<false>();
 #pragma unroll
   for (int m = 0; m < MT; ++m)
     if (j == 0) {

@@ -4,9 +4,9 @@ Bounds, with u = 2^-24 and everything taken from the oracle's magnitudes: a scor
 of exact operands, the scales' and the offsets' products (fp32 throughout), so it is off by dS <=
 gamma(D + 16) qk + 8 u qk + 100 u, qk the largest scale sum |q| (|c s| + |o|); the last terms are the score's
 roundings in units of log2 and its distance from the reference exponent (which lies within 40 of a score).
-A weight is off by 2 dS (its own and the sum's), the sums by gamma(seen + 64).  e^S s is rounded to fp16 once
-for bf16 results, half a step, 2^-11 of each term, and held by two fp16 values for fp16 ones, 2^-22; for terms
-below 2^-20 of the largest 2^-25 against a largest of at least 2^5 (2^-30), times the largest code and scale."""
+A weight is off by 2 dS (its own and the sum's), the sums by gamma(seen + 64).  For bf16 results either
+e^S s is rounded to fp16 once, half a step, 2^-11 of each term, or e^S and c s + o are, twice that (with their
+product 2^-10 + 2^-22); for fp16 ones e^S s is held by two fp16 values, 2^-22; for terms below 2^-20 of the largest 2^-25 against a largest of at least 2^5 (2^-30), times the largest code and scale."""
 import numpy as np
 import pytest
 
@@ -90,7 +90,7 @@ def check(p, label="", oracle=None, **kw):
     n = np.maximum(mag["seen"], 0)[:, None]
     dS = gamma(p.D + 16) * mag["qk"] + U32 * (8 * mag["qk"] + 100)
     step = float(p.cache["v_params"][:, :, :, 0].float().nan_to_num().max())
-    bound = mag["pv"] * ((2.0 ** -22 if p.ty == "f16" else 2.0 ** -11) + 2 * dS + gamma(n + 64.0))[..., None] + (n * 2.0 ** (p.bits - 30) * step)[..., None]
+    bound = mag["pv"] * ((2.0 ** -22 if p.ty == "f16" else 2.0 ** -10 + 2.0 ** -22) + 2 * dS + gamma(n + 64.0))[..., None] + (n * 2.0 ** (p.bits - 30) * step)[..., None]
     assert_elementwise(host_f64(out)[own], ref[own], bound[own], p.ty, label + " out")
     seen = np.isfinite(rl) & own[:, None]
     got = host_f64(lse)
@@ -302,6 +302,32 @@ def test_hidden_tokens_do_not_leak(new, kv):
     i = tok - first
     assert bool(t.isnan(out[i, :, 32:]).all()) and not bool(t.isnan(out[i, :, :32]).any())
     assert not bool(t.isnan(lse[i]).any())
+
+
+@pytest.mark.parametrize("bits,D,group", [(4, 64, 32), (8, 128, 32), (4, 256, 32), (4, 128, 64)])
+@pytest.mark.parametrize("ty", ["f16", "bf16"])
+@KERNELS
+def test_hidden_values_beyond_fp16(bits, D, group, ty, kv):
+    """Finite parameters whose values pass fp16's range, in slots that no row sees, change no bit; great
+    ones that rows see are within the bound."""
+    t = torch()
+    p = Problem([100, 77], [70, 60], bits=bits, D=D, group=group, page=16, ty=ty, seed=16)
+    clean = [host_bits(x).copy() for x in p.call(max_kv=kv)]
+    used = np.zeros((p.cache["k"].shape[0], 16), bool)
+    for b, n in enumerate(p.lens):
+        used[p.table_h[b, np.arange(n) // 16], np.arange(n) % 16] = True
+    hide = t.from_numpy(~used).cuda()
+    p.cache["v"].permute(0, 2, 1, 3)[hide] = 255
+    p.cache["v_params"].permute(0, 2, 1, 3, 4)[hide] = 60000.0
+    got = [host_bits(x) for x in p.call(max_kv=kv)]
+    assert all(np.array_equal(a, b) for a, b in zip(got, clean))
+    # offsets up to 2^15 and scales up to 2^15 / 2^bits: a value stays below 2^16 - 2^15 / 2^bits
+    p.cache["v_params"][:, :, :, 0] = 2.0 ** (15 - bits)
+    p.cache["v_params"][:, :, :, 1] = -(2.0 ** 15)
+    p.cache["v_params"][:, :, ::2, 1] = 2.0 ** 14
+    if ty == "bf16":  # (fp16 results would hold them too, but a sum's bound passes their range)
+        check(p, "great values", max_kv=kv)
+    t.cuda.synchronize()
 
 
 def test_pages_outside_the_pool():
