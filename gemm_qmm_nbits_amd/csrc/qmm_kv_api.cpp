@@ -17,6 +17,7 @@ size_t type_size(int t) { return t == QMM_F32 ? 4 : 2; }
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
 constexpr int64_t kMaxTokens = 1LL << 24;
+constexpr int64_t kMaxStored = 1LL << 20;  // each work-group reads all later slots: work grows with the square
 constexpr int64_t kMaxStride = 1LL << 40;
 // work-groups of 256 threads in one launch: fewer than 2^32 threads
 constexpr int64_t kMaxGroups = (1LL << 24) - 1;
@@ -48,6 +49,7 @@ qmm_status check_store(const void* K, int64_t krs, int64_t khs, const void* V, i
   if (s != QMM_OK) return s;
   if (!valid_type(type)) return QMM_E_DTYPE;
   if ((s = check_tokens(T, c)) != QMM_OK) return s;
+  if (T > kMaxStored) return QMM_E_SHAPE;
   if (!valid_stride(krs) || !valid_stride(khs) || !valid_stride(vrs) || !valid_stride(vhs)) return QMM_E_SHAPE;
   if (T == 0) return QMM_OK;
   if (!K || !V || !slots) return QMM_E_NULL;

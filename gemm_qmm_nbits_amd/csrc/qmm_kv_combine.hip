@@ -138,6 +138,7 @@ KvPlan kv_plan(int q_heads, int heads, int D, int64_t B, int64_t max_q, int64_t 
   // sooner: 4 waves share a row tile's tokens, and there are four times as many work-groups.  The first where
   // there is work enough (32 heads on 8, 128 dimensions, one sequence: 512 of 512 tokens 33 against 21 us, 1024 of
   // 1024 37 and 45, 512 of 8192 139 and 182).
+  // (a sequence with fewer queries than max_q leaves work-groups without rows; they end at once.)
   k.by_rows = rows > 64 && rows * heads * B >= (1ll << 26) / std::max<int64_t>(max_kv, 1);
   k.mt = rows <= 16 ? 1 : 2;
   const int64_t per = rows_of(k);
@@ -150,14 +151,18 @@ KvPlan kv_plan(int q_heads, int heads, int D, int64_t B, int64_t max_q, int64_t 
   int64_t splits;
   const int64_t room = D == 256 ? 256 : 512;  // work-groups at once: two to a compute unit, or one
   if (k.by_rows) {
-    // whole rounds of work-groups; what is left over would take a
-    // round of its own and is split as far as that round has room
+    // whole rounds of work-groups; what is left over would take a round of its own and is split as far as
+    // that round has room (640 work-groups: 662 us, 571 with the last 128 in four parts each)
     k.whole = k.groups / room * room;
     const int64_t left = k.groups - k.whole;
-    // (not where the last row tiles see few tokens anyway: a prompt from its first token on)
+    // (not where the last row tiles see few tokens anyway, a prompt from its first token on: 2048 of 2048
+    // tokens 111 us, 148 split)
     splits = left > 0 && (k.whole == 0 || max_kv >= 2 * max_q) ? std::min(room / left, over(max_kv, 512)) : 1;
   } else {
-    // one round of work-groups, with 256 tokens at least, or more where there is more work
+    // one round of work-groups, with 256 tokens at least, or more where there is more work: up to 3072 with
+    // 2048 tokens at least, so that sequences of other lengths spread over the chip (10 cache heads, unsplit and
+    // split: 32 sequences of 8 to 8191 tokens 112 and 71 us, 64 of 8 to 16 k 250 and 222; 64 of 4 to 8 k, 8 heads, 8
+    // bits 157.5 and 157.2)
     splits = std::max(std::min(std::max<int64_t>(room / k.groups, 1), over(max_kv, 256)),
                       std::min(over(3072, k.groups), over(max_kv, 2048)));
   }

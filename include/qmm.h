@@ -561,11 +561,12 @@ qmm_status qmm_validate_lora_grad(const void* dY, const void* X, int type, int64
  *   K, V    [T][heads][D] of `type` (any of the three types), element (t, h, d) at
  *           t * row_stride + h * head_stride + d (strides in elements, >= 0).  Rows that are 16-byte
  *           aligned are the fastest.
- *   slots   int32 [T] (device).  A slot outside the pool: the token is not stored.  Of several tokens
- *           with one slot the last is stored.
+ *   slots   int32 [T] (device), T <= 2^20.  A slot outside the pool: the token is not stored.  Of several
+ *           tokens with one slot the last is stored.
  *
  * qkv_cache_load -- the values of T slots: K, V dense [T][heads][D] of `type`, fp32(c * s + o) rounded
- *   to it; zeros for a slot outside the pool.  K or V may be NULL (not read).
+ *   to it; zeros for a slot outside the pool.  K or V may be NULL (not read).  T <= 2^24.  In both calls
+ *   T * heads <= 2^26.
  *
  * qkv_attention -- for query i of sequence b (n of them, the last n of its kv_len[b] tokens, so at
  * position p = kv_len[b] - n + i) and head a, over the tokens t of the sequence that it sees:
@@ -583,15 +584,21 @@ qmm_status qmm_validate_lora_grad(const void* dY, const void* X, int type, int64
  *   kv_len  int32 [B] (device), clamped into [0, table_width * page].
  *   table   int32 [B][table_width] (device): pages of each sequence; one outside the pool is not seen.
  *   max_q   the greatest number of queries of a sequence (1 when cu_q is NULL); sets the grid.
- *   max_kv  the greatest kv_len expected: only how the work is split depends on it (0: the table's).
+ *   max_kv  the greatest kv_len expected (0: table_width * page, the most there can be): how the work is
+ *           split depends on it, and the order of the sums; longer sequences are right all the same.
  *   sinks   fp32 [q_heads] (device) or NULL (none).  window 0: none.
  *   Codes enter the products as they are and scales are applied in fp32: S and lse carry fp32 sums'
- *   errors; e^(S_t) s is rounded to fp16 (relative 2^-11, of its largest down to 2^-30) for the
- *   second product.  Queries are scaled by a power of two per row to fp16: exact down to 2^-31 of the
- *   row's largest element.  A query with a NaN or an infinity (or elements past 2^100) gives NaN.
- *   B <= 65535, T <= 2^24, q_heads <= 4096 a multiple of heads with q_heads / heads <= 512.
- *   workspace: at least qkv_attention_workspace_bytes, 256-byte aligned; calls that share one must not
- *   overlap.  The sums' order depends on the sizes, max_q, max_kv and the lengths only.
+ *   errors.  For the second product e^(S_t) s is rounded to fp16 (relative 2^-11, of its largest down to
+ *   2^-30) for bf16 results and is held by two fp16 values (2^-22) for fp16 ones; with many rows, groups of
+ *   32 and bf16 results e^(S_t) and c * s + o are rounded to fp16 instead.  There a value beyond fp16's
+ *   range (the store writes none) counts as NaN where a row sees it.
+ *   Queries are scaled by a power of two per row to fp16: exact down to 2^-31 of the row's largest element.
+ *   A query with a NaN or an infinity (or elements past 2^100) gives NaN.
+ *   B <= 65535, T <= 2^24, q_heads <= 4096 a multiple of heads with q_heads / heads <= 512, max_q *
+ *   q_heads / heads < 2^31; QMM_E_SHAPE also where max_q, heads and B ask for 2^24 work-groups or more.
+ *   workspace: at least qkv_attention_workspace_bytes (max_kv as in the call, table_width * page for 0; no
+ *   workspace where that is 0), 256-byte aligned; calls that share one must not overlap.  The order of the
+ *   sums depends on the sizes, max_q, max_kv, the window and the lengths only: equal calls give equal bits.
  * ------------------------------------------------------------------------- */
 typedef struct {
   uint8_t* k;

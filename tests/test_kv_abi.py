@@ -65,6 +65,7 @@ def test_token_refusals(f):
 
 
 def test_store_refusals():
+    assert store(T=1 << 20) == 0 and store(T=(1 << 20) + 1) == -5 and load(T=(1 << 20) + 1) == 0
     assert store(K=None) == -1 and store(V=None) == -1
     assert store(K=FAKE + 1) == -6 and store(K=FAKE + 2) == 0 and store(V=FAKE + 2, type=Q.QMM_F32) == -6
     for k in ("krs", "khs", "vrs", "vhs"):
