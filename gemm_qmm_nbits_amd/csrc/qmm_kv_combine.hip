@@ -159,12 +159,12 @@ KvPlan kv_plan(int q_heads, int heads, int D, int64_t B, int64_t max_q, int64_t 
     // tokens 111 us, 148 split)
     splits = left > 0 && (k.whole == 0 || max_kv >= 2 * max_q) ? std::min(room / left, over(max_kv, 512)) : 1;
   } else {
-    // one round of work-groups, with 256 tokens at least, or more where there is more work: up to 3072 with
+    // one round of work-groups, with 256 tokens at least, or more where there is more work: up to 3200 with
     // 2048 tokens at least, so that sequences of other lengths spread over the chip (10 cache heads, unsplit and
     // split: 32 sequences of 8 to 8191 tokens 112 and 71 us, 64 of 8 to 16 k 250 and 222; 64 of 4 to 8 k, 8 heads, 8
     // bits 157.5 and 157.2)
     splits = std::max(std::min(std::max<int64_t>(room / k.groups, 1), over(max_kv, 256)),
-                      std::min(over(3072, k.groups), over(max_kv, 2048)));
+                      std::min(over(3200, k.groups), over(max_kv, 2048)));
   }
   k.splits = (int)std::min<int64_t>(std::max<int64_t>(splits, 1), kMaxParts);
   if (k.splits == 1) k.whole = k.groups;

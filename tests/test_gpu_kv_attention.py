@@ -6,7 +6,8 @@ gamma(D + 16) qk + 8 u qk + 100 u, qk the largest scale sum |q| (|c s| + |o|); t
 roundings in units of log2 and its distance from the reference exponent (which lies within 40 of a score).
 A weight is off by 2 dS (its own and the sum's), the sums by gamma(seen + 64).  For bf16 results either
 e^S s is rounded to fp16 once, half a step, 2^-11 of each term, or e^S and c s + o are, twice that (with their
-product 2^-10 + 2^-22); for fp16 ones e^S s is held by two fp16 values, 2^-22; for terms below 2^-20 of the largest 2^-25 against a largest of at least 2^5 (2^-30), times the largest code and scale."""
+product 2^-10 + 2^-22); for fp16 ones e^S s is held by two fp16 values, 2^-22; for terms
+below 2^-20 of the largest 2^-25 against a largest of at least 2^5 (2^-30), times the largest code and scale."""
 import numpy as np
 import pytest
 
@@ -90,7 +91,8 @@ def check(p, label="", oracle=None, **kw):
     n = np.maximum(mag["seen"], 0)[:, None]
     dS = gamma(p.D + 16) * mag["qk"] + U32 * (8 * mag["qk"] + 100)
     step = float(p.cache["v_params"][:, :, :, 0].float().nan_to_num().max())
-    bound = mag["pv"] * ((2.0 ** -22 if p.ty == "f16" else 2.0 ** -10 + 2.0 ** -22) + 2 * dS + gamma(n + 64.0))[..., None] + (n * 2.0 ** (p.bits - 30) * step)[..., None]
+    weights = 2.0 ** -22 if p.ty == "f16" else 2.0 ** -10 + 2.0 ** -22
+    bound = mag["pv"] * (weights + 2 * dS + gamma(n + 64.0))[..., None] + (n * 2.0 ** (p.bits - 30) * step)[..., None]
     assert_elementwise(host_f64(out)[own], ref[own], bound[own], p.ty, label + " out")
     seen = np.isfinite(rl) & own[:, None]
     got = host_f64(lse)
