@@ -149,7 +149,9 @@ KvPlan kv_plan(int q_heads, int heads, int D, int64_t B, int64_t max_q, int64_t 
   if (window > 0 && window < max_kv) max_kv = std::min(max_kv, window + std::min(max_q, (per - 1) / (q_heads / heads) + 2));
   auto over = [](int64_t n, int64_t d) { return (n + d - 1) / d; };
   int64_t splits;
-  const int64_t room = D == 256 ? 256 : 512;  // work-groups at once: two to a compute unit, or one
+  // work-groups at once: two to a compute unit; one; three (2048 queries at 8192 tokens, 64 heads of 64 on 8: 528 us, 554
+  // with 512)
+  const int64_t room = D == 256 ? 256 : D == 64 && k.by_rows ? 768 : 512;
   if (k.by_rows) {
     // whole rounds of work-groups; what is left over would take a round of its own and is split as far as
     // that round has room (640 work-groups: 662 us, 571 with the last 128 in four parts each)
@@ -157,7 +159,15 @@ KvPlan kv_plan(int q_heads, int heads, int D, int64_t B, int64_t max_q, int64_t 
     const int64_t left = k.groups - k.whole;
     // (not where the last row tiles see few tokens anyway, a prompt from its first token on: 2048 of 2048
     // tokens 111 us, 148 split)
-    splits = left > 0 && (k.whole == 0 || max_kv >= 2 * max_q) ? std::min(room / left, over(max_kv, 512)) : 1;
+    splits = 1;
+    if (left > 0 && (k.whole == 0 || max_kv >= 2 * max_q)) {
+      const int64_t most = over(max_kv, 512);
+      splits = std::max<int64_t>(std::min(room / left, most), 1);
+      // (where that is less than 8: parts that fill more of several rounds.  320 work-groups, 1024 of 16384 tokens: 811
+      // us, in eight parts each 582 with the join.)
+      for (int64_t s = splits + 1; s <= std::min<int64_t>(8, most); ++s)
+        if (20 * over(left * s, room) * splits < 19 * over(left * splits, room) * s) splits = s;
+    }
   } else {
     // one round of work-groups, with 256 tokens at least, or more where there is more work: up to 3200 with
     // 2048 tokens at least, so that sequences of other lengths spread over the chip (10 cache heads, unsplit and

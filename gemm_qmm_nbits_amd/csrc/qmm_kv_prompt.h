@@ -7,7 +7,7 @@
 // per lane.  Two buffers: while the waves work on one tile the words of the next are on their way to
 // registers, and are written to the other buffer at the end; one barrier per tile.
 //
-// 2048 queries at 8192 tokens, 40 heads of 128 dimensions on 10, 4 bits, groups of 64: 540 us, 556 TFLOP/s (each wave
+// 2048 queries at 8192 tokens, 40 heads of 128 dimensions on 10, 4 bits, groups of 64: 498 us, 604 TFLOP/s (each wave
 // its own operands: 1020).  Bound by vector instructions beside the matrix ones, 260 per wave and tile to 36,
 // and by what two waves per SIMD leave open: 32 rows' sums and queries fill a wave's registers (64 rows a wave spill:
 // 937 against 636 us in an earlier form).  Operands read further ahead, and the next tile's stores put among the
@@ -162,9 +162,12 @@ struct FragKeys {
   }
 };
 
-template <bool VALUES>
+template <bool VALUES, bool FIRST>
 struct FragValues {
   static constexpr bool kValues = VALUES;
+  __device__ __forceinline__ void scored() {
+    if constexpr (FIRST) __builtin_amdgcn_s_setprio(0);
+  }
   const uint8_t* frags;
   const int* flag;
   __device__ __forceinline__ bool bad() const { return __builtin_amdgcn_readfirstlane(*flag) != 0; }
@@ -178,6 +181,10 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : D == 64 ? 3 : 2) void kv_p
   constexpr int NC = D / 32, NV = D / 16, MT = kPromptTiles, kRows = 16 * MT;
   constexpr int kFrags = (2 * NC + NV) * 1024, kParams = 2 * 32 * 4 * G;
   constexpr bool kValues = !FINE && G == NC;
+  // Of the two waves of a SIMD the one that makes scores goes first, so that one's matrix instructions meet the
+  // other's vector ones: 2048 queries at 8192 tokens 540 -> 498 us, 512 at 4096 of eight sequences 492 -> 430, 2048
+  // at 2048 of one 104 -> 109.  With three waves (64 dimensions) it costs: 549 -> 600; with one (256) 819 -> 829.
+  constexpr bool kFirst = D == 128;
   constexpr int kAhead = kValues ? 2 : 1, kRing = kAhead + 1;  // tiles that parameters come ahead (codes: one)
   __shared__ __attribute__((aligned(1024))) uint8_t buf[2][kFrags];
   __shared__ __attribute__((aligned(16))) uint32_t params[kRing][kParams / 4];  // of tile s: s % kRing
@@ -249,8 +256,9 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : D == 64 ? 3 : 2) void kv_p
     const uint8_t* read = buf[at_buf];
     if (t < own.end && t + 32 > own.begin) {
       const FragKeys<G, NC> keys{read + lane * 16, (const uint8_t*)params[now] + x * 4 * G + 2 * G};
-      FragValues<kValues> values{read + 2 * NC * 1024 + lane * 16, bad + now};
+      FragValues<kValues, kFirst> values{read + 2 * NC * 1024 + lane * 16, bad + now};
       const uint8_t* pj = (const uint8_t*)params[now] + j * 16 * G;
+      if constexpr (kFirst) __builtin_amdgcn_s_setprio(1);
       tile_step<FINE>(q, a, t, ok, own.whole(t), j, keys, values, pj, pj + kParams / 2);
     }
     at_buf ^= 1;

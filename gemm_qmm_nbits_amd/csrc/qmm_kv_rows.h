@@ -444,7 +444,7 @@ struct Sums {
 };
 
 // One tile of 32 tokens from t on.  keys.operand(hh, c), keys.offsets(hh): operands of the first product;
-// values.read(), values.operand(n): of the second; kp, vp: parameters of token 4 j in LDS.  ok: whether each
+// values.scored(): the scores are there; values.read(), values.operand(n): of the second; kp, vp: parameters of token 4 j in LDS.  ok: whether each
 // half has a page (bits 0, 1).  FINE: p s as two fp16 values.  Values::kValues: the second product takes values
 // fp16(c s + o) with p alone as weights; values.bad() tells whether a parameter of the tile is not finite (its
 // values are 0 then).
@@ -609,6 +609,7 @@ __device__ __forceinline__ void tile_step(const Queries<BITS, D, G, MT>& q, Sums
     }
   }
 
+  values.scored();
   f16x8 pb[MT][G], pl[FINE ? MT : 1][FINE ? G : 1];
   float pr[MT][8];
 #pragma unroll

@@ -116,6 +116,7 @@ template <int BITS, int D, int G>
 struct TileValues {
   typedef Format<BITS, D, G> F;
   static constexpr bool kValues = false;
+  __device__ __forceinline__ void scored() {}
   uint32_t w[8][F::kValueWords];
   const uint8_t* at;
   __device__ __forceinline__ void read() {
