@@ -13,7 +13,7 @@
 // The keys' offsets enter as one product of their own: o_tg against the group sums of q, which three fp16
 // pieces hold to 33 bits (one in each of the contraction's first three quarters).
 //
-// p = 2^(s - R): R, the row's reference, is kept such that p times the largest value scale stays below
+// p = 2^(s - R): R, the row's reference, is kept such that p times the largest value scale's magnitude stays below
 // 2^15 (p s is rounded to fp16) and is raised when a tile would exceed that, to put it at 2^7; the sums are
 // then scaled down.  No other lane is asked for its maximum unless that happens.  p s enters as one fp16
 // value (relative 2^-11) for bf16 results and as two (2^-22) for fp16 ones.
@@ -119,15 +119,21 @@ struct Params {
   }
   __device__ __forceinline__ float scale(int i, int g) const { return half_of(s[i][g / 2], g & 1); }
   __device__ __forceinline__ float offset(int i, int g) const { return half_of(o[i][g / 2], g & 1); }
-  // the scales' bits of token i, as pairs
-  __device__ __forceinline__ u16x2 scale_bits(int i, int q) const {
-    return __builtin_bit_cast(u16x2, G == 1 ? s[i][0] & 0xffffu : s[i][q]);
-  }
 };
 
-// An upper bound of log2 of the largest of scales (not negative) whose bits' maximum is m.
-__device__ __forceinline__ float exponent_above(u16x2 m) {
-  const uint32_t v = max((uint32_t)m[0], (uint32_t)m[1]);
+// Raises m to the magnitudes of a pair of fp16 numbers, NaN above all.  (One instruction.  In inline
+// assembly it costs registers that spill: 64 sequences of 8 to 16 k tokens, groups of 64, 216 -> 238 us, of 4 to 8 k,
+// groups of 32, 154 -> 223.)
+__device__ __forceinline__ void raise_to(f16x2& m, uint32_t pair) {
+  const f16x2 x = __builtin_bit_cast(f16x2, pair);
+  m = __builtin_elementwise_maximum(__builtin_elementwise_maximum(m, x), -x);
+}
+
+// An upper bound of log2 of the scales' magnitudes whose maximum is m (G = 1: its low half).
+template <int G>
+__device__ __forceinline__ float exponent_above(f16x2 m) {
+  const u16x2 b = __builtin_bit_cast(u16x2, m);
+  const uint32_t v = G == 1 ? (uint32_t)b[0] : max((uint32_t)b[0], (uint32_t)b[1]);
   return (float)((int)max((v >> 10) & 31u, 1u) - 14);
 }
 
@@ -519,32 +525,29 @@ __device__ __forceinline__ void tile_step(const Queries<BITS, D, G, MT>& q, Sums
   } else {
     vs[0].load(vp);
     vs[1].load(vp + 64 * G);
-    u16x2 mx = {0, 0};
+    f16x2 mx = {0, 0};
 #pragma unroll
     for (int e = 0; e < 8; ++e)
 #pragma unroll
-      for (int w = 0; w < Params<G>::kWords; ++w) mx = __builtin_elementwise_max(mx, vs[e >> 2].scale_bits(e & 3, w));
+      for (int w = 0; w < Params<G>::kWords; ++w) raise_to(mx, vs[e >> 2].s[e & 3][w]);
 #pragma unroll
-    for (int m = 0; m < MT; ++m) ve[m] = exponent_above(mx);
+    for (int m = 0; m < MT; ++m) ve[m] = exponent_above<G>(mx);
   }
   if (!kValues && !(whole && ok == 3)) {
     uint32_t vis[MT];
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
       vis[m] = 0;
-      u16x2 mx = {0, 0};
+      f16x2 mx = {0, 0};
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const bool see = sees(m, e);
         vis[m] |= see ? 1u << e : 0u;
         S[m][e >> 2][e & 3] = see ? S[m][e >> 2][e & 3] : -INFINITY;
 #pragma unroll
-        for (int w = 0; w < Params<G>::kWords; ++w) {
-          const u16x2 bits = vs[e >> 2].scale_bits(e & 3, w);
-          mx = see ? __builtin_elementwise_max(mx, bits) : mx;
-        }
+        for (int w = 0; w < Params<G>::kWords; ++w) raise_to(mx, see ? vs[e >> 2].s[e & 3][w] : 0u);
       }
-      ve[m] = exponent_above(mx);
+      ve[m] = exponent_above<G>(mx);
     }
     // a parameter that is not finite has all exponent bits set
     vs[0].load_offsets();

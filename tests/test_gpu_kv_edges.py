@@ -1,0 +1,64 @@
+"""GPU parity of attention over the low-bit cache at its edges: scales of either sign, hidden tokens next to great
+values, queries of a wide range, rows that are NaN, the widest windows; against the fp64 oracle.
+
+Bounds as in test_gpu_kv_attention.py: with u = 2^-24 a score is off by dS <= gamma(D + 16) qk + 8 u qk + 100 u, a
+weight by 2 dS, the sums by gamma(seen + 64).  Roundings to fp16, half a step each, 2^-11: none for fp16 results (two
+fp16 values hold a weight, 2^-22), one for bf16 ones (e^S s), two where many rows meet groups of 32 (e^S and c s + o,
+with their product 2^-10 + 2^-22); for terms below 2^-20 of the largest weight times the largest scale 2^-30 of that,
+times the largest code."""
+import numpy as np
+import pytest
+
+from gemm_qmm_nbits_amd import qmm as Q
+from oracle import kv_oracle as KO
+
+from gpu_util import U32, assert_elementwise, gamma, host_bits, host_f64, say, torch
+from test_gpu_kv_attention import MUCH, Problem
+
+pytestmark = pytest.mark.gpu
+
+# queries per sequence, tokens expected, whether the call takes the kernel for many rows
+CALLS = pytest.mark.parametrize("new,kv,many", [(1, None, False), (70, None, False), (70, MUCH, True)],
+                                ids=["one", "few", "many"])
+
+
+def check(p, many, label="", **kw):
+    """One call against the oracle; returns (out, lse).  many: it takes the kernel for many rows."""
+    group = p.cache["group"]
+    say(f"  {label} lens={p.lens} news={p.news} heads={p.heads}/{p.kv} D={p.D} bits={p.bits} group={group} {p.ty} "
+        f"many={many} {sorted(kw)}")
+    out, lse = p.call(**kw)
+    ref, rl, mag = KO.attention(host_f64(p.Q), p.host_cache(), p.table_h, p.lens, cu_q=p.cu_h,
+                                scale=kw.get("scale"), window=kw.get("window", 0),
+                                sinks=None if kw.get("sinks") is None else host_f64(kw["sinks"]))
+    own = mag["seen"] >= 0
+    n = np.maximum(mag["seen"], 0)[:, None]
+    dS = gamma(p.D + 16) * mag["qk"] + U32 * (8 * mag["qk"] + 100)
+    step = float(p.cache["v_params"][:, :, :, 0].float().abs().nan_to_num().max())
+    weights = 2.0 ** -22 if p.ty == "f16" else 2.0 ** -10 + 2.0 ** -22 if many and group == 32 else 2.0 ** -11
+    bound = mag["pv"] * (weights + 2 * dS + gamma(n + 64.0))[..., None] + (n * 2.0 ** (p.bits - 30) * step)[..., None]
+    assert_elementwise(host_f64(out)[own], ref[own], bound[own], p.ty, label + " out")
+    seen = np.isfinite(rl) & own[:, None]
+    got = host_f64(lse)
+    assert np.array_equal(np.isneginf(got[own]), np.isneginf(rl[own]))
+    lim = 2 * dS + gamma(n + 64.0) + 2.0 ** -22 * (np.abs(np.where(np.isfinite(rl), rl, 0.0)) + 40)
+    worst = np.abs(got[seen] - rl[seen]) / np.broadcast_to(lim, got.shape)[seen]
+    assert worst.size == 0 or worst.max() <= 1.0, (label, "lse", worst.max())
+    return out, lse
+
+
+@pytest.mark.parametrize("bits,D,group", [(4, 64, 32), (8, 64, 64), (4, 128, 32), (4, 128, 64), (8, 128, 128),
+                                          (4, 256, 64), (8, 256, 32)])
+@pytest.mark.parametrize("ty", ["f16", "bf16"])
+@CALLS
+def test_scales_of_either_sign(bits, D, group, ty, new, kv, many):
+    """A code stands for c s + o whatever the sign of s: small negative scales (and -0.0) beside large positive ones
+    and the reverse, in one token and in one tile."""
+    t = torch()
+    p = Problem([100, 77], [new, new], D=D, bits=bits, group=group, ty=ty, seed=D + bits + new)
+    rng = np.random.default_rng(D + group)
+    shape = p.cache["v_params"][:, :, :, 0].shape
+    for choice in ([1.0, -0.001], [-1.0, 0.001], [1.0, -0.0], [-1.0, 0.001, -0.001, 1.0, -0.0, 0.0]):
+        p.cache["v_params"][:, :, :, 0] = t.from_numpy(rng.choice(choice, shape)).half().cuda()
+        p.cache["k_params"][:, :, :, 0] *= t.from_numpy(rng.choice([1.0, -1.0], shape)).half().cuda()
+        check(p, many, f"scales {choice}", max_kv=kv)
