@@ -86,9 +86,10 @@ struct Share {
     }
   }
 
-  // frags: 2 NC key operands, then NV value operands, 1 KiB each.  VALUES: params: the tile's, in LDS; bad: set
-  // where one of values is not finite
-  __device__ __forceinline__ void store(uint8_t* frags, const uint32_t* params, int* bad, int wave, int lane) const {
+  // frags: 2 NC key operands, then NV value operands, 1 KiB each.  VALUES: params: the tile's, in LDS; bad: its
+  // tokens' groups with values that are not finite, and whether there are any
+  __device__ __forceinline__ void store(uint8_t* frags, const uint32_t* params, uint32_t* bad, int wave,
+                                        int lane) const {
     const int x = lane & 15, q = lane >> 4;
 #pragma unroll
     for (int i = 0; i < NC / 2; ++i)
@@ -127,7 +128,21 @@ struct Share {
           r[i][t] = __builtin_bit_cast(uint32_t, y);
         }
       if (__builtin_expect(__builtin_amdgcn_ballot_w64(z[0] != z[0] || z[1] != z[1]) != 0, 0)) {
-        *bad = 1;
+        bad[32] = 1;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) to[i * 64] = r[i];
+        // (from LDS in a loop: over registers, unrolled, it spills hundreds of them at 256 dimensions)
+#pragma unroll 1
+        for (int i = 0; i < kPer; ++i) {
+          const u32x4 y = to[i * 64];
+#pragma unroll
+          for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+              if (((y[t] >> (16 * half)) & 0x7c00u) == 0x7c00u)
+                // token 2 t + half of the 8 of quarter `wave`; a group is two tiles of dimensions
+                atomicOr(bad + 16 * (t >> 1) + 4 * wave + 2 * (t & 1) + half, 1u << ((q * kPer + i) / 2));
+        }
 #pragma unroll
         for (int i = 0; i < kPer; ++i)
 #pragma unroll
@@ -169,8 +184,9 @@ struct FragValues {
     if constexpr (FIRST) __builtin_amdgcn_s_setprio(0);
   }
   const uint8_t* frags;
-  const int* flag;
-  __device__ __forceinline__ bool bad() const { return __builtin_amdgcn_readfirstlane(*flag) != 0; }
+  const uint32_t* flags;  // of tokens, of all
+  __device__ __forceinline__ bool bad() const { return __builtin_amdgcn_readfirstlane(flags[32]) != 0; }
+  __device__ __forceinline__ uint32_t bad_groups(int token) const { return flags[token]; }
   __device__ __forceinline__ void read() {}
   __device__ __forceinline__ f16x8 operand(int n) const { return *(const f16x8*)(frags + n * 1024); }
 };
@@ -188,7 +204,8 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : D == 64 ? 3 : 2) void kv_p
   constexpr int kAhead = kValues ? 2 : 1, kRing = kAhead + 1;  // tiles that parameters come ahead (codes: one)
   __shared__ __attribute__((aligned(1024))) uint8_t buf[2][kFrags];
   __shared__ __attribute__((aligned(16))) uint32_t params[kRing][kParams / 4];  // of tile s: s % kRing
-  __shared__ int bad[3];  // of tile s: bad[s % 3], cleared two tiles ahead
+  // of tile s: bad[s % 3], cleared two tiles ahead: tokens' groups, then whether there are any (words to a whole wave)
+  __shared__ uint32_t bad[3][64];
 
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int lane = threadIdx.x & 63, x = lane & 15, j = lane >> 4;
@@ -233,18 +250,18 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : D == 64 ? 3 : 2) void kv_p
     q.take(m, mine, lane);
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   }
-  if (threadIdx.x < 3) bad[threadIdx.x] = 0;
+  if (wave < 3) bad[wave][lane] = 0;
   __syncthreads();  // the buffers are free
   Sums<BITS, D, G, MT> a;
   a.clear();
-  if (t0 < t1) share.store(buf[0], params[0], bad, wave, lane);
+  if (t0 < t1) share.store(buf[0], params[0], bad[0], wave, lane);
   if (kValues && t0 + 32 < t1) share.store_params(params[1], wave, lane);
   int at_buf = 0;
   for (int t = t0, s = 1; t < t1; t += 32, ++s) {
     __syncthreads();  // this tile is written, and the other buffer read
     const bool more = t + 32 < t1, ahead = t + 32 * kAhead < t1;
     const int now = (s - 1) % kRing, next = s % kRing, then = (s + kAhead - 1) % kRing;
-    if (kValues && threadIdx.x == 0) bad[then] = 0;
+    if (kValues && wave == 0) bad[then][lane] = 0;
     if (kValues && more) share.load(p.c, rows, wave, lane);
     if (ahead) {
       const int sa = s + kAhead - 1, ta = t + 32 * kAhead;
@@ -256,13 +273,13 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : D == 64 ? 3 : 2) void kv_p
     const uint8_t* read = buf[at_buf];
     if (t < own.end && t + 32 > own.begin) {
       const FragKeys<G, NC> keys{read + lane * 16, (const uint8_t*)params[now] + x * 4 * G + 2 * G};
-      FragValues<kValues, kFirst> values{read + 2 * NC * 1024 + lane * 16, bad + now};
+      FragValues<kValues, kFirst> values{read + 2 * NC * 1024 + lane * 16, bad[now]};
       const uint8_t* pj = (const uint8_t*)params[now] + j * 16 * G;
       if constexpr (kFirst) __builtin_amdgcn_s_setprio(1);
       tile_step<FINE>(q, a, t, ok, own.whole(t), j, keys, values, pj, pj + kParams / 2);
     }
     at_buf ^= 1;
-    if (more) share.store(buf[at_buf], params[next], bad + next, wave, lane);
+    if (more) share.store(buf[at_buf], params[next], bad[next], wave, lane);
     if (ahead) share.store_params(params[then], wave, lane);
     ok = kValues ? next_ok : ahead_ok;
     next_ok = ahead_ok;

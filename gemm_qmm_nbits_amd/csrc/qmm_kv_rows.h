@@ -452,8 +452,8 @@ struct Sums {
 // One tile of 32 tokens from t on.  keys.operand(hh, c), keys.offsets(hh): operands of the first product;
 // values.scored(): the scores are there; values.read(), values.operand(n): of the second; kp, vp: parameters of token 4 j in LDS.  ok: whether each
 // half has a page (bits 0, 1).  FINE: p s as two fp16 values.  Values::kValues: the second product takes values
-// fp16(c s + o) with p alone as weights; values.bad() tells whether a parameter of the tile is not finite (its
-// values are 0 then).
+// fp16(c s + o) with p alone as weights; values.bad() tells whether the tile holds values that are not finite (they are
+// 0 there), values.bad_groups(i) in which groups of its token i.
 template <bool FINE, int BITS, int D, int G, int MT, typename Keys, typename Values>
 __device__ __forceinline__ void tile_step(const Queries<BITS, D, G, MT>& q, Sums<BITS, D, G, MT>& a, int t, int ok,
                                           bool whole, int j, const Keys& keys, Values& values, const uint8_t* kp,
@@ -511,15 +511,9 @@ __device__ __forceinline__ void tile_step(const Queries<BITS, D, G, MT>& q, Sums
     if (__builtin_expect(values.bad(), 0)) {
 #pragma unroll 1
       for (int e = 0; e < 8; ++e) {
-        uint32_t seen = 0;
+        const uint32_t groups = values.bad_groups(16 * (e >> 2) + 4 * j + (e & 3));
 #pragma unroll
-        for (int m = 0; m < MT; ++m) seen |= sees(m, e) ? ((1u << G) - 1) << (G * m) : 0;
-        const uint16_t* at = (const uint16_t*)(vp + 64 * G * (e >> 2)) + 2 * G * (e & 3);
-#pragma unroll 1
-        for (int g = 0; g < G; ++g)
-          // (not finite, or beyond fp16 at the largest code)
-          if (!(fabsf(fmaf(half_of(at[g], 0), (1 << BITS) - 1, half_of(at[G + g], 0))) < 65520.0f))
-            a.nan |= seen & (((1u << G) + 1) << g);
+        for (int m = 0; m < MT; ++m) a.nan |= sees(m, e) ? groups << (G * m) : 0;
       }
     }
   } else {

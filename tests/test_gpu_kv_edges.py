@@ -62,3 +62,30 @@ def test_scales_of_either_sign(bits, D, group, ty, new, kv, many):
         p.cache["v_params"][:, :, :, 0] = t.from_numpy(rng.choice(choice, shape)).half().cuda()
         p.cache["k_params"][:, :, :, 0] *= t.from_numpy(rng.choice([1.0, -1.0], shape)).half().cuda()
         check(p, many, f"scales {choice}", max_kv=kv)
+
+
+@pytest.mark.parametrize("bits,D", [(4, 64), (4, 128), (8, 128), (4, 256)])
+@CALLS
+def test_hidden_tokens_next_to_great_values(bits, D, new, kv, many):
+    """Tokens that read as up to 57344 or 65024 and whose parameters allow for more than fp16 holds: NaN in a token
+    of their tile that a row does not see, behind the sequence or after the query, changes no bit of it."""
+    t = torch()
+    p = Problem([100, 77], [new, new], bits=bits, D=D, group=32, page=16, seed=D + bits)
+    # 4 bits: codes up to 14, 14 * 8192 - 57344; 8 bits: up to 239, 239 * 512 - 57344
+    p.cache["v"].bitwise_and_(0xee if bits == 4 else 0xef)
+    p.cache["v_params"][:, :, ::3, 0] = 8192.0 if bits == 4 else 512.0
+    p.cache["v_params"][:, :, ::3, 1] = -57344.0
+    clean = [host_bits(x).copy() for x in check(p, many, "great values", max_kv=kv)]
+    assert bool(t.isfinite(p.call(max_kv=kv)[0]).all())
+    for b, n in enumerate(p.lens):                      # places behind the sequences' ends
+        page = int(p.table_h[b, n // 16])
+        p.cache["v_params"][page, :, n % 16:] = float("nan")
+    got = [host_bits(x) for x in p.call(max_kv=kv)]
+    assert all(np.array_equal(a, b) for a, b in zip(got, clean))
+    tok = p.lens[0] - 1                                 # the last query's own token
+    p.cache["v_params"][int(p.table_h[0, tok // 16]), :, tok % 16, :, -1] = float("nan")
+    out, lse = p.call(max_kv=kv)
+    assert bool(t.isnan(out[new - 1, :, -32:]).all()) and bool(t.isfinite(out[new - 1, :, :-32]).all())
+    keep = np.arange(p.T) != new - 1
+    assert np.array_equal(host_bits(out)[keep], clean[0][keep])
+    assert np.array_equal(host_bits(lse)[keep], clean[1][keep]) and bool(t.isfinite(lse).all())
