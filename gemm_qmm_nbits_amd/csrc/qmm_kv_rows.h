@@ -291,19 +291,19 @@ struct QueryPieces {
         finite = fmaf(f[e], 0.0f, finite);  // NaN once an element is not finite
       }
       top = over_lanes<true>(finite == 0.0f ? top : INFINITY, LR);
-      // largest magnitude to [2^7, 2^8): a group's sum stays below 2^15
+      // largest magnitude to [2^7, 2^8): a group's sum stays below 2^15, and fp16 has steps of 2^-31 of it
       const int be = (int)(__float_as_uint(top) >> 23);
       const int ex = min(max(134 - max(be, 1), -96), 100);
       const float up = __uint_as_float((uint32_t)(ex + 127) << 23);
       float sum = 0.0f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float y = f[e] * up;
-        sum += (float)(_Float16)y;
+        const _Float16 y = (_Float16)(f[e] * up);
+        sum += (float)y;
         const int field = 2 * (a & 3) + e / 4, j = e % 4;
-        // (slots of odd and even fields differ only by lane: the factor of odd 4-bit fields is the lane's)
-        const float z = BITS == 4 && (field & 1) ? y * 0.0625f : y;
-        *(_Float16*)(tile + (a >> 2) * 1024 + (j * 16 + x) * 16 + 2 * slot_of_field<BITS>(field)) = (_Float16)z;
+        // (4 bits: odd fields' codes come times 16, even ones' queries, exactly)
+        const _Float16 z = BITS == 4 && !(field & 1) ? y * (_Float16)16 : y;
+        *(_Float16*)(tile + (a >> 2) * 1024 + (j * 16 + x) * 16 + 2 * slot_of_field<BITS>(field)) = z;
       }
       sum = over_lanes<false>(sum, lg);
       uint8_t* sq = tile + (D / 32) * 1024 + x * 16;
@@ -357,7 +357,7 @@ struct Queries {
     for (int w = (G + 1) / 2; w < 4; ++w) s[w] = 0;
     sq[m] = __builtin_bit_cast(f16x8, s);
     f1[m] = ((const float*)(from + (NC + 1) * 1024))[lane & 15];
-    f24[m] = f1[m] * 0x1p24f;
+    f24[m] = f1[m] * (BITS == 4 ? 0x1p20f : 0x1p24f);
   }
 };
 

@@ -592,8 +592,9 @@ qmm_status qmm_validate_lora_grad(const void* dY, const void* X, int type, int64
  *   2^-30) for bf16 results and is held by two fp16 values (2^-22) for fp16 ones; with many rows, groups of
  *   32 and bf16 results e^(S_t) and c * s + o are rounded to fp16 instead.  There a value beyond fp16's
  *   range (the store writes none) counts as NaN where a row sees it.
- *   Queries are scaled by a power of two per row to fp16: exact down to 2^-31 of the row's largest element.
- *   A query with a NaN or an infinity (or elements past 2^100) gives NaN.
+ *   Queries are scaled by a power of two per row to fp16: elements are rounded to multiples of 2^-31 of the
+ *   row's largest one or finer (of 2^-124 in rows below 2^-93).  A query with a NaN or an infinity gives NaN, and
+ *   so may one with elements, or scale times elements, past 2^100.
  *   B <= 65535, T <= 2^24, q_heads <= 4096 a multiple of heads with q_heads / heads <= 512, max_q *
  *   q_heads / heads < 2^31; QMM_E_SHAPE also where max_q, heads and B ask for 2^24 work-groups or more.
  *   workspace: at least qkv_attention_workspace_bytes (max_kv as in the call, table_width * page for 0; no

@@ -89,3 +89,22 @@ def test_hidden_tokens_next_to_great_values(bits, D, new, kv, many):
     keep = np.arange(p.T) != new - 1
     assert np.array_equal(host_bits(out)[keep], clean[0][keep])
     assert np.array_equal(host_bits(lse)[keep], clean[1][keep]) and bool(t.isfinite(lse).all())
+
+
+@pytest.mark.parametrize("bits,D,group", [(4, 64, 32), (4, 128, 64), (4, 256, 128), (8, 64, 32), (8, 128, 64)])
+@pytest.mark.parametrize("ty", ["f16", "bf16"])
+@CALLS
+def test_small_elements_of_queries(bits, D, group, ty, new, kv, many):
+    """Elements that are multiples of 2^-30 of the row's largest enter exactly: the bound has no term for them.  The
+    largest ones meet keys that are zero, a group of scale and offset 0, so that the small ones make the scores."""
+    t = torch()
+    p = Problem([100, 77], [new, new], D=D, bits=bits, group=group, ty=ty, seed=D + bits)
+    p.cache["k_params"][..., 0] = 0.0
+    rng = np.random.default_rng(D)
+    unit = 2.0 ** -24 if ty == "f16" else 2.0 ** -30
+    x = rng.integers(-16, 17, (p.T, p.heads, D)) * unit
+    x[..., :group] = rng.standard_normal((p.T, p.heads, group)) * 0.1 * unit * 2.0 ** 30
+    x[..., 5] = unit * 2.0 ** 30
+    x[..., :group] = x[..., :group].clip(-unit * 2.0 ** 30, unit * 2.0 ** 30)
+    p.Q.copy_(t.from_numpy(x))
+    check(p, many, "small elements", scale=0.02 / unit, max_kv=kv)
