@@ -19,8 +19,7 @@ __device__ __forceinline__ void finish(const KvAttnArgs& p, int64_t row, int d, 
   if (p.sinks) {
     const float sink = p.sinks[row % p.q_heads];
     if (!none) total += __builtin_amdgcn_exp2f(fmaf(sink, 1.44269504f, -ref));
-    const float hi = fmaxf(lse, sink);
-    lse = hi == -INFINITY ? hi : hi + log1pf(expf(fminf(lse, sink) - hi));
+    lse = kv::join_sink(lse, sink);
   }
   if (p.lse && d == 0) p.lse[row] = lse;
   const float inv = none ? 0.0f : 1.0f / total;

@@ -137,6 +137,12 @@ __device__ __forceinline__ float exponent_above(f16x2 m) {
   return (float)((int)max((v >> 10) & 31u, 1u) - 14);
 }
 
+// log(e^lse + e^sink); NaN where one of them is.
+__device__ __forceinline__ float join_sink(float lse, float sink) {
+  const float away = lse == sink ? 0.0f : fabsf(lse - sink);  // (two infinities of one sign are at no distance)
+  return fmaxf(lse, sink) + log1pf(expf(-away));
+}
+
 // A work-group's place in the call: a part of the tokens, a sequence, a cache head and its row tiles (rows
 // are queries times the heads that share the cache head, heads fastest).
 struct Place {
@@ -430,8 +436,7 @@ struct Sums {
     if (p.sinks) {
       const float sink = p.sinks[out_row % p.q_heads];
       total += __builtin_amdgcn_exp2f(fmaf(sink, 1.44269504f, -ref[m]));
-      const float hi = fmaxf(lse, sink);
-      lse = hi == -INFINITY ? hi : hi + log1pf(expf(fminf(lse, sink) - hi));
+      lse = join_sink(lse, sink);
     }
     if (p.lse && j == 0) p.lse[out_row] = lse;
     const float inv = l[m] == 0.0f ? 0.0f : 1.0f / total;

@@ -108,3 +108,57 @@ def test_small_elements_of_queries(bits, D, group, ty, new, kv, many):
     x[..., :group] = x[..., :group].clip(-unit * 2.0 ** 30, unit * 2.0 ** 30)
     p.Q.copy_(t.from_numpy(x))
     check(p, many, "small elements", scale=0.02 / unit, max_kv=kv)
+
+
+@pytest.mark.parametrize("ty", ["f16", "bf16"])
+@CALLS
+@pytest.mark.parametrize("parts", [False, True])
+def test_rows_that_are_nan_with_sinks(ty, new, kv, many, parts):
+    """A query, a key or a sink that is not a number: result and lse of the rows that meet it are NaN, with sinks as
+    without; the other rows keep their bits."""
+    t = torch()
+    p = Problem([60, 45], [min(new, 60), min(new, 45)], ty=ty, seed=new)
+    if parts:
+        kv = MUCH if many else 100000
+    n0 = p.news[0]
+    sinks = t.linspace(-3, 3, p.heads, device="cuda")
+    sinks[6] = -float("inf")
+    args = dict(sinks=sinks, max_kv=kv)
+    clean = [host_bits(x).copy() for x in check(p, many, "sinks", **args)]
+
+    def rest(out, lse, bad):
+        assert bool(t.isnan(out[bad]).all()) and bool(t.isnan(lse[bad]).all())
+        keep = ~bad.cpu().numpy()
+        assert np.array_equal(host_bits(out)[keep], clean[0][keep])
+        assert np.array_equal(host_bits(lse)[keep], clean[1][keep])
+
+    bad = t.zeros(p.T, p.heads, dtype=t.bool, device="cuda")
+    q = p.Q.clone()
+    for r, a, x in ((0, 1, float("nan")), (0, 6, float("nan")), (n0, 3, float("inf"))):
+        p.Q[r, a, 7] = x
+        bad[r, a] = True
+    rest(*p.call(**args), bad)
+    p.Q.copy_(q)
+    sinks[2] = float("nan")                 # (every row sees a token: see Problem's lens and news)
+    bad = t.zeros_like(bad)
+    bad[:, 2] = True
+    rest(*p.call(**args), bad)
+    sinks[2] = 0.0
+    clean = [host_bits(x).copy() for x in p.call(**args)]
+    p.cache["k_params"][int(p.table_h[1, 0]), 1, 0, 1] = float("nan")  # sequence 1, token 0, heads 4 to 7
+    bad = t.zeros_like(bad)
+    bad[n0:, 4:] = True
+    rest(*p.call(**args), bad)
+
+
+def test_sinks_and_rows_that_see_nothing():
+    """out = 0 and lse = the sink, whatever it is."""
+    t = torch()
+    p = Problem([0, 2], [1, 2], seed=3)
+    sinks = t.tensor([0.0, -float("inf"), float("inf"), float("nan"), -5.0, 200.0, 1e-30, -300.0], device="cuda")
+    for kv in (None, 100000):
+        out, lse = p.call(sinks=sinks, max_kv=kv)
+        assert not bool(out[0].any())
+        assert bool(((lse[0] == sinks) | (t.isnan(lse[0]) & t.isnan(sinks))).all())
+        assert not bool(out[1:, 2].any()) and bool((lse[:, 2] == float("inf")).all())
+        assert bool(t.isnan(out[1:, 3]).all()) and bool(t.isnan(lse[:, 3]).all())
