@@ -1,6 +1,7 @@
 // Entry points of the low-bit key/value cache: argument checks and launches.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 
 #include "qmm.h"
@@ -219,7 +220,7 @@ qmm_status qkv_attention(const void* Q, int64_t row_stride, int64_t head_stride,
   p.max_q = max_q;
   p.scale = scale * 1.44269504088896341f;
   p.causal = causal;
-  p.window = window;
+  p.window = std::min<int64_t>(window, 1LL << 31);  // positions are below that; differences stay in range
   p.sinks = sinks;
   p.c = *cache;
   p.page_log2 = log2_of(cache->page);

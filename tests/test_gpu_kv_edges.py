@@ -162,3 +162,16 @@ def test_sinks_and_rows_that_see_nothing():
         assert bool(((lse[0] == sinks) | (t.isnan(lse[0]) & t.isnan(sinks))).all())
         assert not bool(out[1:, 2].any()) and bool((lse[:, 2] == float("inf")).all())
         assert bool(t.isnan(out[1:, 3]).all()) and bool(t.isnan(lse[:, 3]).all())
+
+
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31, 2 ** 62, 2 ** 63 - 1])
+@pytest.mark.parametrize("news", [[49, 2, 5], [140, 70, 3]])
+@pytest.mark.parametrize("kv", [None, MUCH])
+def test_widest_windows(window, news, kv):
+    """A window that covers every sequence is none, up to the largest integer, also where queries stand before
+    their sequence's first token."""
+    p = Problem([40, 50, 0], news, seed=4)
+    many = kv == MUCH and max(news) * 4 > 64
+    want = [host_bits(x).copy() for x in check(p, many, "no window", max_kv=kv)]
+    got = [host_bits(x) for x in check(p, many, "window", window=window, max_kv=kv)]
+    assert all(np.array_equal(a, b) for a, b in zip(got, want))
