@@ -67,3 +67,26 @@ def test_forms_agree():
     last = int(a.cu_h[2]) - 1
     assert np.array_equal(host_bits(out[last, :2 * n]), host_bits(o[last]))
     assert np.array_equal(host_bits(lse[last, :2 * n]), host_bits(e[last]))
+
+
+@pytest.mark.parametrize("bits,D,group", FORMATS)
+@pytest.mark.parametrize("ty", ["f16", "bf16"])
+@pytest.mark.parametrize("new", [1, 7])
+def test_few_rows_whole_and_in_parts(bits, D, group, ty, new):
+    """Up to 16 rows of a cache head and more, in one part (no workspace) and in several: bf16 results to one
+    rounding of a weight, 2^-11, whatever the groups."""
+    p = Problem([90, 400, 7], [new] * 3, D=D, bits=bits, group=group, ty=ty, seed=D + group + new)
+    assert part_rows(p, 256) == 0
+    check(p, False, "in one part", max_kv=256)
+    assert part_rows(p, MUCH) > 0
+    check(p, False, "in parts", max_kv=MUCH)
+
+
+@pytest.mark.parametrize("bits,D,group", FORMATS)
+@pytest.mark.parametrize("std", [0.1, 1.0, 4.0])
+def test_many_rows_to_one_rounding(bits, D, group, std):
+    """bf16 results of many rows, flat softmax to peaked: one rounding of a weight where groups are of 64 or 128, two
+    with groups of 32 (and one again where few rows are asked for)."""
+    p = Problem([200, 61], [90, 40], heads=4, kv=1, D=D, bits=bits, group=group, seed=D + bits, q_std=std)
+    check(p, True, "many", max_kv=MUCH)
+    check(p, False, "few", max_kv=256)
