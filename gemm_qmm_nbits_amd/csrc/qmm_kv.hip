@@ -1,13 +1,16 @@
 // Low-bit key/value cache: quantizing tokens into their slots, and reading slots back.
 //
 // Both move each byte once and are bound by memory: 65536 tokens of 10 heads of 128 dimensions, 4 bits to bf16,
-// read back in 102 us (4.2 TB/s of codes in and values out); 8191 tokens of 4 heads stored in 19 us, of which
-// the search for slots that repeat and the loads' latency take most.  Small calls are their launch: 4 us.
+// read back in 102 us (4.2 TB/s of codes in and values out); 8191 tokens of 4 heads stored in 18 us, of which
+// the search for slots that repeat and the loads' latency take most.  Small calls are their launch: 3.5 us to read
+// back, 5 to store.
+// The search reads all later slots in every work-group, so long stores grow with the square: 4 heads of 128 dimensions,
+// 8 bits: 32768 tokens 88 us, 131072 932, 2^20 44 ms (their bytes need 20, 80 and 640 us).
 //
-// A row (one token, one head) is spread over D / 8 lanes of 8 dimensions each, so a group's range is a reduction over 4, 8 or 16 lanes; the order of the
-// codes in the cache (every 4th dimension for keys, every 16th for values) is reached by exchanging index
-// bits between the field number inside a lane's word and the lane number, a few lane exchanges of packed
-// words instead of one byte store per element.
+// A row (one token, one head) is spread over D / 8 lanes of 8 dimensions each, so a group's range is a reduction
+// over 4, 8 or 16 lanes; the order of the codes in the cache (every 4th dimension for keys, every 16th for values)
+// is reached by exchanging index bits between the field number inside a lane's word and the lane number, a few lane
+// exchanges of packed words instead of one byte store per element.
 #include <algorithm>
 
 #include "qmm_device.h"

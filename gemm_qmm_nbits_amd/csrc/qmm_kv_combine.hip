@@ -137,7 +137,10 @@ KvPlan kv_plan(int q_heads, int heads, int D, int64_t B, int64_t max_q, int64_t 
   // sooner: 4 waves share a row tile's tokens, and there are four times as many work-groups.  The first where
   // there is work enough (32 heads on 8, 128 dimensions, one sequence: 512 of 512 tokens 33 against 21 us, 1024 of
   // 1024 37 and 45, 512 of 8192 139 and 182).
-  // (a sequence with fewer queries than max_q leaves work-groups without rows; they end at once.)
+  // (a sequence with fewer queries than max_q leaves work-groups without rows; they end at once, but are counted.
+  // Windows are not: a work-group of many rows reads the tokens of its window once for 128 rows, one of few for 32.
+  // 64 heads of 64 on 8, windows of 128 and 1024: 2048 queries at 8192 tokens 36 against 93 and 112 against 165 us, 512
+  // at 4096 of eight sequences 48 against 150 and 157 against 269.)
   k.by_rows = rows > 64 && rows * heads * B >= (1ll << 26) / std::max<int64_t>(max_kv, 1);
   k.mt = rows <= 16 ? 1 : 2;
   const int64_t per = rows_of(k);
@@ -163,7 +166,8 @@ KvPlan kv_plan(int q_heads, int heads, int D, int64_t B, int64_t max_q, int64_t 
       const int64_t most = over(max_kv, 512);
       splits = std::max<int64_t>(std::min(room / left, most), 1);
       // (where that is less than 8: parts that fill more of several rounds.  320 work-groups, 1024 of 16384 tokens: 811
-      // us, in eight parts each 582 with the join.)
+      // us, in eight parts each 582 with the join.  What parts write and the join reads is not weighed: five prompts,
+      // 64 dimensions, 424 of 1960 work-groups in five parts each, 72 MB, a join of 14 us in 271.)
       for (int64_t s = splits + 1; s <= std::min<int64_t>(8, most); ++s)
         if (20 * over(left * s, room) * splits < 19 * over(left * splits, room) * s) splits = s;
     }

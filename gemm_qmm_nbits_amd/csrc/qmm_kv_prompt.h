@@ -17,8 +17,11 @@
 // 2^-11; the scale and the offset are multiples of 2^-24, so small values are exact), and the weights p alone
 // are rounded to fp16: the second product then needs neither scales nor offsets per row.  2048 queries at 8192
 // tokens, 4 bits: 40 heads of 128 dimensions on 10 682 -> 551 us, 64 of 64 on 8 664 -> 586, 16 of 256 on 8
-// 1003 -> 837; with groups of 64 or 128 between 8 % more and 6 % less.  For fp16 results it would cost a bit:
-// codes.
+// 1003 -> 837; with groups of 64 or 128 between 8 % more and 6 % less.  fp16 results have the bits that these
+// roundings would take, and keep the codes.
+//
+// Registers: fp16 results spill 29 to 37 of them with groups of 32 at 128 and 256 dimensions, 24 and 4 with groups of
+// 32 and 64 at 64 dimensions; no other form spills.
 #pragma once
 
 #include "qmm_kv_rows.h"
@@ -191,7 +194,8 @@ struct FragValues {
   __device__ __forceinline__ f16x8 operand(int n) const { return *(const f16x8*)(frags + n * 1024); }
 };
 
-// (Waves per SIMD: three at 64 dimensions, 312 us for five prompts of up to 3001 tokens, against 347 with two.)
+// (Waves per SIMD: three at 64 dimensions, 312 us for five prompts of up to 3001 tokens, against 347 with two, when no
+// work-group was split; 257 and 14 for the join now.)
 template <int BITS, int D, int G, bool FINE>
 __global__ __launch_bounds__(kThreads, D == 256 ? 1 : D == 64 ? 3 : 2) void kv_prompt_kernel(KvAttnArgs p) {
   constexpr int NC = D / 32, NV = D / 16, MT = kPromptTiles, kRows = 16 * MT;

@@ -9,6 +9,9 @@
 // are bound by the chain of table, tile, join: one sequence of 1500 tokens 6.7 us and 3.9 for the parts' join.
 // (Three buffers instead of two leave room for fewer work-groups: 8 bits 190 us instead of 161.  Four row tiles
 // of 16 instead of two spill: 80 us instead of 44; so do four waves per SIMD at 128 dimensions: 502.)
+// Two row tiles spill as well, 18 to 55 registers at 128 dimensions (19 where 16 sequences have 4 queries of 8 heads,
+// 24 us) and 6 to 63 at 256; one spills 11 to 13 at 128 dimensions, 4 bits, groups of 32, and up to 6 at 64 with groups
+// of 32 and fp16 results.
 #pragma once
 
 #include "qmm_kv_rows.h"

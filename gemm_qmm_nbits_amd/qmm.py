@@ -958,9 +958,9 @@ def qkv_attention(Q, cache, table, kv_len, cu_q=None, max_q=None, max_kv=None, s
     Q [T, q_heads, D] fp16 or bf16 (any row and head strides); table int32 [B, width]: the pages of each sequence;
     kv_len int32 [B]: its tokens, those of the queries included.  cu_q int32 [B + 1]: the queries of sequence b are the
     rows cu_q[b] .. cu_q[b + 1] - 1, its last tokens (None: one query per sequence, T = B).  max_q: the most queries of
-    a sequence (default T), max_kv: the most tokens expected (default: the table's); host numbers, no device value is
-    read.  scale defaults to D ** -0.5; window > 0: the last `window` tokens up to the query's own; sinks fp32
-    [q_heads]: logits that take part in the sum only.  Rows of no sequence are not written."""
+    a sequence (default T; the grid follows it), max_kv: the most tokens expected (default: the table's); host numbers,
+    no device value is read.  scale defaults to D ** -0.5; window > 0: the last `window` tokens up to the query's own;
+    sinks fp32 [q_heads]: logits that take part in the sum only.  Rows of no sequence are not written."""
     ty, dev, heads, page, D, c = _kv_cache(cache)
     if Q.dim() != 3:
         raise ValueError("Q must be [T, q_heads, D]")

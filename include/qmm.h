@@ -545,8 +545,9 @@ qmm_status qmm_validate_lora_grad(const void* dY, const void* X, int type, int64
  * The cache is a pool of pages; a slot is page_id * page + place.  A key (or value) of one token
  * and head is a row of D codes, unsigned `bits`-wide fields, least significant first; `group`
  * consecutive dimensions share a fp16 scale s and offset o, and code c stands for c * s + o (not
- * rounded).  Dimension d is the field at position (d % W) * (D / W) + d / W of its row, W = 4 for
- * keys and 16 for values: the order in which the lanes of a matrix instruction take them.
+ * rounded; s of either sign, though the store writes none below 0).  Dimension d is the field at
+ * position (d % W) * (D / W) + d / W of its row, W = 4 for keys and 16 for values: the order in which
+ * the lanes of a matrix instruction take them.
  *   k, v                uint8 [pages][heads][page][D * bits / 8], 16-byte aligned
  *   k_params, v_params  fp16 [pages][heads][page][2][D / group] (scales, then offsets), 16-byte aligned
  *   bits in {4, 8}, D in {64, 128, 256}, group in {32, 64, 128} and <= D, page a power of two in
@@ -562,7 +563,8 @@ qmm_status qmm_validate_lora_grad(const void* dY, const void* X, int type, int64
  *           t * row_stride + h * head_stride + d (strides in elements, >= 0).  Rows that are 16-byte
  *           aligned are the fastest.
  *   slots   int32 [T] (device), T <= 2^20.  A slot outside the pool: the token is not stored.  Of several
- *           tokens with one slot the last is stored.
+ *           tokens with one slot the last is stored; the search for them grows with T^2 and is what a call of
+ *           more than 32768 tokens takes (several calls in order store the same, sooner).
  *
  * qkv_cache_load -- the values of T slots: K, V dense [T][heads][D] of `type`, fp32(c * s + o) rounded
  *   to it; zeros for a slot outside the pool.  K or V may be NULL (not read).  T <= 2^24.  In both calls
@@ -588,8 +590,9 @@ qmm_status qmm_validate_lora_grad(const void* dY, const void* X, int type, int64
  *           split depends on it, and the order of the sums; longer sequences are right all the same.
  *   sinks   fp32 [q_heads] (device) or NULL (none).  window 0: none.
  *   Codes enter the products as they are and scales are applied in fp32: S and lse carry fp32 sums'
- *   errors.  For the second product e^(S_t) s is rounded to fp16 (relative 2^-11, of its largest down to
- *   2^-30) for bf16 results and is held by two fp16 values (2^-22) for fp16 ones; with many rows, groups of
+ *   errors.  For the second product e^(S_t) s is rounded to fp16 (relative 2^-11; below 2^-20 of the largest
+ *   e^(S_t) times the largest |s|, 2^-30 of that) for bf16 results and is held by two fp16 values (2^-22) for
+ *   fp16 ones: so much of sum e^(S_t) |s| c, as codes are not centred; with many rows, groups of
  *   32 and bf16 results e^(S_t) and c * s + o are rounded to fp16 instead.  There a value beyond fp16's
  *   range (the store writes none) counts as NaN where a row sees it.
  *   Queries are scaled by a power of two per row to fp16: elements are rounded to multiples of 2^-31 of the
